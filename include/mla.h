@@ -72,7 +72,10 @@ typedef enum {
     MLA_ERR_BAD_BLOCK_TABLE = 4,     /* device saw a block id outside [0, num_blocks) */
     MLA_ERR_BAD_SEQ_LEN = 5,         /* device saw a length < s_q or > max_blocks*page */
     MLA_ERR_DEVICE_TIMEOUT = 6,      /* a bounded device-side wait gave up */
-    MLA_ERR_CUDA = 7                 /* a CUDA runtime call failed */
+    MLA_ERR_CUDA = 7,                /* a CUDA runtime call failed */
+    MLA_ERR_BAD_TREE = 8,            /* device saw drafted nodes, parents or kept nodes that are no tree's */
+    MLA_ERR_OUT_OF_PAGES = 9,        /* device found fewer free pages than a call to grow wants */
+    MLA_ERR_BAD_SEQ_INDEX = 10       /* device saw a sequence index outside the table, or one twice */
 } mla_status_t;
 
 typedef enum {
@@ -346,9 +349,193 @@ mla_status_t mla_lse_merge_prepare(int rows, int n_h, int d_c, const float *o_la
 mla_status_t mla_lse_merge_finish(int rows, int n_h, int d_c, const float *acc, const float *lse_max,
                                   float *o_lat, float *lse, mla_stream_t stream);
 
+/* ----------------------------------------------------------------------------------------
+ * Drafted trees (speculative decoding).
+ *
+ * A drafter proposes for every sequence a tree of tokens that would follow its committed ones,
+ * the target model scores all of them in one step, and the longest path that it agrees with is
+ * kept.  MLA article, section 분리 RoPE: a token's cache row is [c^KV ; RoPE(k^R)] and its score
+ * set is its own past.  For a drafted node that past is every committed token and, of the
+ * drafted ones, its ancestors and itself.
+ *
+ * A batch's trees are packed like prompts: sequence b's nodes are rows cu_nodes[b] ..
+ * cu_nodes[b+1] - 1 of every per-node array, parents before children, n_b = their number (0: none).
+ * cu_nodes is a device array [B+1], cu_nodes[0] = 0, non-decreasing.  cu_nodes[B] may be less than
+ * total_nodes: the rows behind it belong to no sequence (a captured step's padding) and every call
+ * leaves their outputs as they were, except that mla_tree_prepare marks them (below).
+ * seq_lens[b] counts the committed tokens and the drafted nodes, as mla_decode's counts the current
+ * tokens.  With ctx_b = seq_lens[b] - n_b, node k of sequence b
+ *     sits in cache slot   ctx_b + k                 (nodes of equal depth need slots of their own)
+ *     has RoPE position    ctx_b + depth(k)          (0 for a child of the last committed token)
+ *     sees token j         if j < ctx_b, or if bit (j - ctx_b) of its mask row is set.
+ * One step: mla_tree_prepare once; per layer mla_tree_append, mla_absorb_q (pos from
+ * mla_tree_prepare), mla_decode_tree, mla_out_proj; after verification mla_cache_keep.
+ * A sequence with more nodes than the arguments allow, or whose rows are not rows of the batch, sets
+ * MLA_ERR_BAD_TREE on the device and is skipped.  At most MLA_MAX_TREE_NODES nodes a sequence.
+ * ---------------------------------------------------------------------------------------- */
+#define MLA_MAX_TREE_NODES 1024
+
+/* mla_tree_prepare -- masks, slots and positions of a batch's trees from their parents.
+ *   cu_nodes   [B+1] int32;  parent [total_nodes] int32: the parent's number within the sequence
+ *              (less than the node's own), -1 for a child of the last committed token
+ *   seq_lens   [B] int32, committed tokens and nodes
+ *   mask_words 32-bit words of a mask row, >= max_b ceil(n_b / 32), <= MLA_MAX_TREE_NODES / 32
+ *   mask       [total_nodes, mask_words], written: bit k % 32 of word k / 32 is set for every ancestor
+ *              k of the node and for the node itself
+ *   pos, slot, seq_idx [total_nodes] int32, written: RoPE position, cache slot, sequence.  Rows behind
+ *              cu_nodes[B], and those of a sequence with seq_lens[b] < n_b (MLA_ERR_BAD_SEQ_LEN), get
+ *              seq_idx -1, which mla_tree_append skips; the former get mask, pos and slot 0.
+ * A parent outside [-1, k) sets MLA_ERR_BAD_TREE; the node is taken as a child of the last committed
+ * token.  B = 0 with total_nodes = 0 is a no-op. */
+mla_status_t mla_tree_prepare(int B, const int32_t *cu_nodes, int total_nodes, const int32_t *parent,
+                              const int32_t *seq_lens, int mask_words, uint32_t *mask, int32_t *pos,
+                              int32_t *slot, int32_t *seq_idx, mla_stream_t stream);
+
+/* mla_tree_append -- mla_cache_append for drafted nodes: token t's row is rotated at pos[t] and written
+ * to slot[t] of sequence seq_idx[t].  A token with seq_idx -1 is skipped.  Other arguments, cache
+ * formats and errors as for mla_cache_append (slot in the place of pos where the table is indexed).
+ * A slot is written by one token of a call. */
+mla_status_t mla_tree_append(const mla_dims_t *dims, int T, const void *c_kv, const void *k_r,
+                             const int32_t *seq_idx, const int32_t *slot, const int32_t *pos,
+                             const int32_t *block_table, int num_seqs, int max_blocks_per_seq,
+                             int num_blocks, void *kv_pool, void *kr_pool, float *kv_scale,
+                             mla_stream_t stream);
+
+/* mla_decode_tree -- absorbed attention of every drafted node over the cache: for node row t of
+ * sequence b and head h, over the tokens j that it sees,
+ *     s_j = (q_abs[t,h,0:d_c] . c_j + q_abs[t,h,d_c:] . kR_j) / sqrt(d_h + d_r),
+ *     o_lat = sum_j softmax(s)_j c_j,       lse = ln sum_j exp(s_j).
+ * A node that sees no token (no committed one and an empty mask row) gets o_lat = 0, lse = -inf.
+ * The mask is taken as it is: any set of drafted tokens, not only ancestors.
+ * What a masked token's row holds does not matter, infinities and NaN included.
+ *   cu_nodes    [B+1], total_nodes, max_nodes: a host-side upper bound of the n_b
+ *   q_abs       [total_nodes, n_h, d_c+d_r] act dtype (from mla_absorb_q)
+ *   cache, block_table, seq_lens, max_seq_len: as for mla_decode; seq_lens[b] in [n_b, max_seq_len]
+ *               (otherwise MLA_ERR_BAD_SEQ_LEN on the device, the sequence's rows 0 and -inf)
+ *   mask        [total_nodes, mask_words], mask_words >= ceil(max_nodes / 32)
+ *   workspace   device scratch of workspace_bytes >= mla_decode_tree_workspace_size(dims, B,
+ *               total_nodes, max_seq_len), 256-byte aligned; its content on entry does not matter
+ *   o_lat       [total_nodes, n_h, d_c] of out_dtype (F32 or BF16), written
+ *   lse         [total_nodes, n_h] fp32, written (may be NULL)
+ * The tensor-core kernel runs for d_c = 512, d_r = 64, 64-token pages, bf16 activations, a bf16 or FP8
+ * cache, any number of heads and no MLA_FLAG_SIMT_DECODE (q_abs, pools and o_lat 16-byte aligned, or
+ * MLA_ERR_INVALID_ARG); other shapes run on the CUDA cores.
+ * Precision: operands as they are (FP8: the codes exactly, the scales in fp32), fp32 accumulation and
+ * softmax; on the tensor cores P is rounded to bf16 for the value product, as in mla_decode.
+ * Deterministic: the result depends only on the logical cache content. */
+size_t mla_decode_tree_workspace_size(const mla_dims_t *dims, int B, int total_nodes, int max_seq_len);
+mla_status_t mla_decode_tree(const mla_dims_t *dims, int B, const int32_t *cu_nodes, int total_nodes,
+                             int max_nodes, const void *q_abs, const void *kv_pool, const void *kr_pool,
+                             const float *kv_scale, const int32_t *block_table, int max_blocks_per_seq,
+                             int num_blocks, const int32_t *seq_lens, int max_seq_len,
+                             const uint32_t *mask, int mask_words, void *workspace,
+                             size_t workspace_bytes, void *o_lat, mla_dtype_t out_dtype, float *lse,
+                             mla_stream_t stream);
+
+/* One layer's cache buffers, as mla_cache_append takes them. */
+typedef struct {
+    void *kv_pool;
+    void *kr_pool;   /* FP8 cache only, otherwise NULL */
+    float *kv_scale; /* FP8 cache only, otherwise NULL */
+} mla_pool_t;
+
+/* mla_cache_keep -- after verification: the accepted path's rows move up behind the committed ones, in
+ * every layer.  The row of node keep[b, i] of sequence b goes to slot ctx_b + i, i < num_keep[b]; rows
+ * are moved as they are (a path's i-th node was rotated at ctx_b + i already).
+ *   pools       [num_pools] host array, the layers' caches behind one block table
+ *   keep        [B, max_keep] int32 on the device, each row's first num_keep[b] strictly ascending
+ *   num_keep    [B] int32, in [0, min(max_keep, n_b)]
+ *   new_lens    [B] int32, written: ctx_b + num_keep[b] (may be NULL; not seq_lens itself, which the
+ *               layers' blocks read while it is written)
+ * A sequence whose kept nodes are not as stated (MLA_ERR_BAD_TREE), or whose length or pages are bad,
+ * is left as it is, its new length seq_lens[b].  Pages of the drafted rows are the sequence's own
+ * (mla_pages_grow sees to that): a page that two sequences of the call share is not written in order. */
+mla_status_t mla_cache_keep(const mla_dims_t *dims, int num_pools, const mla_pool_t *pools, int B,
+                            const int32_t *cu_nodes, int total_nodes, const int32_t *block_table,
+                            int max_blocks_per_seq, int num_blocks, const int32_t *seq_lens,
+                            const int32_t *keep, const int32_t *num_keep, int max_keep,
+                            int32_t *new_lens, mla_stream_t stream);
+
+/* ----------------------------------------------------------------------------------------
+ * Pages of the cache.
+ *
+ * A page (cache block) may be held by several sequences: samples of one prompt, beams, a common
+ * prefix.  These calls keep, on the device and in stream order (no host round trip, so a captured step
+ * can hold them),
+ *     block_table [num_seqs, max_blocks]  int32, -1: no page
+ *     refs        [num_blocks] int32      how many table entries hold the page; 0: free
+ *     seq_lens    [num_seqs] int32        tokens
+ * for all layers at once: the layers' pools share the table.  Every result is determined by the
+ * arguments: free pages are taken lowest id first, in the order of the call's entries.
+ * A sequence's rows are written only behind its length, and mla_pages_grow makes the page they start
+ * in the sequence's own; so full pages are shared for good, and a part-filled one until a holder grows.
+ * Lists (parent, child, seqs, new_lens) are device arrays [n].  A list entry that is out of range, or
+ * a sequence named twice where one is asked for, sets MLA_ERR_BAD_SEQ_INDEX (MLA_ERR_BAD_SEQ_LEN for a
+ * length that is negative or does not fit the table); what the call then does is said with each.
+ *   workspace  device scratch of workspace_bytes >= mla_pages_workspace_size(table, n) (n: the longest
+ *              list it serves, 0 for mla_pages_compact alone), 256-byte aligned, content on entry of no
+ *              matter.  Calls that may run at the same time take a workspace each.
+ * ---------------------------------------------------------------------------------------- */
+typedef struct {
+    int page_size;
+    int num_seqs;    /* rows of block_table */
+    int max_blocks;  /* entries of a row */
+    int num_blocks;  /* pages of the pool */
+    int32_t *block_table;
+    int32_t *refs;
+    int32_t *seq_lens;
+} mla_page_table_t;
+
+size_t mla_pages_workspace_size(const mla_page_table_t *table, int n);
+
+/* mla_pages_fork -- sequence child[i] becomes a copy of parent[i] as it was before the call: its table
+ * row, whose pages gain a holder, and its length.  What child[i] held before is given back.  A sequence
+ * may be parent of many and child of one, of itself too (a beam search's reordering).  A bad entry is
+ * skipped; where one child is named twice, both entries are. */
+mla_status_t mla_pages_fork(const mla_page_table_t *table, int n, const int32_t *parent,
+                            const int32_t *child, void *workspace, size_t workspace_bytes,
+                            mla_stream_t stream);
+
+/* mla_pages_grow -- sequence seqs[i] (NULL: sequence i) grows to new_lens[i] tokens: pages for them are
+ * taken, and its last page, where that is part-filled and held by others too, is replaced by a page of
+ * its own, whose content moves[k] = (from, to) asks mla_cache_copy_pages for.  Of the sequences of one
+ * call that share such a page the last keeps it if nobody else holds it.  An entry with new_lens[i] <=
+ * its length is left as it is.  Entries beyond the length that already hold a page keep it.
+ *   moves      [n, 2] int32, num_moves [1] int32 on the device, written
+ * All or nothing: a bad entry, or too few free pages (MLA_ERR_OUT_OF_PAGES), leaves the table as it
+ * was, with num_moves 0. */
+mla_status_t mla_pages_grow(const mla_page_table_t *table, int n, const int32_t *seqs,
+                            const int32_t *new_lens, int32_t *moves, int32_t *num_moves,
+                            void *workspace, size_t workspace_bytes, mla_stream_t stream);
+
+/* mla_pages_trim -- sequence seqs[i] (NULL: sequence i) is cut to new_lens[i] tokens (0: it ends): its
+ * pages behind them lose a holder, pages reserved beyond its length among them; a longer new_lens[i]
+ * leaves the length.  A sequence may be named more than once: the shortest counts.  Bad entries are
+ * skipped. */
+mla_status_t mla_pages_trim(const mla_page_table_t *table, int n, const int32_t *seqs,
+                            const int32_t *new_lens, mla_stream_t stream);
+
+/* mla_pages_compact -- the pages in use take the lowest ids: with u pages in use, the k-th one behind
+ * the first u ids moves to the k-th free id among them, table and counts follow, and moves[k] = (from,
+ * to) asks mla_cache_copy_pages for its content.  Pages u .. num_blocks - 1 are free afterwards.
+ *   moves      [num_blocks / 2, 2] int32, num_moves [1] int32 on the device, written
+ * A table entry that names a page nobody holds is left and sets MLA_ERR_BAD_BLOCK_TABLE. */
+mla_status_t mla_pages_compact(const mla_page_table_t *table, int32_t *moves, int32_t *num_moves,
+                               void *workspace, size_t workspace_bytes, mla_stream_t stream);
+
+/* mla_cache_copy_pages -- page moves[k].from is copied to page moves[k].to in every layer.
+ *   moves      [max_moves, 2] int32 on the device; num_moves [1] int32 on the device, how many of them
+ *              (NULL: max_moves); more than max_moves are not read
+ * No page is the target of two moves, nor target of one and source of another.  A move that names a page
+ * outside the pool is skipped and sets MLA_ERR_BAD_BLOCK_TABLE. */
+mla_status_t mla_cache_copy_pages(const mla_dims_t *dims, int num_pools, const mla_pool_t *pools,
+                                  int num_blocks, const int32_t *moves, const int32_t *num_moves,
+                                  int max_moves, mla_stream_t stream);
+
 /* Reads and clears the device error word of the current device.  Synchronises the device.
- * Returns MLA_OK, MLA_ERR_BAD_BLOCK_TABLE, MLA_ERR_BAD_SEQ_LEN or MLA_ERR_DEVICE_TIMEOUT
- * (the first condition seen since the last call), or MLA_ERR_CUDA. */
+ * Returns MLA_OK, MLA_ERR_BAD_BLOCK_TABLE, MLA_ERR_BAD_SEQ_LEN, MLA_ERR_DEVICE_TIMEOUT,
+ * MLA_ERR_BAD_TREE, MLA_ERR_OUT_OF_PAGES or MLA_ERR_BAD_SEQ_INDEX (the first condition seen since
+ * the last call), or MLA_ERR_CUDA. */
 mla_status_t mla_get_last_device_error(void);
 
 /* Static, human-readable name of a status code. */

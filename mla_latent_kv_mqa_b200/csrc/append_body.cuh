@@ -16,6 +16,7 @@ struct AppendArgs {
     int T, d_c, d_r, page;
     const void *c_kv, *k_r;
     const int32_t *seq_idx, *pos, *bt;
+    const int32_t *slot;  // mla_tree_append: where token t goes in its sequence (its RoPE position is pos[t])
     int num_seqs, max_blocks, num_blocks;
     void *kv_pool;
     __nv_bfloat16 *kr_pool;
@@ -27,14 +28,14 @@ AppendArgs append_args(const mla_dims_t &d, int T, const void *c_kv, const void 
                        void *kv_pool, void *kr_pool, float *kv_scale);
 
 // One warp writes token t's cache row.  KV: 0 = f32 cache, 1 = bf16 cache, 2 = fp8 content
-// cache.  Bad sequence indices, positions or block ids are recorded, never dereferenced.
+// cache.  SLOT: the row goes to a.slot[t] instead of a.pos[t].  Bad sequence indices, positions or block ids are recorded, never dereferenced.
 // The token's inputs depend only on t, so all of a lane's loads (up to AP_BATCH content values
 // and its RoPE pair) are issued before the sequence / position / block-table lookups and travel
 // together with them; loads interleaved with the row's stores would each wait for the previous
 // store (the compiler cannot prove the input and the pool apart), one trip to memory apiece.
 constexpr int AP_BATCH = 16;  // content values per lane in the first batch: d_c <= 512
 
-template <typename Tin, int KV>
+template <typename Tin, int KV, bool SLOT = false>
 __device__ __forceinline__ void append_token(const AppendArgs &a, const RopeFreqs &rope, int t, int lane,
                                              unsigned *err) {
     const int d_c = a.d_c, d_r = a.d_r, page = a.page;
@@ -59,16 +60,18 @@ __device__ __forceinline__ void append_token(const AppendArgs &a, const RopeFreq
     const float x1 = lane < half ? to_f32(k_in[lane + half]) : 0.f;
     const int s = seq_idx[t];
     const int p = pos[t];
-    if (s < 0 || s >= num_seqs || p < 0 || p / page >= max_blocks) {
+    const int j = SLOT ? a.slot[t] : p;
+    if (SLOT && s == -1) return;  // a node that belongs to no sequence (the batch's padding)
+    if (s < 0 || s >= num_seqs || p < 0 || j < 0 || j / page >= max_blocks) {
         if (lane == 0) record_error(err, kErrBadBlock);
         return;
     }
-    const int blk = bt[(size_t)s * max_blocks + p / page];
+    const int blk = bt[(size_t)s * max_blocks + j / page];
     if (blk < 0 || blk >= num_blocks) {
         if (lane == 0) record_error(err, kErrBadBlock);
         return;
     }
-    const size_t slot = (size_t)blk * page + (p % page);
+    const size_t slot = (size_t)blk * page + (j % page);
 
     // RoPE of the shared key (pairs k, k + d_r/2).
     auto put_rope = [&](int k, float a0, float a1) {

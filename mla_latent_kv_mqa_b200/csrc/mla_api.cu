@@ -7,6 +7,7 @@
 
 #include "append_body.cuh"
 #include "mla_internal.cuh"
+#include "tree.cuh"
 
 namespace mla {
 
@@ -96,6 +97,9 @@ const char *mla_status_string(mla_status_t s) {
         case MLA_ERR_BAD_SEQ_LEN: return "MLA_ERR_BAD_SEQ_LEN";
         case MLA_ERR_DEVICE_TIMEOUT: return "MLA_ERR_DEVICE_TIMEOUT";
         case MLA_ERR_CUDA: return "MLA_ERR_CUDA";
+        case MLA_ERR_BAD_TREE: return "MLA_ERR_BAD_TREE";
+        case MLA_ERR_OUT_OF_PAGES: return "MLA_ERR_OUT_OF_PAGES";
+        case MLA_ERR_BAD_SEQ_INDEX: return "MLA_ERR_BAD_SEQ_INDEX";
     }
     return "MLA_ERR_UNKNOWN";
 }
@@ -347,6 +351,211 @@ mla_status_t mla_lse_merge_finish(int rows, int n_h, int d_c, const float *acc, 
     if (rows == 0) return MLA_OK;
     if (!acc || !lse_max || !o_lat) return MLA_ERR_INVALID_ARG;
     return from_cuda(launch_lse_merge_finish(rows, n_h, d_c, acc, lse_max, o_lat, lse, (cudaStream_t)stream));
+}
+
+// ---- drafted trees ------------------------------------------------------------------------------
+mla_status_t mla_tree_prepare(int B, const int32_t *cu_nodes, int total_nodes, const int32_t *parent,
+                              const int32_t *seq_lens, int mask_words, uint32_t *mask, int32_t *pos,
+                              int32_t *slot, int32_t *seq_idx, mla_stream_t stream) {
+    if (B < 0 || total_nodes < 0 || mask_words < 1 || mask_words > kMaxTreeNodes / 32 || B == INT_MAX)
+        return MLA_ERR_INVALID_ARG;
+    if (total_nodes == 0) return MLA_OK;
+    if (!cu_nodes || !parent || (B > 0 && !seq_lens) || !mask || !pos || !slot || !seq_idx) return MLA_ERR_INVALID_ARG;
+    return from_cuda(launch_tree_prepare(B, cu_nodes, total_nodes, parent, seq_lens, mask_words, mask, pos, slot,
+                                         seq_idx, (cudaStream_t)stream));
+}
+
+mla_status_t mla_tree_append(const mla_dims_t *dims, int T, const void *c_kv, const void *k_r,
+                             const int32_t *seq_idx, const int32_t *slot, const int32_t *pos,
+                             const int32_t *block_table, int num_seqs, int max_blocks_per_seq,
+                             int num_blocks, void *kv_pool, void *kr_pool, float *kv_scale,
+                             mla_stream_t stream) {
+    bool work;
+    mla_status_t s = check_append(dims, T, c_kv, k_r, seq_idx, pos, block_table, num_seqs, max_blocks_per_seq,
+                                  num_blocks, kv_pool, kr_pool, kv_scale, &work);
+    if (s != MLA_OK || !work) return s;
+    if (!slot) return MLA_ERR_INVALID_ARG;
+    return from_cuda(launch_tree_append(*dims, T, c_kv, k_r, seq_idx, slot, pos, block_table, num_seqs,
+                                        max_blocks_per_seq, num_blocks, kv_pool, kr_pool, kv_scale,
+                                        (cudaStream_t)stream));
+}
+
+// The sizes of mla_decode_tree that the kernels index with: node rows times heads in int.
+static bool tree_sizes_ok(const mla_dims_t *dims, int B, int total_nodes, int max_seq_len) {
+    return B >= 0 && B <= (1 << 20) && total_nodes >= 0 && max_seq_len >= 1 &&
+           (int64_t)total_nodes * dims->n_h <= INT_MAX && dims->n_h <= 65535;
+}
+
+size_t mla_decode_tree_workspace_size(const mla_dims_t *dims, int B, int total_nodes, int max_seq_len) {
+    if (check_dims(dims) != MLA_OK || !tree_sizes_ok(dims, B, total_nodes, max_seq_len)) return 0;
+    return tree_simt_workspace_bytes(*dims, total_nodes, max_seq_len) + 256;
+}
+
+mla_status_t mla_decode_tree(const mla_dims_t *dims, int B, const int32_t *cu_nodes, int total_nodes,
+                             int max_nodes, const void *q_abs, const void *kv_pool, const void *kr_pool,
+                             const float *kv_scale, const int32_t *block_table, int max_blocks_per_seq,
+                             int num_blocks, const int32_t *seq_lens, int max_seq_len,
+                             const uint32_t *mask, int mask_words, void *workspace,
+                             size_t workspace_bytes, void *o_lat, mla_dtype_t out_dtype, float *lse,
+                             mla_stream_t stream) {
+    mla_status_t s = check_dims(dims);
+    if (s != MLA_OK) return s;
+    if (!act_ok(out_dtype)) return MLA_ERR_UNSUPPORTED;
+    if (!tree_sizes_ok(dims, B, total_nodes, max_seq_len) || max_blocks_per_seq < 1 || num_blocks < 1 ||
+        max_nodes < 1 || max_nodes > kMaxTreeNodes || mask_words < (max_nodes + 31) / 32)
+        return MLA_ERR_INVALID_ARG;
+    if ((int64_t)max_blocks_per_seq * dims->page_size > INT_MAX ||
+        max_seq_len > max_blocks_per_seq * dims->page_size)
+        return MLA_ERR_INVALID_ARG;
+    if (B == 0 || total_nodes == 0) return MLA_OK;
+    if (!cu_nodes || !q_abs || !kv_pool || !block_table || !seq_lens || !mask || !workspace || !o_lat)
+        return MLA_ERR_INVALID_ARG;
+    const bool fp8 = dims->kv_dtype == MLA_DTYPE_FP8_E4M3;
+    if (fp8 != (kr_pool != nullptr) || fp8 != (kv_scale != nullptr)) return MLA_ERR_INVALID_ARG;
+    if (!aligned(workspace, 256)) return MLA_ERR_INVALID_ARG;
+    const size_t need = mla_decode_tree_workspace_size(dims, B, total_nodes, max_seq_len);
+    if (need == 0) return MLA_ERR_CUDA;  // the device could not be queried
+    if (workspace_bytes < need) return MLA_ERR_WORKSPACE_TOO_SMALL;
+    TreeArgs a;
+    a.B = B;
+    a.T = total_nodes;
+    a.max_nodes = max_nodes;
+    a.n_h = dims->n_h;
+    a.d_c = dims->d_c;
+    a.d_r = dims->d_r;
+    a.page = dims->page_size;
+    a.scale_log2 = (float)(1.4426950408889634 / sqrt((double)(dims->d_h + dims->d_r)));
+    a.q_abs = q_abs;
+    a.kv_pool = kv_pool;
+    a.kr_pool = kr_pool;
+    a.kv_scale = kv_scale;
+    a.cu = cu_nodes;
+    a.bt = block_table;
+    a.seq_lens = seq_lens;
+    a.max_blocks = max_blocks_per_seq;
+    a.num_blocks = num_blocks;
+    a.max_seq_len = max_seq_len;
+    a.mask = mask;
+    a.mask_words = mask_words;
+    a.o = o_lat;
+    a.out_bf16 = out_dtype == MLA_DTYPE_BF16;
+    a.lse = lse;
+    a.err = device_error_word();
+    return from_cuda(launch_tree_simt(*dims, a, workspace, (cudaStream_t)stream));
+}
+
+// A list of caches behind one table: every pool's buffers as the cache type asks.
+static mla_status_t check_pools(const mla_dims_t *dims, int num_pools, const mla_pool_t *pools) {
+    if (num_pools < 0 || (num_pools > 0 && !pools)) return MLA_ERR_INVALID_ARG;
+    const bool fp8 = dims->kv_dtype == MLA_DTYPE_FP8_E4M3;
+    for (int i = 0; i < num_pools; ++i) {
+        if (!pools[i].kv_pool || fp8 != (pools[i].kr_pool != nullptr) || fp8 != (pools[i].kv_scale != nullptr))
+            return MLA_ERR_INVALID_ARG;
+    }
+    return MLA_OK;
+}
+
+mla_status_t mla_cache_keep(const mla_dims_t *dims, int num_pools, const mla_pool_t *pools, int B,
+                            const int32_t *cu_nodes, int total_nodes, const int32_t *block_table,
+                            int max_blocks_per_seq, int num_blocks, const int32_t *seq_lens,
+                            const int32_t *keep, const int32_t *num_keep, int max_keep,
+                            int32_t *new_lens, mla_stream_t stream) {
+    mla_status_t s = check_dims(dims);
+    if (s != MLA_OK) return s;
+    s = check_pools(dims, num_pools, pools);
+    if (s != MLA_OK) return s;
+    if (B < 0 || total_nodes < 0 || max_blocks_per_seq < 1 || num_blocks < 1 || max_keep < 1 ||
+        max_keep > kMaxTreeNodes || (int64_t)max_blocks_per_seq * dims->page_size > INT_MAX)
+        return MLA_ERR_INVALID_ARG;
+    if (B == 0 || num_pools == 0) return MLA_OK;
+    if (!cu_nodes || !block_table || !seq_lens || !keep || !num_keep || new_lens == seq_lens)
+        return MLA_ERR_INVALID_ARG;
+    return from_cuda(launch_cache_keep(*dims, num_pools, pools, B, cu_nodes, total_nodes, block_table,
+                                       max_blocks_per_seq, num_blocks, seq_lens, keep, num_keep, max_keep, new_lens,
+                                       (cudaStream_t)stream));
+}
+
+// ---- pages ----------------------------------------------------------------------------------------
+static mla_status_t check_table(const mla_page_table_t *t, int n, PageTable *p) {
+    if (!t || n < 0) return MLA_ERR_INVALID_ARG;
+    if (t->page_size < 1 || t->num_seqs < 1 || t->max_blocks < 1 || t->num_blocks < 1) return MLA_ERR_INVALID_ARG;
+    if ((int64_t)t->max_blocks * t->page_size > INT_MAX || (int64_t)t->num_seqs * t->max_blocks > INT_MAX ||
+        (int64_t)n * t->max_blocks > INT_MAX || t->num_blocks > INT_MAX / 2 || n >= (1 << 30))
+        return MLA_ERR_INVALID_ARG;
+    if (!t->block_table || !t->refs || !t->seq_lens) return MLA_ERR_INVALID_ARG;
+    *p = PageTable{t->page_size, t->num_seqs, t->max_blocks, t->num_blocks, t->block_table, t->refs, t->seq_lens,
+                   nullptr};
+    return MLA_OK;
+}
+
+static mla_status_t check_pages_ws(const PageTable &p, int n, const void *ws, size_t bytes) {
+    if (!ws || !aligned(ws, 256)) return MLA_ERR_INVALID_ARG;
+    return bytes < pages_workspace_bytes(p, n) ? MLA_ERR_WORKSPACE_TOO_SMALL : MLA_OK;
+}
+
+size_t mla_pages_workspace_size(const mla_page_table_t *table, int n) {
+    PageTable p;
+    return check_table(table, n, &p) == MLA_OK ? pages_workspace_bytes(p, n) : 0;
+}
+
+mla_status_t mla_pages_fork(const mla_page_table_t *table, int n, const int32_t *parent,
+                            const int32_t *child, void *workspace, size_t workspace_bytes,
+                            mla_stream_t stream) {
+    PageTable p;
+    mla_status_t s = check_table(table, n, &p);
+    if (s != MLA_OK || n == 0) return s;
+    if (!parent || !child) return MLA_ERR_INVALID_ARG;
+    if ((s = check_pages_ws(p, n, workspace, workspace_bytes)) != MLA_OK) return s;
+    p.err = device_error_word();
+    return from_cuda(launch_pages_fork(p, n, parent, child, workspace, (cudaStream_t)stream));
+}
+
+mla_status_t mla_pages_grow(const mla_page_table_t *table, int n, const int32_t *seqs,
+                            const int32_t *new_lens, int32_t *moves, int32_t *num_moves,
+                            void *workspace, size_t workspace_bytes, mla_stream_t stream) {
+    PageTable p;
+    mla_status_t s = check_table(table, n, &p);
+    if (s != MLA_OK) return s;
+    if (!num_moves || (n > 0 && (!new_lens || !moves)) || (!seqs && n > p.num_seqs)) return MLA_ERR_INVALID_ARG;
+    if ((s = check_pages_ws(p, n, workspace, workspace_bytes)) != MLA_OK) return s;
+    p.err = device_error_word();
+    return from_cuda(launch_pages_grow(p, n, seqs, new_lens, moves, num_moves, workspace, (cudaStream_t)stream));
+}
+
+mla_status_t mla_pages_trim(const mla_page_table_t *table, int n, const int32_t *seqs,
+                            const int32_t *new_lens, mla_stream_t stream) {
+    PageTable p;
+    mla_status_t s = check_table(table, n, &p);
+    if (s != MLA_OK || n == 0) return s;
+    if (!new_lens || (!seqs && n > p.num_seqs)) return MLA_ERR_INVALID_ARG;
+    p.err = device_error_word();
+    return from_cuda(launch_pages_trim(p, n, seqs, new_lens, (cudaStream_t)stream));
+}
+
+mla_status_t mla_pages_compact(const mla_page_table_t *table, int32_t *moves, int32_t *num_moves,
+                               void *workspace, size_t workspace_bytes, mla_stream_t stream) {
+    PageTable p;
+    mla_status_t s = check_table(table, 0, &p);
+    if (s != MLA_OK) return s;
+    if (!num_moves || (p.num_blocks > 1 && !moves)) return MLA_ERR_INVALID_ARG;
+    if ((s = check_pages_ws(p, 0, workspace, workspace_bytes)) != MLA_OK) return s;
+    p.err = device_error_word();
+    return from_cuda(launch_pages_compact(p, moves, num_moves, workspace, (cudaStream_t)stream));
+}
+
+mla_status_t mla_cache_copy_pages(const mla_dims_t *dims, int num_pools, const mla_pool_t *pools,
+                                  int num_blocks, const int32_t *moves, const int32_t *num_moves,
+                                  int max_moves, mla_stream_t stream) {
+    mla_status_t s = check_dims(dims);
+    if (s != MLA_OK) return s;
+    s = check_pools(dims, num_pools, pools);
+    if (s != MLA_OK) return s;
+    if (num_blocks < 1 || max_moves < 0 || (int64_t)dims->page_size * (dims->d_c + dims->d_r) * 4 > INT_MAX)
+        return MLA_ERR_INVALID_ARG;
+    if (num_pools == 0 || max_moves == 0) return MLA_OK;
+    if (!moves) return MLA_ERR_INVALID_ARG;
+    return from_cuda(launch_copy_pages(*dims, num_pools, pools, num_blocks, moves, num_moves, max_moves,
+                                       (cudaStream_t)stream));
 }
 
 mla_status_t mla_out_proj(const mla_dims_t *dims, int T, const float *o_lat, const void *w_uv,

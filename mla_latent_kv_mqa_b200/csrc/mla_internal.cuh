@@ -16,6 +16,9 @@ enum : unsigned {
     kErrBadBlock = MLA_ERR_BAD_BLOCK_TABLE,
     kErrBadSeqLen = MLA_ERR_BAD_SEQ_LEN,
     kErrTimeout = MLA_ERR_DEVICE_TIMEOUT,
+    kErrBadTree = MLA_ERR_BAD_TREE,
+    kErrOutOfPages = MLA_ERR_OUT_OF_PAGES,
+    kErrBadSeqIndex = MLA_ERR_BAD_SEQ_INDEX,
 };
 
 // Address of this device's error word (set up once per device by the API layer).

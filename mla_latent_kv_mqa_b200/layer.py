@@ -52,6 +52,26 @@ class PagedLatentCache:
             if poison:
                 self.kv_pool.fill_(float("nan"))
 
+    @classmethod
+    def over(cls, dims: N.mla_dims_t, kv_pool, kr_pool=None, kv_scale=None) -> "PagedLatentCache":
+        """A cache over buffers that the caller holds (one layer of a stacked allocation, say)."""
+        fp8 = dims.kv_dtype == N.MLA_DTYPE_FP8_E4M3
+        row = dims.d_c if fp8 else dims.d_c + dims.d_r
+        dt = torch.uint8 if fp8 else torch.float32 if dims.kv_dtype == N.MLA_DTYPE_F32 else torch.bfloat16
+        n, page = kv_pool.shape[0], dims.page_size
+        want = [(kv_pool, (n, page, row), dt)]
+        if fp8:
+            want += [(kr_pool, (n, page, dims.d_r), torch.bfloat16), (kv_scale, (n, page), torch.float32)]
+        elif kr_pool is not None or kv_scale is not None:
+            raise ValueError("kr_pool and kv_scale belong to an FP8 cache")
+        for x, shape, dtype in want:
+            if x is None or tuple(x.shape) != shape or x.dtype != dtype or not x.is_contiguous():
+                raise ValueError(f"cache buffer must be contiguous {dtype} {shape}")
+        self = cls.__new__(cls)
+        self.dims, self.num_blocks = dims, int(n)
+        self.kv_pool, self.kr_pool, self.kv_scale = kv_pool, kr_pool, kv_scale
+        return self
+
     @property
     def nbytes(self) -> int:
         n = self.kv_pool.numel() * self.kv_pool.element_size()
@@ -73,6 +93,7 @@ class MLADecodeLayer:
         self._ws = None
         self._ws_key = None
         self._pf_ws = None
+        self._tree_ws = None
 
     # -- the four calls ----------------------------------------------------------------------
     def append(self, cache: PagedLatentCache, c_kv, k_r, seq_idx, pos, block_table, stream=None):
@@ -161,6 +182,35 @@ class MLADecodeLayer:
         N.mla_prefill(d, B, cu_seqlens, T, max_seq_len, q_c, q_r, c_kv, k_r, self.w_uk, self.w_uv, self._pf_ws,
                       self._pf_ws.numel(), o, lse, stream)
         return o, lse
+
+    # -- drafted trees (see tree.DraftTrees) ---------------------------------------------------
+    def tree_append(self, cache: PagedLatentCache, c_kv, k_r, trees, block_table, stream=None):
+        """The drafted nodes' rows into their slots (trees.prepare first)."""
+        B, max_blocks = block_table.shape
+        N.mla_tree_append(self.dims, c_kv.shape[0], c_kv, k_r, trees.seq_idx, trees.slot, trees.pos, block_table, B,
+                          max_blocks, cache.num_blocks, cache.kv_pool, cache.kr_pool, cache.kv_scale, stream)
+
+    def decode_tree(self, cache: PagedLatentCache, q_abs, block_table, seq_lens, trees, max_seq_len,
+                    out_dtype="f32", o_lat=None, lse=None, stream=None):
+        """Every drafted node over the committed tokens and the nodes its mask names; returns
+        (o_lat [nodes, n_h, d_c], lse [nodes, n_h])."""
+        d = self.dims
+        B, max_blocks = block_table.shape
+        T = trees.total_nodes
+        dt = DTYPE[out_dtype]
+        if q_abs.shape[0] != T or B != trees.B:
+            raise ValueError("decode_tree: q_abs has a row per node, block_table one per tree")
+        if o_lat is None:
+            o_lat = torch.empty((T, d.n_h, d.d_c), dtype=TORCH_ACT[dt], device=q_abs.device)
+        if lse is None:
+            lse = torch.empty((T, d.n_h), dtype=torch.float32, device=q_abs.device)
+        n = N.mla_decode_tree_workspace_size(d, B, T, max_seq_len)
+        if self._tree_ws is None or self._tree_ws.numel() < n:
+            self._tree_ws = torch.empty(max(n, 256), dtype=torch.uint8, device=q_abs.device)
+        N.mla_decode_tree(d, B, trees.cu_nodes, T, trees.max_nodes, q_abs, cache.kv_pool, cache.kr_pool,
+                          cache.kv_scale, block_table, max_blocks, cache.num_blocks, seq_lens, max_seq_len,
+                          trees.mask, trees.mask_words, self._tree_ws, self._tree_ws.numel(), o_lat, dt, lse, stream)
+        return o_lat, lse
 
     def out_proj(self, o_lat, out_dtype="f32", out=None, stream=None):
         d = self.dims

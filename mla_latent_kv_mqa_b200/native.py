@@ -31,6 +31,10 @@ MLA_ERR_BAD_BLOCK_TABLE = 4
 MLA_ERR_BAD_SEQ_LEN = 5
 MLA_ERR_DEVICE_TIMEOUT = 6
 MLA_ERR_CUDA = 7
+MLA_ERR_BAD_TREE = 8
+MLA_ERR_OUT_OF_PAGES = 9
+MLA_ERR_BAD_SEQ_INDEX = 10
+MLA_MAX_TREE_NODES = 1024
 # mla_dtype_t
 MLA_DTYPE_F32 = 0
 MLA_DTYPE_BF16 = 1
@@ -58,6 +62,16 @@ def make_dims(n_h, d_h, d_c, d_r, page_size=64, rope_base=1e4, act_dtype=MLA_DTY
     return mla_dims_t(n_h, d_h, d_c, d_r, page_size, rope_base, act_dtype, kv_dtype, flags)
 
 
+class mla_pool_t(ctypes.Structure):
+    _fields_ = [("kv_pool", ctypes.c_void_p), ("kr_pool", ctypes.c_void_p), ("kv_scale", ctypes.c_void_p)]
+
+
+class mla_page_table_t(ctypes.Structure):
+    _fields_ = [("page_size", ctypes.c_int), ("num_seqs", ctypes.c_int), ("max_blocks", ctypes.c_int),
+                ("num_blocks", ctypes.c_int), ("block_table", ctypes.c_void_p), ("refs", ctypes.c_void_p),
+                ("seq_lens", ctypes.c_void_p)]
+
+
 _vp, _i, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
 _dp = ctypes.POINTER(mla_dims_t)
 _lib.mla_absorb_q.argtypes = [_dp, _i, _vp, _vp, _vp, _vp, _vp, _vp]
@@ -78,6 +92,21 @@ _lib.mla_prefill_workspace_size.restype = _sz
 _lib.mla_prefill.argtypes = [_dp, _i, _vp, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp, _vp, _vp]
 _lib.mla_lse_merge_prepare.argtypes = [_i, _i, _i, _vp, _vp, _vp, _vp, _vp]
 _lib.mla_lse_merge_finish.argtypes = [_i, _i, _i, _vp, _vp, _vp, _vp, _vp]
+_pp, _tp = ctypes.POINTER(mla_pool_t), ctypes.POINTER(mla_page_table_t)
+_lib.mla_tree_prepare.argtypes = [_i, _vp, _i, _vp, _vp, _i, _vp, _vp, _vp, _vp, _vp]
+_lib.mla_tree_append.argtypes = [_dp, _i, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _vp, _vp, _vp, _vp]
+_lib.mla_decode_tree_workspace_size.argtypes = [_dp, _i, _i, _i]
+_lib.mla_decode_tree_workspace_size.restype = _sz
+_lib.mla_decode_tree.argtypes = [_dp, _i, _vp, _i, _i, _vp, _vp, _vp, _vp, _vp, _i, _i, _vp, _i, _vp, _i, _vp, _sz,
+                                 _vp, _i, _vp, _vp]
+_lib.mla_cache_keep.argtypes = [_dp, _i, _pp, _i, _vp, _i, _vp, _i, _i, _vp, _vp, _vp, _i, _vp, _vp]
+_lib.mla_pages_workspace_size.argtypes = [_tp, _i]
+_lib.mla_pages_workspace_size.restype = _sz
+_lib.mla_pages_fork.argtypes = [_tp, _i, _vp, _vp, _vp, _sz, _vp]
+_lib.mla_pages_grow.argtypes = [_tp, _i, _vp, _vp, _vp, _vp, _vp, _sz, _vp]
+_lib.mla_pages_trim.argtypes = [_tp, _i, _vp, _vp, _vp]
+_lib.mla_pages_compact.argtypes = [_tp, _vp, _vp, _vp, _sz, _vp]
+_lib.mla_cache_copy_pages.argtypes = [_dp, _i, _pp, _i, _vp, _vp, _i, _vp]
 _lib.mla_get_last_device_error.argtypes = []
 _lib.mla_status_string.argtypes = [_i]
 _lib.mla_status_string.restype = ctypes.c_char_p
@@ -85,7 +114,8 @@ _lib.mla_version.restype = _i
 for _f in ("mla_absorb_q", "mla_cache_append", "mla_decode", "mla_decode_fixed_scratch", "mla_out_proj",
            "mla_decode_project", "mla_prefill", "mla_append_absorb", "mla_get_last_device_error",
            "mla_lse_merge_prepare",
-           "mla_lse_merge_finish"):
+           "mla_lse_merge_finish", "mla_tree_prepare", "mla_tree_append", "mla_decode_tree", "mla_cache_keep",
+           "mla_pages_fork", "mla_pages_grow", "mla_pages_trim", "mla_pages_compact", "mla_cache_copy_pages"):
     getattr(_lib, _f).restype = _i
 
 
@@ -211,6 +241,78 @@ def mla_lse_merge_prepare(rows, n_h, d_c, o_lat, lse, lse_max, acc, stream=None)
 def mla_lse_merge_finish(rows, n_h, d_c, acc, lse_max, o_lat, lse=None, stream=None):
     _check(_lib.mla_lse_merge_finish(rows, n_h, d_c, _ptr(acc), _ptr(lse_max), _ptr(o_lat), _ptr(lse),
                                      _stream(stream)), "mla_lse_merge_finish")
+
+
+def mla_tree_prepare(B, cu_nodes, total_nodes, parent, seq_lens, mask_words, mask, pos, slot, seq_idx, stream=None):
+    _check(_lib.mla_tree_prepare(B, _ptr(cu_nodes), total_nodes, _ptr(parent), _ptr(seq_lens), mask_words, _ptr(mask),
+                                 _ptr(pos), _ptr(slot), _ptr(seq_idx), _stream(stream)), "mla_tree_prepare")
+
+
+def mla_tree_append(dims, T, c_kv, k_r, seq_idx, slot, pos, block_table, num_seqs, max_blocks_per_seq, num_blocks,
+                    kv_pool, kr_pool=None, kv_scale=None, stream=None):
+    _check(_lib.mla_tree_append(ctypes.byref(dims), T, _ptr(c_kv), _ptr(k_r), _ptr(seq_idx), _ptr(slot), _ptr(pos),
+                                _ptr(block_table), num_seqs, max_blocks_per_seq, num_blocks, _ptr(kv_pool),
+                                _ptr(kr_pool), _ptr(kv_scale), _stream(stream)), "mla_tree_append")
+
+
+def mla_decode_tree_workspace_size(dims, B, total_nodes, max_seq_len) -> int:
+    return int(_lib.mla_decode_tree_workspace_size(ctypes.byref(dims), B, total_nodes, max_seq_len))
+
+
+def mla_decode_tree(dims, B, cu_nodes, total_nodes, max_nodes, q_abs, kv_pool, kr_pool, kv_scale, block_table,
+                    max_blocks_per_seq, num_blocks, seq_lens, max_seq_len, mask, mask_words, workspace,
+                    workspace_bytes, o_lat, out_dtype=MLA_DTYPE_F32, lse=None, stream=None):
+    _check(_lib.mla_decode_tree(ctypes.byref(dims), B, _ptr(cu_nodes), total_nodes, max_nodes, _ptr(q_abs),
+                                _ptr(kv_pool), _ptr(kr_pool), _ptr(kv_scale), _ptr(block_table), max_blocks_per_seq,
+                                num_blocks, _ptr(seq_lens), max_seq_len, _ptr(mask), mask_words, _ptr(workspace),
+                                workspace_bytes, _ptr(o_lat), out_dtype, _ptr(lse), _stream(stream)),
+           "mla_decode_tree")
+
+
+def make_pools(pools):
+    """Array of mla_pool_t from (kv_pool, kr_pool, kv_scale) triples (tensors, addresses or None)."""
+    return (mla_pool_t * len(pools))(*[mla_pool_t(_ptr(a), _ptr(b), _ptr(c)) for a, b, c in pools])
+
+
+def mla_cache_keep(dims, pools, B, cu_nodes, total_nodes, block_table, max_blocks_per_seq, num_blocks, seq_lens, keep,
+                   num_keep, max_keep, new_lens=None, stream=None):
+    """``pools``: make_pools(...)."""
+    _check(_lib.mla_cache_keep(ctypes.byref(dims), len(pools), pools, B, _ptr(cu_nodes), total_nodes,
+                               _ptr(block_table), max_blocks_per_seq, num_blocks, _ptr(seq_lens), _ptr(keep),
+                               _ptr(num_keep), max_keep, _ptr(new_lens), _stream(stream)), "mla_cache_keep")
+
+
+def make_page_table(page_size, num_seqs, max_blocks, num_blocks, block_table, refs, seq_lens) -> mla_page_table_t:
+    return mla_page_table_t(page_size, num_seqs, max_blocks, num_blocks, _ptr(block_table), _ptr(refs), _ptr(seq_lens))
+
+
+def mla_pages_workspace_size(table, n) -> int:
+    return int(_lib.mla_pages_workspace_size(ctypes.byref(table), n))
+
+
+def mla_pages_fork(table, n, parent, child, workspace, workspace_bytes, stream=None):
+    _check(_lib.mla_pages_fork(ctypes.byref(table), n, _ptr(parent), _ptr(child), _ptr(workspace), workspace_bytes,
+                               _stream(stream)), "mla_pages_fork")
+
+
+def mla_pages_grow(table, n, seqs, new_lens, moves, num_moves, workspace, workspace_bytes, stream=None):
+    _check(_lib.mla_pages_grow(ctypes.byref(table), n, _ptr(seqs), _ptr(new_lens), _ptr(moves), _ptr(num_moves),
+                               _ptr(workspace), workspace_bytes, _stream(stream)), "mla_pages_grow")
+
+
+def mla_pages_trim(table, n, seqs, new_lens, stream=None):
+    _check(_lib.mla_pages_trim(ctypes.byref(table), n, _ptr(seqs), _ptr(new_lens), _stream(stream)), "mla_pages_trim")
+
+
+def mla_pages_compact(table, moves, num_moves, workspace, workspace_bytes, stream=None):
+    _check(_lib.mla_pages_compact(ctypes.byref(table), _ptr(moves), _ptr(num_moves), _ptr(workspace), workspace_bytes,
+                                  _stream(stream)), "mla_pages_compact")
+
+
+def mla_cache_copy_pages(dims, pools, num_blocks, moves, num_moves, max_moves, stream=None):
+    """``pools``: make_pools(...); ``num_moves``: device int32 [1], or None for all max_moves."""
+    _check(_lib.mla_cache_copy_pages(ctypes.byref(dims), len(pools), pools, num_blocks, _ptr(moves), _ptr(num_moves),
+                                     max_moves, _stream(stream)), "mla_cache_copy_pages")
 
 
 def mla_get_last_device_error() -> int:

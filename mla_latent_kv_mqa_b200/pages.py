@@ -1,0 +1,75 @@
+"""The pages of a paged latent cache, kept on the device: which sequence holds which, and how many
+hold each (include/mla.h, "Pages of the cache").
+
+    seqs = PagedSequences(page_size, num_seqs, max_blocks, num_blocks)
+    moves = seqs.grow(new_lens)                  # pages for new tokens, own copies of shared last pages
+    seqs.copy_pages(caches, moves)               # before the new rows are appended
+    seqs.fork(parent, child)                     # samples, beams: child holds parent's pages too
+    seqs.trim(new_lens)                          # cut or end sequences
+    seqs.copy_pages(caches, seqs.compact())      # pages in use to the front of the pool
+
+``block_table``, ``refs`` and ``seq_lens`` are the tensors the other calls take.  One table serves the
+caches of all layers.
+"""
+from __future__ import annotations
+
+import torch
+
+from . import native as N
+
+
+class PagedSequences:
+    def __init__(self, page_size: int, num_seqs: int, max_blocks: int, num_blocks: int, device="cuda"):
+        i32 = dict(dtype=torch.int32, device=device)
+        self.block_table = torch.full((num_seqs, max_blocks), -1, **i32)
+        self.refs = torch.zeros(num_blocks, **i32)
+        self.seq_lens = torch.zeros(num_seqs, **i32)
+        self.num_blocks = int(num_blocks)
+        self._table = N.make_page_table(page_size, num_seqs, max_blocks, num_blocks, self.block_table, self.refs,
+                                        self.seq_lens)
+        self._ws = None
+        self._i32 = i32
+
+    def _workspace(self, n: int):
+        need = N.mla_pages_workspace_size(self._table, n)
+        if self._ws is None or self._ws.numel() < need:
+            self._ws = torch.empty(max(need, 256), dtype=torch.uint8, device=self.block_table.device)
+        return self._ws
+
+    def fork(self, parent, child, stream=None):
+        """Sequence child[i] becomes a copy of parent[i]; all parents are read before any child changes."""
+        if parent.numel() != child.numel():
+            raise ValueError("fork: a parent for every child")
+        n = parent.numel()
+        ws = self._workspace(n)
+        N.mla_pages_fork(self._table, n, parent, child, ws, ws.numel(), stream)
+
+    def grow(self, new_lens, seqs=None, stream=None):
+        """Sequences ``seqs`` (default: 0, 1, ...) grow to ``new_lens`` tokens; returns the page copies
+        to make as (moves [n, 2], their number [1]) on the device, for copy_pages."""
+        n = new_lens.numel()
+        if seqs is not None and seqs.numel() != n:
+            raise ValueError("grow: a length for every sequence")
+        ws = self._workspace(n)
+        moves, count = torch.empty((n, 2), **self._i32), torch.empty(1, **self._i32)
+        N.mla_pages_grow(self._table, n, seqs, new_lens, moves, count, ws, ws.numel(), stream)
+        return moves, count
+
+    def trim(self, new_lens, seqs=None, stream=None):
+        """Sequences are cut to ``new_lens`` tokens (0: the sequence ends); their pages lose a holder."""
+        if seqs is not None and seqs.numel() != new_lens.numel():
+            raise ValueError("trim: a length for every sequence")
+        N.mla_pages_trim(self._table, new_lens.numel(), seqs, new_lens, stream)
+
+    def compact(self, stream=None):
+        """The pages in use take the lowest ids; returns the page copies to make, for copy_pages."""
+        ws = self._workspace(0)
+        moves, count = torch.empty((self.num_blocks // 2, 2), **self._i32), torch.empty(1, **self._i32)
+        N.mla_pages_compact(self._table, moves, count, ws, ws.numel(), stream)
+        return moves, count
+
+    def copy_pages(self, caches, moves, stream=None):
+        """Copy the pages ``moves`` = (pairs, number) names, in every cache."""
+        pairs, count = moves
+        pools = N.make_pools([(c.kv_pool, c.kr_pool, c.kv_scale) for c in caches])
+        N.mla_cache_copy_pages(caches[0].dims, pools, self.num_blocks, pairs, count, pairs.shape[0], stream)

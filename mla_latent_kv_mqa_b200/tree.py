@@ -1,0 +1,56 @@
+"""Drafted trees of a batch: which nodes, and the buffers that a step's calls share.
+
+A speculative step of one model::
+
+    trees = DraftTrees(cu_nodes, parent, max_nodes)
+    trees.prepare(seq_lens)                                            # once: masks, slots, positions
+    for layer, cache in ...:
+        layer.tree_append(cache, c_kv, k_r, trees, block_table)        # the nodes' rows
+        q_abs = layer.absorb(q_c, q_r, trees.pos)
+        o_lat, lse = layer.decode_tree(cache, q_abs, block_table, seq_lens, trees, max_seq_len)
+        o = layer.out_proj(o_lat)
+    new_lens = trees.keep(caches, block_table, seq_lens, keep, num_keep)   # the accepted path
+
+seq_lens counts the committed tokens and the nodes (include/mla.h, "Drafted trees").
+"""
+from __future__ import annotations
+
+import torch
+
+from . import native as N
+
+
+class DraftTrees:
+    """The drafted nodes of B sequences, packed: ``cu_nodes`` [B + 1] and ``parent`` [total_nodes],
+    int32 on the device, and ``max_nodes``, a host-side bound of a sequence's nodes.
+
+    ``mask`` [total_nodes, mask_words], ``pos``, ``slot`` and ``seq_idx`` [total_nodes] are written by
+    prepare(); a caller with masks of its own hands ``mask`` over instead (int32 words)."""
+
+    def __init__(self, cu_nodes: torch.Tensor, parent: torch.Tensor, max_nodes: int, mask: torch.Tensor | None = None):
+        if not 1 <= max_nodes <= N.MLA_MAX_TREE_NODES:
+            raise ValueError(f"max_nodes must be in [1, {N.MLA_MAX_TREE_NODES}]")
+        self.cu_nodes, self.parent, self.max_nodes = cu_nodes, parent, int(max_nodes)
+        self.B, self.total_nodes = cu_nodes.numel() - 1, parent.numel()
+        self.mask_words = (self.max_nodes + 31) // 32 if mask is None else mask.shape[1]
+        if mask is not None and (mask.shape[0] != self.total_nodes or 32 * self.mask_words < self.max_nodes or
+                                 not mask.is_contiguous()):
+            raise ValueError("mask must be contiguous [total_nodes, >= ceil(max_nodes / 32)]")
+        dev = cu_nodes.device
+        self.mask = torch.empty((self.total_nodes, self.mask_words), dtype=torch.int32, device=dev) if mask is None else mask
+        self.pos, self.slot, self.seq_idx = (torch.empty(self.total_nodes, dtype=torch.int32, device=dev) for _ in range(3))
+
+    def prepare(self, seq_lens, stream=None):
+        N.mla_tree_prepare(self.B, self.cu_nodes, self.total_nodes, self.parent, seq_lens, self.mask_words, self.mask,
+                           self.pos, self.slot, self.seq_idx, stream)
+
+    def keep(self, caches, block_table, seq_lens, keep, num_keep, new_lens=None, stream=None):
+        """The rows of the accepted nodes ``keep`` [B, max_keep] (each row's first num_keep[b],
+        ascending) to behind the committed tokens, in every cache; returns the new lengths."""
+        B, max_blocks = block_table.shape
+        if new_lens is None:
+            new_lens = torch.empty(B, dtype=torch.int32, device=block_table.device)
+        pools = N.make_pools([(c.kv_pool, c.kr_pool, c.kv_scale) for c in caches])
+        N.mla_cache_keep(caches[0].dims, pools, B, self.cu_nodes, self.total_nodes, block_table, max_blocks,
+                         caches[0].num_blocks, seq_lens, keep, num_keep, keep.shape[1], new_lens, stream)
+        return new_lens
