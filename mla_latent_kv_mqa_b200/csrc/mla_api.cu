@@ -383,11 +383,12 @@ mla_status_t mla_tree_append(const mla_dims_t *dims, int T, const void *c_kv, co
 // The sizes of mla_decode_tree that the kernels index with: node rows times heads in int.
 static bool tree_sizes_ok(const mla_dims_t *dims, int B, int total_nodes, int max_seq_len) {
     return B >= 0 && B <= (1 << 20) && total_nodes >= 0 && max_seq_len >= 1 &&
-           (int64_t)total_nodes * dims->n_h <= INT_MAX && dims->n_h <= 65535;
+           (int64_t)total_nodes * dims->n_h <= INT_MAX - 1024 && dims->n_h <= 65535;
 }
 
 size_t mla_decode_tree_workspace_size(const mla_dims_t *dims, int B, int total_nodes, int max_seq_len) {
     if (check_dims(dims) != MLA_OK || !tree_sizes_ok(dims, B, total_nodes, max_seq_len)) return 0;
+    if (tree_tc_supported(*dims)) return tree_tc_workspace_bytes(B);
     return tree_simt_workspace_bytes(*dims, total_nodes, max_seq_len) + 256;
 }
 
@@ -441,6 +442,14 @@ mla_status_t mla_decode_tree(const mla_dims_t *dims, int B, const int32_t *cu_no
     a.out_bf16 = out_dtype == MLA_DTYPE_BF16;
     a.lse = lse;
     a.err = device_error_word();
+    if (tree_tc_supported(*dims)) {
+        // TMA reads of the cache and q_abs, vector stores of o_lat; page rows as int TMA coordinates
+        if (!aligned(q_abs, 16) || !aligned(kv_pool, 16) || (kr_pool && !aligned(kr_pool, 16)) ||
+            (kv_scale && !aligned(kv_scale, 16)) || !aligned(o_lat, 16) ||
+            (int64_t)num_blocks * dims->page_size > INT_MAX)
+            return MLA_ERR_INVALID_ARG;
+        return from_cuda(launch_tree_tc(*dims, a, workspace, (cudaStream_t)stream));
+    }
     return from_cuda(launch_tree_simt(*dims, a, workspace, (cudaStream_t)stream));
 }
 

@@ -1,0 +1,869 @@
+// Tensor-core (tcgen05, CTA pairs) mla_decode_tree for d_c = 512, d_R = 64, 64-token pages.
+//
+// MLA article (itwiki "멀티 헤드 잠재 어텐션"), section 분리 RoPE output equation in the absorbed form
+// of section 행렬 흡수, for the drafted nodes of a sequence.  All nodes and heads of a sequence attend
+// to the same cache rows, so its (node, head) pairs are the rows of two dense contractions, whatever
+// the number of heads.  A tile is 128 of them, a step 256 tokens (four pages):
+//     S[128 x 256]  = Q[128 x 576] . KV[256 x 576]^T,     O[128 x 512] += P[128 x 256] . V[256 x 512].
+//
+// Split over a pair of SMs.  O in fp32 for 128 rows fills one SM's tensor memory, so the pair's two CTAs
+// take 64 rows each (cta_group::2, M = 128): O is 256 columns, S two buffers of 128.  No score and no P
+// crosses the pair, nothing is computed twice, and each operand byte of B is read from one CTA's shared
+// memory only: for S each CTA holds the K rows of two of the step's pages, for O the halves of V's
+// columns that its half of N takes.  In a CTA's tensor memory lanes 0-63 hold its rows against the
+// first half of N and lanes 64-127 the same rows against the second, so a softmax thread owns half a
+// row of S and exchanges the maximum with its partner.
+//
+// Roles (8 warps a CTA).  One thread loads (Q per tile; K and V as 16 KB stages in the order the MMAs
+// use them: K(u+1) before V(u), so that S of the next step is computed while this one's softmax runs);
+// one thread of the even CTA issues all MMAs; four warps do the softmax in log2 units with a lazily
+// moved maximum (O is rescaled when it grows by more than 8), write P as the MMA's A operand, and at a
+// tile's end write O; two warps clean the V rows that some row of the tile does not see.
+//
+// Masks.  Steps before ctx need none.  In the others a row's thread selects by its node's bits.  P is 0
+// where a node does not see a token, and 0 times what such a row holds must be 0: the cleaning warps zero
+// the rows behind the sequence, and the infinities and NaN of drafted rows (whoever sees such a row has
+// them in its scores already).  Committed rows are seen by every row of the tile.
+//
+// Split along the tokens.  All (tile, step) units of the batch are dealt to the pairs in contiguous
+// equal runs; a tile that lies in several runs leaves partial (O, m, l), at most two a pair, which a
+// second kernel joins.
+//
+// Every wait is bounded (2 s).  On give-up both CTAs' abort flags are set, MLA_ERR_DEVICE_TIMEOUT is
+// recorded, and both CTAs stay until copies and MMAs in flight have had time to land.
+#include <cudaTypedefs.h>
+#include <math.h>
+
+#include <mutex>
+
+#include "mla_internal.cuh"
+#include "sm100.cuh"
+#include "tmap.cuh"
+#include "tree.cuh"
+
+namespace mla {
+namespace {
+
+using namespace sm100;
+
+constexpr int DC = 512, ROW = 576, PG = 64, NCB = ROW / 64;
+constexpr int TILE = 128, HALF = 64;              // rows of a tile, and of a CTA
+constexpr int STEP = 256, SPG = STEP / PG;        // tokens and pages of a step
+constexpr int CB = PG * 128;                      // 64 rows x 64 bf16 columns, 128-byte swizzle
+constexpr int STAGE = 2 * CB, STAGES = 7;         // K: two pages' column block; V: a page's 128 columns
+constexpr int Q_OFF = 0, P_OFF = NCB * CB, RING_OFF = P_OFF + SPG * CB;
+constexpr int DATA = RING_OFF + STAGES * STAGE;
+constexpr int THREADS = 256;
+constexpr int CLEAN_WARP0 = 2, CLEAN_THREADS = 64, SM_WARP0 = 4, SM_THREADS = 128;
+constexpr uint32_t S_COL = 0, O_COL = 256, TMEM_COLS = 512;
+constexpr float RESCALE_LOG2 = 8.0f;
+constexpr int BAR_MAX = 1, BAR_CLEAN = 2;
+
+struct __align__(8) Ctrl {
+    uint64_t full[STAGES];    // even CTA: both CTAs' halves of a stage have landed (or were cleaned)
+    uint64_t empty[STAGES];   // each CTA: the MMAs that read the stage are done
+    uint64_t land[STAGES];    // each CTA: a V stage that the cleaning warps have to go over has landed
+    uint64_t q_full, q_empty;
+    uint64_t s_full[2], s_free[2], p_full, pv_done, o_free;
+    uint32_t tmem_base, abort;
+    int w_b, w_tile, w_step, w_n;
+    long long scan_u[THREADS / 32];
+    int scan_t[THREADS / 32];
+    float top[2][2][HALF], sum[2][HALF];  // by step parity (a thread may be a step behind its partner), half, row
+};
+constexpr int SMEM = 1024 + DATA + (int)((sizeof(Ctrl) + 127) / 128 * 128);
+static_assert(SMEM <= 232448, "shared memory per block");
+
+// A batch in units, for the join: unit_off[b], tile_off[b] of every sequence, totals at [B].
+struct TreePlan {
+    long long *unit_off;
+    int *tile_off;
+    float *o, *m, *l;  // [2 pairs][128][512], [2 pairs][128]
+    int pairs;
+};
+
+struct Seq {
+    int t0, n, L, ctx, tiles, steps;
+};
+__device__ __forceinline__ Seq seq_of(const TreeArgs &a, int b) {
+    Seq s;
+    s.t0 = a.cu[b];
+    s.n = a.cu[b + 1] - s.t0;
+    s.L = a.seq_lens[b];
+    s.ctx = s.L - s.n;
+    s.tiles = (int)(((long long)s.n * a.n_h + TILE - 1) / TILE);
+    s.steps = s.ctx < 0 || s.L > a.max_seq_len || s.L > a.max_blocks * PG ? 0 : (s.L + STEP - 1) / STEP;
+    return s;
+}
+
+// Walks a pair's units; every role walks the same ones.
+struct Walk {
+    Seq s;
+    int b, tile, step, left;
+    bool first;  // of its segment (a run of one tile's steps)
+    bool head;   // the segment is the pair's first
+    int seg0;    // the segment's first step
+    __device__ void init(const TreeArgs &a, const int *w) {
+        b = w[0];
+        tile = w[1];
+        step = seg0 = w[2];
+        left = w[3];
+        first = head = true;
+        if (left > 0) s = seq_of(a, b);
+    }
+    __device__ bool done() const { return left <= 0; }
+    __device__ bool last() const { return left == 1 || step == s.steps - 1; }
+    __device__ void next(const TreeArgs &a) {
+        first = last();
+        if (first) head = false;
+        --left;
+        if (++step == s.steps) {
+            step = 0;
+            if (++tile == s.tiles) {
+                tile = 0;
+                while (left > 0 && ++b < a.B) {
+                    s = seq_of(a, b);
+                    if (s.steps > 0 && s.tiles > 0) break;
+                }
+                if (b >= a.B) left = 0;
+            }
+        }
+        if (first) seg0 = step;
+    }
+};
+
+struct Ring {
+    int i;
+    uint32_t ph;
+    __device__ void adv() {
+        if (++i == STAGES) {
+            i = 0;
+            ph ^= 1u;
+        }
+    }
+};
+
+__device__ __forceinline__ long long unit_start(long long c, long long U, int pairs) { return c * U / pairs; }
+__device__ __forceinline__ int pair_of_unit(long long u, long long U, int pairs) {
+    int c = (int)(u * pairs / U);
+    while (c + 1 < pairs && unit_start(c + 1, U, pairs) <= u) ++c;
+    while (c > 0 && unit_start(c, U, pairs) > u) --c;
+    return c;
+}
+
+// The pair's run: every CTA scans the batch's tiles and units (two passes where the batch is larger than
+// the block); pair 0 also leaves the offsets for the join.  One sequence that is no tree refuses all.
+__device__ __noinline__ void schedule(const TreeArgs &a, const TreePlan &pl, int pair, uint32_t rank, Ctrl *c) {
+    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+    auto block_scan = [&](long long &u, int &t, long long &all_u, int &all_t) {  // inclusive
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long yu = __shfl_up_sync(0xffffffffu, u, o);
+            const int yt = __shfl_up_sync(0xffffffffu, t, o);
+            if (lane >= o) {
+                u += yu;
+                t += yt;
+            }
+        }
+        if (lane == 31) {
+            c->scan_u[w] = u;
+            c->scan_t[w] = t;
+        }
+        __syncthreads();
+        long long bu = 0;
+        int bt = 0;
+        all_u = 0;
+        all_t = 0;
+        for (int k = 0; k < THREADS / 32; ++k) {
+            if (k < w) {
+                bu += c->scan_u[k];
+                bt += c->scan_t[k];
+            }
+            all_u += c->scan_u[k];
+            all_t += c->scan_t[k];
+        }
+        u += bu;
+        t += bt;
+        __syncthreads();
+    };
+    const bool report = pair == 0 && rank == 0;
+    if (tid == 0) c->w_n = 0;
+    bool bad = false, bad_len = false;
+    long long U = 0;
+    for (int b0 = 0; b0 < a.B; b0 += THREADS) {
+        const int b = b0 + tid;
+        long long u = 0, all_u;
+        int t = 0, all_t;
+        if (b < a.B) {
+            TreeSpan sp;
+            if (!tree_span(a.cu, b, a.B, a.T, a.max_nodes, &sp)) {
+                bad = true;
+            } else {
+                const Seq s = seq_of(a, b);
+                bad_len |= s.n > 0 && s.steps == 0;
+                u = (long long)s.tiles * s.steps;
+            }
+        }
+        block_scan(u, t, all_u, all_t);
+        U += all_u;
+    }
+    bad = __syncthreads_or(bad);
+    if (bad) U = 0;
+    if (report && (bad || bad_len)) record_error(a.err, bad ? kErrBadTree : kErrBadSeqLen);
+    const long long s0 = unit_start(pair, U, pl.pairs), s1 = unit_start(pair + 1, U, pl.pairs);
+    long long cu = 0;
+    int ct = 0;
+    for (int b0 = 0; b0 < a.B; b0 += THREADS) {
+        const int b = b0 + tid;
+        Seq s;
+        long long u = 0, all_u;
+        int t = 0, all_t;
+        if (b < a.B && !bad) {
+            s = seq_of(a, b);
+            u = (long long)s.tiles * s.steps;
+            t = s.tiles;
+        }
+        const long long mine = u;
+        const int mine_t = t;
+        block_scan(u, t, all_u, all_t);
+        const long long u0 = cu + u - mine;
+        if (b < a.B) {
+            if (mine > 0 && u0 <= s0 && s0 < u0 + mine && s1 > s0) {
+                c->w_b = b;
+                c->w_tile = (int)((s0 - u0) / s.steps);
+                c->w_step = (int)((s0 - u0) % s.steps);
+                c->w_n = (int)(s1 - s0);
+            }
+            if (report) {
+                pl.unit_off[b] = u0;
+                pl.tile_off[b] = ct + t - mine_t;
+            }
+        }
+        cu += all_u;
+        ct += all_t;
+    }
+    if (report && tid == 0) {
+        pl.unit_off[a.B] = U;
+        pl.tile_off[a.B] = ct;
+    }
+    __syncthreads();
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ bool named_red_or(bool v, int id, int n) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)v), "r"(id), "r"(n)
+        : "memory");
+    return r != 0;
+}
+
+// Which of the 32 tokens j .. j + 31 a node sees: all before ctx, its mask's bits from there, none behind L.
+__device__ __forceinline__ uint32_t sees32(const uint32_t *mask, int words, int j, int ctx, int L) {
+    const int rem = L - j, k = j - ctx;
+    if (rem <= 0) return 0u;
+    uint32_t v = 0xffffffffu;
+    if (k > -32) {
+        auto word = [&](int w) { return w < words ? mask[w] : 0u; };
+        if (k < 0)
+            v = (0xffffffffu >> (32 + k)) | (word(0) << -k);
+        else
+            v = __funnelshift_r(word(k >> 5), word((k >> 5) + 1), k & 31);
+    }
+    return rem < 32 ? v & (0xffffffffu >> (32 - rem)) : v;
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
+tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+               const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ TreeArgs a,
+               const __grid_constant__ TreePlan pl) {
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_s = smem_u32(smem_raw), data_s = (raw_s + 1023u) & ~1023u;
+    Ctrl *ctrl = reinterpret_cast<Ctrl *>(smem_raw + (data_s - raw_s) + DATA);
+    volatile uint32_t *abort_flag = &ctrl->abort;
+    auto bar = [&](uint64_t &b) { return smem_u32(&b); };
+    auto lead = [&](uint64_t &b) { return mapa(smem_u32(&b), 0); };  // the even CTA's barrier
+    const uint32_t rank = cluster_ctarank();
+    const int pair = blockIdx.x >> 1, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < STAGES; ++i) {
+            mbar_init(bar(ctrl->full[i]), 2);
+            mbar_init(bar(ctrl->empty[i]), 1);
+            mbar_init(bar(ctrl->land[i]), 1);
+        }
+        mbar_init(bar(ctrl->q_full), 2);
+        mbar_init(bar(ctrl->q_empty), 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar(ctrl->s_full[i]), 1);
+            mbar_init(bar(ctrl->s_free[i]), 2 * SM_THREADS / 32);
+        }
+        mbar_init(bar(ctrl->p_full), 2 * SM_THREADS / 32);
+        mbar_init(bar(ctrl->pv_done), 1);
+        mbar_init(bar(ctrl->o_free), 2 * SM_THREADS / 32);
+        ctrl->abort = 0;
+        fence_mbarrier_init_cluster();
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(smem_u32(&ctrl->tmem_base), TMEM_COLS);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    tc_fence_after();
+    pdl_trigger();
+    pdl_wait();  // inputs are read from here on
+    schedule(a, pl, pair, rank, ctrl);
+    const uint32_t tmem = ctrl->tmem_base;
+    auto fail = [&]() {
+        *abort_flag = 1;
+        st_shared_cluster_u32(mapa(smem_u32(&ctrl->abort), rank ^ 1u), 1u);
+        record_error(a.err, kErrTimeout);
+    };
+
+    if (warp == 0 && lane == 0) {  // ================= loads =================
+        Walk it;
+        it.init(a, &ctrl->w_b);
+        Ring st{0, 0};
+        int ids[SPG];  // the pages of the step whose K went out
+        uint32_t q_ph = 1;
+        bool ok = true;
+        auto pages = [&](const Walk &w) {
+#pragma unroll
+            for (int p = 0; p < SPG; ++p) {
+                const int pg = w.step * SPG + p;
+                ids[p] = -1;
+                if (pg * PG < w.s.L) {
+                    int blk = a.bt[(size_t)w.b * a.max_blocks + pg];
+                    if (blk < 0 || blk >= a.num_blocks) {
+                        record_error(a.err, kErrBadBlock);
+                        blk = 0;  // in bounds; the result is flagged
+                    }
+                    ids[p] = blk;
+                }
+            }
+        };
+        auto load_q = [&](const Walk &w) -> bool {
+            if (!wait(bar(ctrl->q_empty), q_ph, abort_flag)) return false;
+            q_ph ^= 1u;
+            mbar_arrive_expect_tx_remote(lead(ctrl->q_full), NCB * CB);
+            tma_load_3d_pair(data_s + Q_OFF, &tm_q, 0, w.s.t0 * a.n_h + w.tile * TILE + (int)rank * HALF, 0,
+                             lead(ctrl->q_full));
+            return true;
+        };
+        auto load_k = [&]() -> bool {
+            const int p0 = rank ? ids[2] : ids[0], p1 = rank ? ids[3] : ids[1];
+            for (int cb = 0; cb < NCB; ++cb) {
+                if (!wait(bar(ctrl->empty[st.i]), st.ph ^ 1u, abort_flag)) return false;
+                const uint32_t dst = data_s + RING_OFF + st.i * STAGE, full = lead(ctrl->full[st.i]);
+                mbar_arrive_expect_tx_remote(full, (p0 >= 0 ? CB : 0) + (p1 >= 0 ? CB : 0));
+                if (p0 >= 0) tma_load_3d_pair(dst, &tm_k, 0, p0 * PG, cb, full);
+                if (p1 >= 0) tma_load_3d_pair(dst + CB, &tm_k, 0, p1 * PG, cb, full);
+                st.adv();
+            }
+            return true;
+        };
+        auto load_v = [&](const Walk &w, const int (&id)[SPG]) -> bool {
+#pragma unroll
+            for (int p = 0; p < SPG; ++p) {
+                const bool clean = (w.step * SPG + p + 1) * PG > w.s.ctx;
+                for (int nh = 0; nh < 2; ++nh) {
+                    if (!wait(bar(ctrl->empty[st.i]), st.ph ^ 1u, abort_flag)) return false;
+                    const uint32_t dst = data_s + RING_OFF + st.i * STAGE, full = lead(ctrl->full[st.i]);
+                    const int z = nh * 4 + (int)rank * 2;
+                    if (!clean) {
+                        mbar_arrive_expect_tx_remote(full, STAGE);
+                        tma_load_3d_pair(dst, &tm_v, 0, id[p] * PG, z, full);
+                    } else if (id[p] >= 0) {
+                        mbar_arrive_expect_tx(bar(ctrl->land[st.i]), STAGE);
+                        tma_load_3d(dst, &tm_v, 0, id[p] * PG, z, bar(ctrl->land[st.i]));
+                    } else {
+                        mbar_arrive(bar(ctrl->land[st.i]));
+                    }
+                    st.adv();
+                }
+            }
+            return true;
+        };
+        if (!it.done()) {
+            prefetch_tensormap(&tm_q);
+            prefetch_tensormap(&tm_k);
+            prefetch_tensormap(&tm_v);
+            pages(it);
+            ok = load_q(it) && load_k();
+            while (ok && !it.done()) {
+                const Walk cur = it;
+                int cur_ids[SPG];
+#pragma unroll
+                for (int p = 0; p < SPG; ++p) cur_ids[p] = ids[p];
+                it.next(a);
+                if (!it.done()) pages(it);
+                if (!it.done() && !it.first) ok = load_k() && load_v(cur, cur_ids);
+                else ok = load_v(cur, cur_ids) && (it.done() || (load_q(it) && load_k()));
+            }
+            // the last arrivals on this CTA's barriers have come before it may leave (a unit has 17 stages)
+            for (int i = 0; ok && i < STAGES; ++i) {
+                ok = wait(bar(ctrl->empty[st.i]), st.ph ^ 1u, abort_flag);
+                st.adv();
+            }
+            ok = ok && wait(bar(ctrl->q_empty), q_ph, abort_flag);
+        }
+        if (!ok) fail();
+    } else if (warp == 1 && lane == 0 && rank == 0) {  // ================= MMAs of both CTAs =================
+        constexpr uint32_t idesc_qk = idesc_bf16(TILE, STEP, false, false);
+        constexpr uint32_t idesc_pv = idesc_bf16(TILE, 256, false, true);
+        Walk it;
+        it.init(a, &ctrl->w_b);
+        Ring st{0, 0};
+        uint32_t q_ph = 0, s_ph[2] = {1, 1}, p_ph = 0, o_ph = 1;
+        int sb = 0;
+        bool ok = true;
+        auto qk = [&](const Walk &w) -> bool {
+            if (w.first) {
+                if (!wait<true>(bar(ctrl->q_full), q_ph, abort_flag)) return false;
+                q_ph ^= 1u;
+            }
+            if (!wait<true>(bar(ctrl->s_free[sb]), s_ph[sb], abort_flag)) return false;
+            s_ph[sb] ^= 1u;
+            tc_fence_after();
+            for (int cb = 0; cb < NCB; ++cb) {
+                if (!wait<true>(bar(ctrl->full[st.i]), st.ph, abort_flag)) return false;
+                tc_fence_after();
+                const uint32_t kb = data_s + RING_OFF + st.i * STAGE, qb = data_s + Q_OFF + cb * CB;
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    mma_ss_pair(tmem + S_COL + sb * HALF * 2, sdesc_sw128(qb + k * 32, 16, 1024),
+                                sdesc_sw128(kb + k * 32, 16, 1024), idesc_qk, (cb | k) != 0);
+                mma_commit_pair(bar(ctrl->empty[st.i]));
+                st.adv();
+            }
+            mma_commit_pair(bar(ctrl->s_full[sb]));
+            if (w.last()) mma_commit_pair(bar(ctrl->q_empty));
+            sb ^= 1;
+            return true;
+        };
+        auto pv = [&](const Walk &w) -> bool {
+            if (!wait<true>(bar(ctrl->p_full), p_ph, abort_flag)) return false;
+            p_ph ^= 1u;
+            if (w.first) {  // O's last tile has been read
+                if (!wait<true>(bar(ctrl->o_free), o_ph, abort_flag)) return false;
+                o_ph ^= 1u;
+            }
+            tc_fence_after();
+            for (int p = 0; p < SPG; ++p)
+                for (int nh = 0; nh < 2; ++nh) {
+                    if (!wait<true>(bar(ctrl->full[st.i]), st.ph, abort_flag)) return false;
+                    tc_fence_after();
+                    const uint32_t vb = data_s + RING_OFF + st.i * STAGE, pb = data_s + P_OFF + p * CB;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        mma_ss_pair(tmem + O_COL + nh * 128, sdesc_sw128(pb + k * 32, 16, 1024),
+                                    sdesc_sw128(vb + k * 2048, CB, 1024), idesc_pv, !w.first || (p | k) != 0);
+                    mma_commit_pair(bar(ctrl->empty[st.i]));
+                    st.adv();
+                }
+            mma_commit_pair(bar(ctrl->pv_done));
+            return true;
+        };
+        if (!it.done()) {
+            ok = qk(it);
+            while (ok && !it.done()) {
+                const Walk cur = it;
+                it.next(a);
+                if (!it.done() && !it.first) ok = qk(it) && pv(cur);
+                else ok = pv(cur) && (it.done() || qk(it));
+            }
+        }
+        if (!ok) fail();
+    } else if (warp >= CLEAN_WARP0 && warp < SM_WARP0) {  // ================= V rows not seen by all =================
+        const int t = threadIdx.x - CLEAN_WARP0 * 32;
+        Walk it;
+        it.init(a, &ctrl->w_b);
+        Ring st{0, 0};
+        uint32_t land_ph = 0;  // a bit per stage: only the stages that are cleaned use their barrier
+        bool ok = true;
+        auto skip = [&](int n) {
+            for (int i = 0; i < n; ++i) st.adv();
+        };
+        // The ring's order is the loader's: K of the first step, then K(u+1) and V(u) within a segment, V
+        // before K across segments.
+        if (!it.done()) skip(NCB);
+        while (ok && !it.done()) {
+            const Walk cur = it;
+            it.next(a);
+            if (!it.done() && !it.first) skip(NCB);
+            for (int v = 0; ok && v < 2 * SPG; ++v, st.adv()) {
+                const int j0 = (cur.step * SPG + (v >> 1)) * PG;
+                if (j0 + PG <= cur.s.ctx) continue;
+                const bool good = wait(bar(ctrl->land[st.i]), (land_ph >> st.i) & 1u, abort_flag);
+                if (!(ok = !named_red_or(!good, BAR_CLEAN, CLEAN_THREADS))) break;
+                land_ph ^= 1u << st.i;
+                const uint32_t base = data_s + RING_OFF + st.i * STAGE;
+                const int r0 = max(cur.s.ctx - j0, 0);
+                for (int i = r0 * 16 + t; i < PG * 16; i += CLEAN_THREADS) {  // 16-byte chunks of the rows from ctx on
+                    const int row = i >> 4, c = i & 15;
+                    const uint32_t at = base + (c >> 3) * CB + row * 128 + (c & 7) * 16;
+                    uint32_t x[4] = {0u, 0u, 0u, 0u};
+                    if (j0 + row < cur.s.L) {
+                        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                     : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+                                     : "r"(at));
+                        bool hit = false;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            if ((x[k] & 0x7f80u) == 0x7f80u) {
+                                x[k] &= 0xffff0000u;
+                                hit = true;
+                            }
+                            if ((x[k] & 0x7f800000u) == 0x7f800000u) {
+                                x[k] &= 0xffffu;
+                                hit = true;
+                            }
+                        }
+                        if (!hit) continue;
+                    }
+                    st_shared_v4(at, x[0], x[1], x[2], x[3]);
+                }
+                fence_proxy_async_smem();
+                asm volatile("bar.sync %0, %1;" ::"n"(BAR_CLEAN), "n"(CLEAN_THREADS) : "memory");
+                if (t == 0) mbar_arrive_remote(lead(ctrl->full[st.i]));
+            }
+            if (!it.done() && it.first) skip(NCB);
+        }
+        if (!ok && lane == 0) fail();
+    } else if (warp >= SM_WARP0) {  // ================= softmax, P, O =================
+        const int t = threadIdx.x - SM_WARP0 * 32, r = t & (HALF - 1), half = t >> 6;
+        const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t p_row = data_s + P_OFF + (uint32_t)half * 2 * CB + r * 128;
+        Walk it;
+        it.init(a, &ctrl->w_b);
+        int u = 0;
+        float m = -INFINITY, l = 0.f;
+        bool ok = true;
+        while (ok && !it.done()) {
+            const int row = it.tile * TILE + (int)rank * HALF + r;  // of the sequence's (node, head) pairs
+            const bool mine = row < it.s.n * a.n_h;
+            const int sb = u & 1;
+            bool good = wait<true>(bar(ctrl->s_full[sb]), (u >> 1) & 1, abort_flag);
+            tc_fence_after();
+            uint32_t v[STEP / 2];
+            if (good) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    tmem_ld32(tmem + lane_base + S_COL + sb * 128 + c * 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32 * c));
+                tmem_wait_ld();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_remote(lead(ctrl->s_free[sb]));
+            }
+            const int j0 = it.step * STEP + half * (STEP / 2);
+            if (j0 + STEP / 2 > it.s.ctx) {
+                const uint32_t *mask = a.mask + (size_t)(it.s.t0 + (mine ? row / a.n_h : 0)) * a.mask_words;
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    const uint32_t see = sees32(mask, a.mask_words, j0 + 32 * w, it.s.ctx, it.s.L);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (!((see >> j) & 1u)) v[32 * w + j] = 0xff800000u;  // -inf
+                }
+            }
+            float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int j = 0; j < STEP / 2; ++j) x[j & 3] = fmaxf(x[j & 3], __uint_as_float(v[j]));
+            float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * a.scale_log2;
+            ctrl->top[u & 1][half][r] = top;
+            // the PV before last read P and O's rescale may follow: both wait for the last PV
+            if (u > 0) good = good && wait<true>(bar(ctrl->pv_done), (u - 1) & 1, abort_flag);
+            if (named_red_or(!good, BAR_MAX, SM_THREADS)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            top = fmaxf(top, ctrl->top[u & 1][half ^ 1][r]);
+            float fac = 1.f;
+            if (it.first) {
+                m = top;
+                l = 0.f;
+            } else if (top > m + RESCALE_LOG2 || m == -INFINITY) {
+                fac = m == -INFINITY ? 0.f : ex2(m - top);
+                m = fmaxf(m, top);
+            }
+            const float base = m == -INFINITY ? 0.f : m;
+            if (!it.first && __any_sync(0xffffffffu, fac != 1.f)) {
+                l *= fac;
+#pragma unroll 1
+                for (int c = 0; c < 8; ++c) {
+                    uint32_t o[32];
+                    tmem_ld32(tmem + lane_base + O_COL + c * 32, o);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * fac);
+                    tmem_st32(tmem + lane_base + O_COL + c * 32, o);
+                }
+                tmem_wait_st();
+            }
+            float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int c = 0; c < STEP / 16; ++c) {  // eight tokens: one 16-byte chunk of P's row
+                uint32_t pk[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float p0 = ex2(fmaf(__uint_as_float(v[8 * c + 2 * k]), a.scale_log2, -base));
+                    const float p1 = ex2(fmaf(__uint_as_float(v[8 * c + 2 * k + 1]), a.scale_log2, -base));
+                    s[k] += p0 + p1;
+                    pk[k] = pack_bf16x2(p0, p1);
+                }
+                st_shared_v4(p_row + (c >> 3) * CB + (((c & 7) ^ (r & 7)) << 4), pk[0], pk[1], pk[2], pk[3]);
+            }
+            l += (s[0] + s[1]) + (s[2] + s[3]);
+            fence_proxy_async_smem();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_remote(lead(ctrl->p_full));
+
+            if (it.last()) {
+                ctrl->sum[half][r] = l;
+                good = wait<true>(bar(ctrl->pv_done), u & 1, abort_flag);
+                if (named_red_or(!good, BAR_MAX, SM_THREADS)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const float total = l + ctrl->sum[half ^ 1][r];
+                const bool whole = it.seg0 == 0 && it.step == it.s.steps - 1;
+                const int slot = 2 * pair + (it.head ? 0 : 1);
+                const float inv = total == 0.f ? 0.f : 1.f / total;
+                const size_t grow = (size_t)it.s.t0 * a.n_h + row;
+                if (half == 0) {
+                    if (!whole) {
+                        pl.m[slot * TILE + (int)rank * HALF + r] = m;
+                        pl.l[slot * TILE + (int)rank * HALF + r] = total;
+                    } else if (mine && a.lse) {
+                        a.lse[grow] = total == 0.f ? -INFINITY : (base + log2f(total)) * 0.69314718055994531f;
+                    }
+                }
+#pragma unroll 1
+                for (int c = 0; c < 8; ++c) {
+                    uint32_t o[32];
+                    tmem_ld32(tmem + lane_base + O_COL + c * 32, o);
+                    tmem_wait_ld();
+                    const int d = (c >> 2) * 256 + half * 128 + (c & 3) * 32;
+                    if (!whole) {
+                        float4 *dst = reinterpret_cast<float4 *>(pl.o + ((size_t)slot * TILE + rank * HALF + r) * DC + d);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            dst[i] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
+                                                 __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
+                    } else if (mine && a.out_bf16) {
+                        uint4 *dst = reinterpret_cast<uint4 *>(reinterpret_cast<__nv_bfloat16 *>(a.o) + grow * DC + d);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                w[k] = pack_bf16x2(__uint_as_float(o[8 * i + 2 * k]) * inv, __uint_as_float(o[8 * i + 2 * k + 1]) * inv);
+                            dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                    } else if (mine) {
+                        float4 *dst = reinterpret_cast<float4 *>(reinterpret_cast<float *>(a.o) + grow * DC + d);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            dst[i] = make_float4(__uint_as_float(o[4 * i]) * inv, __uint_as_float(o[4 * i + 1]) * inv,
+                                                 __uint_as_float(o[4 * i + 2]) * inv, __uint_as_float(o[4 * i + 3]) * inv);
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_remote(lead(ctrl->o_free));
+            }
+            ++u;
+            it.next(a);
+        }
+        if (!ok && lane == 0) fail();
+    }
+
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    if (*abort_flag) {  // copies and MMAs in flight land within microseconds
+        const uint64_t t0 = globaltimer();
+        while (globaltimer() - t0 < 5000000ull) {
+        }
+        __syncthreads();
+        cluster_sync();
+    }
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem, TMEM_COLS);
+    }
+}
+
+// Joins the tiles that lie in several pairs' runs: o = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s, a warp
+// per row.  Rows of a sequence without steps (a bad length) are 0 and -inf.
+constexpr int JOIN_ROWS = 8;
+__global__ void __launch_bounds__(JOIN_ROWS * 32)
+tree_tc_join_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ TreePlan pl) {
+    pdl_wait();
+    const int g = blockIdx.x, lane = threadIdx.x & 31;
+    if (g >= pl.tile_off[a.B]) return;
+    int lo = 0, hi = a.B;  // the last b with tile_off[b] <= g: the one that holds it, empty ones come before
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (pl.tile_off[mid] <= g) lo = mid;
+        else hi = mid;
+    }
+    const Seq s = seq_of(a, lo);
+    const int tile = g - pl.tile_off[lo], rr = blockIdx.y * JOIN_ROWS + (threadIdx.x >> 5), row = tile * TILE + rr;
+    if (row >= s.n * a.n_h) return;
+    const long long U = pl.unit_off[a.B], u0 = pl.unit_off[lo] + (long long)tile * s.steps;
+    int c0 = 0, c1 = -1;
+    if (s.steps > 0) {
+        c0 = pair_of_unit(u0, U, pl.pairs);
+        c1 = pair_of_unit(u0 + s.steps - 1, U, pl.pairs);
+        if (c0 == c1) return;
+    }
+    auto slot_of = [&](int c) {  // -1: the pair has no units
+        if (unit_start(c, U, pl.pairs) == unit_start(c + 1, U, pl.pairs)) return -1;
+        return 2 * c + (c == c0 && unit_start(c0, U, pl.pairs) != u0 ? 1 : 0);
+    };
+    float M = -INFINITY;
+    for (int c = c0; c <= c1; ++c) {
+        const int sl = slot_of(c);
+        if (sl >= 0) M = fmaxf(M, pl.m[sl * TILE + rr]);
+    }
+    const float base = M == -INFINITY ? 0.f : M;
+    float l = 0.f, acc[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) acc[i] = 0.f;
+    for (int c = c0; c <= c1; ++c) {
+        const int sl = slot_of(c);
+        if (sl < 0) continue;
+        const float ms = pl.m[sl * TILE + rr], ls = pl.l[sl * TILE + rr];
+        const float w = exp2f(ms - base);
+        l += w * ls;
+        if (w == 0.f) continue;
+        const float4 *src = reinterpret_cast<const float4 *>(pl.o + ((size_t)sl * TILE + rr) * DC);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float4 x = src[i * 32 + lane];
+            acc[4 * i] = fmaf(w, x.x, acc[4 * i]);
+            acc[4 * i + 1] = fmaf(w, x.y, acc[4 * i + 1]);
+            acc[4 * i + 2] = fmaf(w, x.z, acc[4 * i + 2]);
+            acc[4 * i + 3] = fmaf(w, x.w, acc[4 * i + 3]);
+        }
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const size_t grow = (size_t)s.t0 * a.n_h + row;
+    if (a.lse && lane == 0) a.lse[grow] = l == 0.f ? -INFINITY : (base + log2f(l)) * 0.69314718055994531f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (a.out_bf16)
+            reinterpret_cast<uint2 *>(reinterpret_cast<__nv_bfloat16 *>(a.o) + grow * DC)[i * 32 + lane] =
+                make_uint2(pack_bf16x2(acc[4 * i] * inv, acc[4 * i + 1] * inv),
+                           pack_bf16x2(acc[4 * i + 2] * inv, acc[4 * i + 3] * inv));
+        else
+            reinterpret_cast<float4 *>(reinterpret_cast<float *>(a.o) + grow * DC)[i * 32 + lane] =
+                make_float4(acc[4 * i] * inv, acc[4 * i + 1] * inv, acc[4 * i + 2] * inv, acc[4 * i + 3] * inv);
+    }
+}
+
+// Pairs that run at once on the current device (0: it cannot be queried), looked up once.
+int tree_pairs() {
+    static int known[64];
+    static std::mutex mu;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    std::lock_guard<std::mutex> lk(mu);
+    if (known[dev]) return known[dev];
+    if (cudaFuncSetAttribute(tree_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM) != cudaSuccess) return 0;
+    int sms = 148;
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * (sms / 2));
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = SMEM;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = 2;
+    attr.val.clusterDim.y = 1;
+    attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, tree_tc_kernel, &cfg) != cudaSuccess || n < 1) {
+        cudaGetLastError();
+        n = sms / 2;
+    }
+    return known[dev] = n;
+}
+
+size_t tree_tc_layout(int pairs, int B, char *base, TreePlan *pl) {
+    size_t off = 0;
+    auto take = [&](size_t bytes) {
+        char *p = base ? base + off : nullptr;
+        off += align_up(bytes, 256);
+        return p;
+    };
+    TreePlan t;
+    t.pairs = pairs;
+    t.unit_off = reinterpret_cast<long long *>(take(((size_t)B + 1) * sizeof(long long)));
+    t.tile_off = reinterpret_cast<int *>(take(((size_t)B + 1) * sizeof(int)));
+    t.o = reinterpret_cast<float *>(take((size_t)2 * pairs * TILE * DC * sizeof(float)));
+    t.m = reinterpret_cast<float *>(take((size_t)2 * pairs * TILE * sizeof(float)));
+    t.l = reinterpret_cast<float *>(take((size_t)2 * pairs * TILE * sizeof(float)));
+    if (pl) *pl = t;
+    return off;
+}
+
+}  // namespace
+
+bool tree_tc_supported(const mla_dims_t &d) {
+    return d.d_c == DC && d.d_r == ROW - DC && d.page_size == PG && d.act_dtype == MLA_DTYPE_BF16 &&
+           d.kv_dtype == MLA_DTYPE_BF16 && !(d.flags & MLA_FLAG_SIMT_DECODE);
+}
+
+size_t tree_tc_workspace_bytes(int B) {
+    const int pairs = tree_pairs();
+    return pairs < 1 ? 0 : tree_tc_layout(pairs, B, nullptr, nullptr);
+}
+
+cudaError_t launch_tree_tc(const mla_dims_t &d, const TreeArgs &a, void *ws, cudaStream_t st) {
+    const int pairs = tree_pairs();
+    if (pairs < 1) return cudaErrorNotSupported;
+    TreePlan pl;
+    tree_tc_layout(pairs, a.B, reinterpret_cast<char *>(ws), &pl);
+    const uint64_t pool_rows = (uint64_t)a.num_blocks * PG, q_rows = (uint64_t)a.T * a.n_h;
+    CUtensorMap tm_q, tm_k, tm_v;
+    if (!tmap_bf16_colblocks(&tm_q, a.q_abs, q_rows, ROW, ROW * 2, HALF, NCB) ||
+        !tmap_bf16_colblocks(&tm_k, a.kv_pool, pool_rows, ROW, ROW * 2, PG, 1) ||
+        !tmap_bf16_colblocks(&tm_v, a.kv_pool, pool_rows, ROW, ROW * 2, PG, 2))
+        return cudaErrorInvalidValue;
+    cudaLaunchAttribute pdl;
+    pdl.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    pdl.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * pairs);
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = SMEM;
+    cfg.stream = st;
+    cfg.attrs = &pdl;
+    cfg.numAttrs = 1;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, tree_tc_kernel, tm_q, tm_k, tm_v, a, pl);
+    if (e != cudaSuccess) return e;
+    const int64_t tiles = a.B + q_rows / TILE;  // at most: a sequence's last tile may be part-filled
+    cfg.gridDim = dim3((unsigned)tiles, TILE / JOIN_ROWS);
+    cfg.blockDim = dim3(JOIN_ROWS * 32);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, tree_tc_join_kernel, a, pl);
+}
+
+}  // namespace mla
