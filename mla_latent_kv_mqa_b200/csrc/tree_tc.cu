@@ -11,17 +11,19 @@
 // crosses the pair, nothing is computed twice, and each operand byte of B is read from one CTA's shared
 // memory only: for S each CTA holds the K rows of two of the step's pages, for O the halves of V's
 // columns that its half of N takes.  In a CTA's tensor memory lanes 0-63 hold its rows against the
-// first half of N and lanes 64-127 the same rows against the second, so a softmax thread owns half a
-// row of S and exchanges the maximum with its partner.
+// first half of N and lanes 64-127 the same rows against the second; a softmax thread owns a row against
+// one of the step's pages and exchanges the maximum with the three others of its row.
 //
-// Roles (8 warps a CTA).  One thread loads (Q per tile; K and V as 16 KB stages in the order the MMAs
-// use them: K(u+1) before V(u), so that S of the next step is computed while this one's softmax runs);
-// one thread of the even CTA issues all MMAs; four warps do the softmax in log2 units with a lazily
-// moved maximum (O is rescaled when it grows by more than 8), write P as the MMA's A operand, and at a
-// tile's end write O; two warps clean the V rows that some row of the tile does not see.
+// Roles (13 of 16 warps a CTA).  One thread loads Q per tile and K, one V, in rings of 16 KB stages; two threads
+// of the even CTA issue the MMAs of S and of O for both CTAs, S of the next step while this one's
+// softmax runs.  (An MMA costs its thread about 60 clocks, the 64 that it runs, and a stage's wait and
+// commit another 170: one thread for both left the tensor cores idle for half the time.)  Eight warps do
+// the softmax in log2 units with a lazily moved maximum (O is rescaled when it grows by more than 8),
+// write P as the MMA's A operand, and at a tile's end write O; one warp cleans the V rows that some row
+// of the tile does not see.
 //
 // Masks.  Steps before ctx need none.  In the others a row's thread selects by its node's bits.  P is 0
-// where a node does not see a token, and 0 times what such a row holds must be 0: the cleaning warps zero
+// where a node does not see a token, and 0 times what such a row holds must be 0: the cleaning warp zeroes
 // the rows behind the sequence, and the infinities and NaN of drafted rows (whoever sees such a row has
 // them in its scores already).  Committed rows are seen by every row of the tile.
 //
@@ -50,26 +52,30 @@ constexpr int DC = 512, ROW = 576, PG = 64, NCB = ROW / 64;
 constexpr int TILE = 128, HALF = 64;              // rows of a tile, and of a CTA
 constexpr int STEP = 256, SPG = STEP / PG;        // tokens and pages of a step
 constexpr int CB = PG * 128;                      // 64 rows x 64 bf16 columns, 128-byte swizzle
-constexpr int STAGE = 2 * CB, STAGES = 7;         // K: two pages' column block; V: a page's 128 columns
-constexpr int Q_OFF = 0, P_OFF = NCB * CB, RING_OFF = P_OFF + SPG * CB;
-constexpr int DATA = RING_OFF + STAGES * STAGE;
-constexpr int THREADS = 256;
-constexpr int CLEAN_WARP0 = 2, CLEAN_THREADS = 64, SM_WARP0 = 4, SM_THREADS = 128;
+constexpr int STAGE = 2 * CB;                     // K: two pages' column block; V: a page's 128 columns
+constexpr int K_STAGES = 4, V_STAGES = 3;
+constexpr int Q_OFF = 0, P_OFF = NCB * CB, K_OFF = P_OFF + SPG * CB, V_OFF = K_OFF + K_STAGES * STAGE;
+constexpr int DATA = V_OFF + V_STAGES * STAGE;
+constexpr int THREADS = 512;
+constexpr int LOAD_K_WARP = 0, LOAD_V_WARP = 1, QK_WARP = 2, PV_WARP = 3, SM_WARP0 = 4, CLEAN_WARP = 12;
+constexpr int SM_WARPS = 8, SM_THREADS = 32 * SM_WARPS;
 constexpr uint32_t S_COL = 0, O_COL = 256, TMEM_COLS = 512;
 constexpr float RESCALE_LOG2 = 8.0f;
-constexpr int BAR_MAX = 1, BAR_CLEAN = 2;
+constexpr int BAR_MAX = 1;
 
 struct __align__(8) Ctrl {
-    uint64_t full[STAGES];    // even CTA: both CTAs' halves of a stage have landed (or were cleaned)
-    uint64_t empty[STAGES];   // each CTA: the MMAs that read the stage are done
-    uint64_t land[STAGES];    // each CTA: a V stage that the cleaning warps have to go over has landed
+    uint64_t k_full[K_STAGES], v_full[V_STAGES];    // even CTA: both CTAs' halves have landed (or were cleaned)
+    uint64_t k_empty[K_STAGES], v_empty[V_STAGES];  // each CTA: the MMAs that read the stage are done
+    uint64_t land[V_STAGES];  // each CTA: a V stage that the cleaning warp has to go over has landed
     uint64_t q_full, q_empty;
-    uint64_t s_full[2], s_free[2], p_full, pv_done, o_free;
+    uint64_t s_full[2], s_free[2];
+    uint64_t p_full[SPG], p_free[SPG];  // a page of P: written / its MMAs done
+    uint64_t o_ok, pv_done;             // O read or rescaled as the step needs / the step's MMAs done
     uint32_t tmem_base, abort;
     int w_b, w_tile, w_step, w_n;
     long long scan_u[THREADS / 32];
     int scan_t[THREADS / 32];
-    float top[2][2][HALF], sum[2][HALF];  // by step parity (a thread may be a step behind its partner), half, row
+    float top[2][SPG][HALF], sum[SPG][HALF];  // by step parity (a thread may be a step behind its partners), page, row
 };
 constexpr int SMEM = 1024 + DATA + (int)((sizeof(Ctrl) + 127) / 128 * 128);
 static_assert(SMEM <= 232448, "shared memory per block");
@@ -135,8 +141,8 @@ struct Walk {
 struct Ring {
     int i;
     uint32_t ph;
-    __device__ void adv() {
-        if (++i == STAGES) {
+    __device__ void adv(int n) {
+        if (++i == n) {
             i = 0;
             ph ^= 1u;
         }
@@ -294,24 +300,31 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     const int pair = blockIdx.x >> 1, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < STAGES; ++i) {
-            mbar_init(bar(ctrl->full[i]), 2);
-            mbar_init(bar(ctrl->empty[i]), 1);
+        for (int i = 0; i < K_STAGES; ++i) {
+            mbar_init(bar(ctrl->k_full[i]), 2);
+            mbar_init(bar(ctrl->k_empty[i]), 1);
+        }
+        for (int i = 0; i < V_STAGES; ++i) {
+            mbar_init(bar(ctrl->v_full[i]), 2);
+            mbar_init(bar(ctrl->v_empty[i]), 1);
             mbar_init(bar(ctrl->land[i]), 1);
         }
         mbar_init(bar(ctrl->q_full), 2);
         mbar_init(bar(ctrl->q_empty), 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar(ctrl->s_full[i]), 1);
-            mbar_init(bar(ctrl->s_free[i]), 2 * SM_THREADS / 32);
+            mbar_init(bar(ctrl->s_free[i]), 2 * SM_WARPS);
         }
-        mbar_init(bar(ctrl->p_full), 2 * SM_THREADS / 32);
+        for (int i = 0; i < SPG; ++i) {
+            mbar_init(bar(ctrl->p_full[i]), 2 * SM_WARPS / SPG);
+            mbar_init(bar(ctrl->p_free[i]), 1);
+        }
+        mbar_init(bar(ctrl->o_ok), 2 * SM_WARPS);
         mbar_init(bar(ctrl->pv_done), 1);
-        mbar_init(bar(ctrl->o_free), 2 * SM_THREADS / 32);
         ctrl->abort = 0;
         fence_mbarrier_init_cluster();
     }
-    if (warp == 1) {
+    if (warp == QK_WARP) {
         tmem_alloc_pair(smem_u32(&ctrl->tmem_base), TMEM_COLS);
         tmem_relinquish_pair();
     }
@@ -329,20 +342,21 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         record_error(a.err, kErrTimeout);
     };
 
-    if (warp == 0 && lane == 0) {  // ================= loads =================
+    if ((warp == LOAD_K_WARP || warp == LOAD_V_WARP) && lane == 0) {  // ================= loads =================
+        const bool kw = warp == LOAD_K_WARP;
         Walk it;
         it.init(a, &ctrl->w_b);
         Ring st{0, 0};
-        int ids[SPG];  // the pages of the step whose K went out
         uint32_t q_ph = 1;
         bool ok = true;
-        auto pages = [&](const Walk &w) {
+        int ids[SPG];
+        auto pages = [&]() {
 #pragma unroll
             for (int p = 0; p < SPG; ++p) {
-                const int pg = w.step * SPG + p;
+                const int pg = it.step * SPG + p;
                 ids[p] = -1;
-                if (pg * PG < w.s.L) {
-                    int blk = a.bt[(size_t)w.b * a.max_blocks + pg];
+                if (!it.done() && pg * PG < it.s.L) {
+                    int blk = a.bt[(size_t)it.b * a.max_blocks + pg];
                     if (blk < 0 || blk >= a.num_blocks) {
                         record_error(a.err, kErrBadBlock);
                         blk = 0;  // in bounds; the result is flagged
@@ -351,33 +365,45 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 }
             }
         };
-        auto load_q = [&](const Walk &w) -> bool {
-            if (!wait(bar(ctrl->q_empty), q_ph, abort_flag)) return false;
-            q_ph ^= 1u;
-            mbar_arrive_expect_tx_remote(lead(ctrl->q_full), NCB * CB);
-            tma_load_3d_pair(data_s + Q_OFF, &tm_q, 0, w.s.t0 * a.n_h + w.tile * TILE + (int)rank * HALF, 0,
-                             lead(ctrl->q_full));
-            return true;
-        };
-        auto load_k = [&]() -> bool {
+        if (!it.done()) {
+            prefetch_tensormap(&tm_q);
+            prefetch_tensormap(&tm_k);
+            prefetch_tensormap(&tm_v);
+            pages();
+        }
+        while (ok && kw && !it.done()) {  // Q per segment; K: the CTA's two pages, a column block a stage
+            if (it.first) {
+                if (!(ok = wait(bar(ctrl->q_empty), q_ph, abort_flag))) break;
+                q_ph ^= 1u;
+                mbar_arrive_expect_tx_remote(lead(ctrl->q_full), NCB * CB);
+                tma_load_3d_pair(data_s + Q_OFF, &tm_q, 0, it.s.t0 * a.n_h + it.tile * TILE + (int)rank * HALF, 0,
+                                 lead(ctrl->q_full));
+            }
             const int p0 = rank ? ids[2] : ids[0], p1 = rank ? ids[3] : ids[1];
+            it.next(a);
+            pages();  // of the next step: the table's latency passes under this one's loads
             for (int cb = 0; cb < NCB; ++cb) {
-                if (!wait(bar(ctrl->empty[st.i]), st.ph ^ 1u, abort_flag)) return false;
-                const uint32_t dst = data_s + RING_OFF + st.i * STAGE, full = lead(ctrl->full[st.i]);
+                if (!(ok = wait(bar(ctrl->k_empty[st.i]), st.ph ^ 1u, abort_flag))) break;
+                const uint32_t dst = data_s + K_OFF + st.i * STAGE, full = lead(ctrl->k_full[st.i]);
                 mbar_arrive_expect_tx_remote(full, (p0 >= 0 ? CB : 0) + (p1 >= 0 ? CB : 0));
                 if (p0 >= 0) tma_load_3d_pair(dst, &tm_k, 0, p0 * PG, cb, full);
                 if (p1 >= 0) tma_load_3d_pair(dst + CB, &tm_k, 0, p1 * PG, cb, full);
-                st.adv();
+                st.adv(K_STAGES);
             }
-            return true;
-        };
-        auto load_v = [&](const Walk &w, const int (&id)[SPG]) -> bool {
+        }
+        while (ok && !kw && !it.done()) {  // V: a page's 128 columns of each half of O a stage
+            int id[SPG];
+#pragma unroll
+            for (int p = 0; p < SPG; ++p) id[p] = ids[p];
+            const int pg0 = it.step * SPG, ctx = it.s.ctx;
+            it.next(a);
+            pages();
 #pragma unroll
             for (int p = 0; p < SPG; ++p) {
-                const bool clean = (w.step * SPG + p + 1) * PG > w.s.ctx;
-                for (int nh = 0; nh < 2; ++nh) {
-                    if (!wait(bar(ctrl->empty[st.i]), st.ph ^ 1u, abort_flag)) return false;
-                    const uint32_t dst = data_s + RING_OFF + st.i * STAGE, full = lead(ctrl->full[st.i]);
+                const bool clean = (pg0 + p + 1) * PG > ctx;
+                for (int nh = 0; ok && nh < 2; ++nh) {
+                    if (!(ok = wait(bar(ctrl->v_empty[st.i]), st.ph ^ 1u, abort_flag))) break;
+                    const uint32_t dst = data_s + V_OFF + st.i * STAGE, full = lead(ctrl->v_full[st.i]);
                     const int z = nh * 4 + (int)rank * 2;
                     if (!clean) {
                         mbar_arrive_expect_tx_remote(full, STAGE);
@@ -388,131 +414,99 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     } else {
                         mbar_arrive(bar(ctrl->land[st.i]));
                     }
-                    st.adv();
+                    st.adv(V_STAGES);
                 }
             }
-            return true;
-        };
-        if (!it.done()) {
-            prefetch_tensormap(&tm_q);
-            prefetch_tensormap(&tm_k);
-            prefetch_tensormap(&tm_v);
-            pages(it);
-            ok = load_q(it) && load_k();
-            while (ok && !it.done()) {
-                const Walk cur = it;
-                int cur_ids[SPG];
-#pragma unroll
-                for (int p = 0; p < SPG; ++p) cur_ids[p] = ids[p];
-                it.next(a);
-                if (!it.done()) pages(it);
-                if (!it.done() && !it.first) ok = load_k() && load_v(cur, cur_ids);
-                else ok = load_v(cur, cur_ids) && (it.done() || (load_q(it) && load_k()));
+        }
+        // the last arrivals on this CTA's barriers have come before it may leave (a unit fills every stage)
+        if (ctrl->w_n > 0) {
+            for (int i = 0; ok && i < (kw ? K_STAGES : V_STAGES); ++i) {
+                ok = wait(bar(kw ? ctrl->k_empty[st.i] : ctrl->v_empty[st.i]), st.ph ^ 1u, abort_flag);
+                st.adv(kw ? K_STAGES : V_STAGES);
             }
-            // the last arrivals on this CTA's barriers have come before it may leave (a unit has 17 stages)
-            for (int i = 0; ok && i < STAGES; ++i) {
-                ok = wait(bar(ctrl->empty[st.i]), st.ph ^ 1u, abort_flag);
-                st.adv();
-            }
-            ok = ok && wait(bar(ctrl->q_empty), q_ph, abort_flag);
+            if (ok && kw) ok = wait(bar(ctrl->q_empty), q_ph, abort_flag);
         }
         if (!ok) fail();
-    } else if (warp == 1 && lane == 0 && rank == 0) {  // ================= MMAs of both CTAs =================
-        constexpr uint32_t idesc_qk = idesc_bf16(TILE, STEP, false, false);
-        constexpr uint32_t idesc_pv = idesc_bf16(TILE, 256, false, true);
+    } else if (warp == QK_WARP && lane == 0 && rank == 0) {  // ================= S of both CTAs =================
+        constexpr uint32_t idesc = idesc_bf16(TILE, STEP, false, false);
         Walk it;
         it.init(a, &ctrl->w_b);
         Ring st{0, 0};
-        uint32_t q_ph = 0, s_ph[2] = {1, 1}, p_ph = 0, o_ph = 1;
-        int sb = 0;
+        uint32_t q_ph = 0;
         bool ok = true;
-        auto qk = [&](const Walk &w) -> bool {
-            if (w.first) {
-                if (!wait<true>(bar(ctrl->q_full), q_ph, abort_flag)) return false;
+        for (int u = 0; ok && !it.done(); ++u) {
+            const int sb = u & 1;
+            if (it.first) {
+                if (!(ok = wait(bar(ctrl->q_full), q_ph, abort_flag))) break;
                 q_ph ^= 1u;
             }
-            if (!wait<true>(bar(ctrl->s_free[sb]), s_ph[sb], abort_flag)) return false;
-            s_ph[sb] ^= 1u;
-            tc_fence_after();
+            if (!(ok = wait(bar(ctrl->s_free[sb]), ((u >> 1) & 1) ^ 1, abort_flag))) break;
             for (int cb = 0; cb < NCB; ++cb) {
-                if (!wait<true>(bar(ctrl->full[st.i]), st.ph, abort_flag)) return false;
+                if (!(ok = wait(bar(ctrl->k_full[st.i]), st.ph, abort_flag))) break;
                 tc_fence_after();
-                const uint32_t kb = data_s + RING_OFF + st.i * STAGE, qb = data_s + Q_OFF + cb * CB;
+                const uint32_t kb = data_s + K_OFF + st.i * STAGE, qb = data_s + Q_OFF + cb * CB;
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    mma_ss_pair(tmem + S_COL + sb * HALF * 2, sdesc_sw128(qb + k * 32, 16, 1024),
-                                sdesc_sw128(kb + k * 32, 16, 1024), idesc_qk, (cb | k) != 0);
-                mma_commit_pair(bar(ctrl->empty[st.i]));
-                st.adv();
+                    mma_ss_pair(tmem + S_COL + sb * 128, sdesc_sw128(qb + k * 32, 16, 1024),
+                                sdesc_sw128(kb + k * 32, 16, 1024), idesc, (cb | k) != 0);
+                mma_commit_pair(bar(ctrl->k_empty[st.i]));
+                st.adv(K_STAGES);
             }
+            if (!ok) break;
             mma_commit_pair(bar(ctrl->s_full[sb]));
-            if (w.last()) mma_commit_pair(bar(ctrl->q_empty));
-            sb ^= 1;
-            return true;
-        };
-        auto pv = [&](const Walk &w) -> bool {
-            if (!wait<true>(bar(ctrl->p_full), p_ph, abort_flag)) return false;
-            p_ph ^= 1u;
-            if (w.first) {  // O's last tile has been read
-                if (!wait<true>(bar(ctrl->o_free), o_ph, abort_flag)) return false;
-                o_ph ^= 1u;
-            }
-            tc_fence_after();
-            for (int p = 0; p < SPG; ++p)
+            if (it.last()) mma_commit_pair(bar(ctrl->q_empty));
+            it.next(a);
+        }
+        if (!ok) fail();
+    } else if (warp == PV_WARP && lane == 0 && rank == 0) {  // ================= O of both CTAs =================
+        constexpr uint32_t idesc = idesc_bf16(TILE, 256, false, true);
+        Walk it;
+        it.init(a, &ctrl->w_b);
+        Ring st{0, 0};
+        bool ok = true;
+        for (int u = 0; ok && !it.done(); ++u) {
+            if (!(ok = wait(bar(ctrl->o_ok), u & 1, abort_flag))) break;
+            for (int p = 0; ok && p < SPG; ++p) {
+                if (!(ok = wait(bar(ctrl->p_full[p]), u & 1, abort_flag))) break;
+                const uint32_t pb = data_s + P_OFF + p * CB;
                 for (int nh = 0; nh < 2; ++nh) {
-                    if (!wait<true>(bar(ctrl->full[st.i]), st.ph, abort_flag)) return false;
+                    if (!(ok = wait(bar(ctrl->v_full[st.i]), st.ph, abort_flag))) break;
                     tc_fence_after();
-                    const uint32_t vb = data_s + RING_OFF + st.i * STAGE, pb = data_s + P_OFF + p * CB;
+                    const uint32_t vb = data_s + V_OFF + st.i * STAGE;
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         mma_ss_pair(tmem + O_COL + nh * 128, sdesc_sw128(pb + k * 32, 16, 1024),
-                                    sdesc_sw128(vb + k * 2048, CB, 1024), idesc_pv, !w.first || (p | k) != 0);
-                    mma_commit_pair(bar(ctrl->empty[st.i]));
-                    st.adv();
+                                    sdesc_sw128(vb + k * 2048, CB, 1024), idesc, !it.first || (p | k) != 0);
+                    mma_commit_pair(bar(ctrl->v_empty[st.i]));
+                    st.adv(V_STAGES);
                 }
-            mma_commit_pair(bar(ctrl->pv_done));
-            return true;
-        };
-        if (!it.done()) {
-            ok = qk(it);
-            while (ok && !it.done()) {
-                const Walk cur = it;
-                it.next(a);
-                if (!it.done() && !it.first) ok = qk(it) && pv(cur);
-                else ok = pv(cur) && (it.done() || qk(it));
+                if (ok) mma_commit_pair(bar(ctrl->p_free[p]));
             }
+            if (!ok) break;
+            mma_commit_pair(bar(ctrl->pv_done));
+            it.next(a);
         }
         if (!ok) fail();
-    } else if (warp >= CLEAN_WARP0 && warp < SM_WARP0) {  // ================= V rows not seen by all =================
-        const int t = threadIdx.x - CLEAN_WARP0 * 32;
+    } else if (warp == CLEAN_WARP) {  // ================= V rows not seen by all =================
         Walk it;
         it.init(a, &ctrl->w_b);
         Ring st{0, 0};
         uint32_t land_ph = 0;  // a bit per stage: only the stages that are cleaned use their barrier
         bool ok = true;
-        auto skip = [&](int n) {
-            for (int i = 0; i < n; ++i) st.adv();
-        };
-        // The ring's order is the loader's: K of the first step, then K(u+1) and V(u) within a segment, V
-        // before K across segments.
-        if (!it.done()) skip(NCB);
         while (ok && !it.done()) {
-            const Walk cur = it;
-            it.next(a);
-            if (!it.done() && !it.first) skip(NCB);
-            for (int v = 0; ok && v < 2 * SPG; ++v, st.adv()) {
-                const int j0 = (cur.step * SPG + (v >> 1)) * PG;
-                if (j0 + PG <= cur.s.ctx) continue;
-                const bool good = wait(bar(ctrl->land[st.i]), (land_ph >> st.i) & 1u, abort_flag);
-                if (!(ok = !named_red_or(!good, BAR_CLEAN, CLEAN_THREADS))) break;
+            for (int v = 0; ok && v < 2 * SPG; ++v, st.adv(V_STAGES)) {
+                const int j0 = (it.step * SPG + (v >> 1)) * PG;
+                if (j0 + PG <= it.s.ctx) continue;
+                if (!(ok = __all_sync(0xffffffffu, wait(bar(ctrl->land[st.i]), (land_ph >> st.i) & 1u, abort_flag)))) break;
                 land_ph ^= 1u << st.i;
-                const uint32_t base = data_s + RING_OFF + st.i * STAGE;
-                const int r0 = max(cur.s.ctx - j0, 0);
-                for (int i = r0 * 16 + t; i < PG * 16; i += CLEAN_THREADS) {  // 16-byte chunks of the rows from ctx on
+                const uint32_t base = data_s + V_OFF + st.i * STAGE;
+                const int r0 = max(it.s.ctx - j0, 0);
+#pragma unroll 4
+                for (int i = r0 * 16 + lane; i < PG * 16; i += 32) {  // 16-byte chunks of the rows from ctx on
                     const int row = i >> 4, c = i & 15;
                     const uint32_t at = base + (c >> 3) * CB + row * 128 + (c & 7) * 16;
                     uint32_t x[4] = {0u, 0u, 0u, 0u};
-                    if (j0 + row < cur.s.L) {
+                    if (j0 + row < it.s.L) {
                         asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                                      : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
                                      : "r"(at));
@@ -533,42 +527,43 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     st_shared_v4(at, x[0], x[1], x[2], x[3]);
                 }
                 fence_proxy_async_smem();
-                asm volatile("bar.sync %0, %1;" ::"n"(BAR_CLEAN), "n"(CLEAN_THREADS) : "memory");
-                if (t == 0) mbar_arrive_remote(lead(ctrl->full[st.i]));
+                __syncwarp();
+                if (lane == 0) mbar_arrive_pair(lead(ctrl->v_full[st.i]));
             }
-            if (!it.done() && it.first) skip(NCB);
+            it.next(a);
         }
         if (!ok && lane == 0) fail();
-    } else if (warp >= SM_WARP0) {  // ================= softmax, P, O =================
-        const int t = threadIdx.x - SM_WARP0 * 32, r = t & (HALF - 1), half = t >> 6;
+    } else if (warp >= SM_WARP0 && warp < SM_WARP0 + SM_WARPS) {  // ================= softmax, P, O =================
+        // thread: row r of the CTA against page pg of the step (64 columns of S), and 128 of O's columns
+        const int r = (warp & 1) * 32 + lane, half = (warp >> 1) & 1, cg = (warp - SM_WARP0) >> 2, pg = 2 * half + cg;
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t p_row = data_s + P_OFF + (uint32_t)half * 2 * CB + r * 128;
+        const uint32_t p_row = data_s + P_OFF + (uint32_t)pg * CB + r * 128;
         Walk it;
         it.init(a, &ctrl->w_b);
-        int u = 0;
         float m = -INFINITY, l = 0.f;
-        bool ok = true;
-        while (ok && !it.done()) {
+        bool ok = true, good = true;
+        for (int u = 0; ok && !it.done(); ++u) {
             const int row = it.tile * TILE + (int)rank * HALF + r;  // of the sequence's (node, head) pairs
             const bool mine = row < it.s.n * a.n_h;
             const int sb = u & 1;
-            bool good = wait<true>(bar(ctrl->s_full[sb]), (u >> 1) & 1, abort_flag);
+            good = good && wait(bar(ctrl->s_full[sb]), (u >> 1) & 1, abort_flag);
             tc_fence_after();
-            uint32_t v[STEP / 2];
+            uint32_t v[PG];
             if (good) {
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    tmem_ld32(tmem + lane_base + S_COL + sb * 128 + c * 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32 * c));
+                for (int c = 0; c < 2; ++c)
+                    tmem_ld32(tmem + lane_base + S_COL + sb * 128 + cg * PG + c * 32,
+                              *reinterpret_cast<uint32_t(*)[32]>(v + 32 * c));
                 tmem_wait_ld();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_remote(lead(ctrl->s_free[sb]));
+                if (lane == 0) mbar_arrive_pair(lead(ctrl->s_free[sb]));
             }
-            const int j0 = it.step * STEP + half * (STEP / 2);
-            if (j0 + STEP / 2 > it.s.ctx) {
+            const int j0 = it.step * STEP + pg * PG;
+            if (j0 + PG > it.s.ctx) {
                 const uint32_t *mask = a.mask + (size_t)(it.s.t0 + (mine ? row / a.n_h : 0)) * a.mask_words;
 #pragma unroll
-                for (int w = 0; w < 4; ++w) {
+                for (int w = 0; w < 2; ++w) {
                     const uint32_t see = sees32(mask, a.mask_words, j0 + 32 * w, it.s.ctx, it.s.L);
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
@@ -577,17 +572,16 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             }
             float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int j = 0; j < STEP / 2; ++j) x[j & 3] = fmaxf(x[j & 3], __uint_as_float(v[j]));
-            float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * a.scale_log2;
-            ctrl->top[u & 1][half][r] = top;
-            // the PV before last read P and O's rescale may follow: both wait for the last PV
-            if (u > 0) good = good && wait<true>(bar(ctrl->pv_done), (u - 1) & 1, abort_flag);
+            for (int j = 0; j < PG; ++j) x[j & 3] = fmaxf(x[j & 3], __uint_as_float(v[j]));
+            float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+            ctrl->top[sb][pg][r] = top;
             if (named_red_or(!good, BAR_MAX, SM_THREADS)) {
                 ok = false;
                 break;
             }
-            tc_fence_after();
-            top = fmaxf(top, ctrl->top[u & 1][half ^ 1][r]);
+#pragma unroll
+            for (int k = 0; k < SPG; ++k) top = fmaxf(top, ctrl->top[sb][k][r]);
+            top *= a.scale_log2;
             float fac = 1.f;
             if (it.first) {
                 m = top;
@@ -597,52 +591,55 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 m = fmaxf(m, top);
             }
             const float base = m == -INFINITY ? 0.f : m;
+            float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int j = 0; j < PG / 2; ++j) {  // P as bf16 pairs, into the front half of v
+                const float p0 = ex2(fmaf(__uint_as_float(v[2 * j]), a.scale_log2, -base));
+                const float p1 = ex2(fmaf(__uint_as_float(v[2 * j + 1]), a.scale_log2, -base));
+                s[j & 3] += p0 + p1;
+                v[j] = pack_bf16x2(p0, p1);
+            }
+            l = l * fac + ((s[0] + s[1]) + (s[2] + s[3]));
+            // a moved maximum rescales O, once the step before is in it
             if (!it.first && __any_sync(0xffffffffu, fac != 1.f)) {
-                l *= fac;
+                good = wait(bar(ctrl->pv_done), (u - 1) & 1, abort_flag);  // the next vote hears of a failure
+                tc_fence_after();
 #pragma unroll 1
                 for (int c = 0; c < 8; ++c) {
-                    uint32_t o[32];
-                    tmem_ld32(tmem + lane_base + O_COL + c * 32, o);
+                    uint32_t o[16];
+                    tmem_ld16(tmem + lane_base + O_COL + cg * 128 + c * 16, o);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * fac);
-                    tmem_st32(tmem + lane_base + O_COL + c * 32, o);
+                    for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * fac);
+                    tmem_st16(tmem + lane_base + O_COL + cg * 128 + c * 16, o);
                 }
                 tmem_wait_st();
             }
-            float s[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int c = 0; c < STEP / 16; ++c) {  // eight tokens: one 16-byte chunk of P's row
-                uint32_t pk[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float p0 = ex2(fmaf(__uint_as_float(v[8 * c + 2 * k]), a.scale_log2, -base));
-                    const float p1 = ex2(fmaf(__uint_as_float(v[8 * c + 2 * k + 1]), a.scale_log2, -base));
-                    s[k] += p0 + p1;
-                    pk[k] = pack_bf16x2(p0, p1);
-                }
-                st_shared_v4(p_row + (c >> 3) * CB + (((c & 7) ^ (r & 7)) << 4), pk[0], pk[1], pk[2], pk[3]);
-            }
-            l += (s[0] + s[1]) + (s[2] + s[3]);
-            fence_proxy_async_smem();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_remote(lead(ctrl->p_full));
+            if (lane == 0) mbar_arrive_pair(lead(ctrl->o_ok));
+            if (u > 0) good = good && wait(bar(ctrl->p_free[pg]), (u - 1) & 1, abort_flag);
+#pragma unroll
+            for (int c = 0; c < PG / 8; ++c)  // eight tokens: one 16-byte chunk of P's row
+                st_shared_v4(p_row + ((c ^ (r & 7)) << 4), v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_pair(lead(ctrl->p_full[pg]));
 
             if (it.last()) {
-                ctrl->sum[half][r] = l;
-                good = wait<true>(bar(ctrl->pv_done), u & 1, abort_flag);
+                ctrl->sum[pg][r] = l;
+                good = good && wait(bar(ctrl->pv_done), u & 1, abort_flag);
                 if (named_red_or(!good, BAR_MAX, SM_THREADS)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const float total = l + ctrl->sum[half ^ 1][r];
+                const float total = (ctrl->sum[0][r] + ctrl->sum[1][r]) + (ctrl->sum[2][r] + ctrl->sum[3][r]);
                 const bool whole = it.seg0 == 0 && it.step == it.s.steps - 1;
                 const int slot = 2 * pair + (it.head ? 0 : 1);
                 const float inv = total == 0.f ? 0.f : 1.f / total;
                 const size_t grow = (size_t)it.s.t0 * a.n_h + row;
-                if (half == 0) {
+                if (pg == 0) {
                     if (!whole) {
                         pl.m[slot * TILE + (int)rank * HALF + r] = m;
                         pl.l[slot * TILE + (int)rank * HALF + r] = total;
@@ -651,11 +648,11 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     }
                 }
 #pragma unroll 1
-                for (int c = 0; c < 8; ++c) {
+                for (int c = 0; c < 4; ++c) {
                     uint32_t o[32];
-                    tmem_ld32(tmem + lane_base + O_COL + c * 32, o);
+                    tmem_ld32(tmem + lane_base + O_COL + cg * 128 + c * 32, o);
                     tmem_wait_ld();
-                    const int d = (c >> 2) * 256 + half * 128 + (c & 3) * 32;
+                    const int d = cg * 256 + half * 128 + c * 32;
                     if (!whole) {
                         float4 *dst = reinterpret_cast<float4 *>(pl.o + ((size_t)slot * TILE + rank * HALF + r) * DC + d);
 #pragma unroll
@@ -680,11 +677,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                                                  __uint_as_float(o[4 * i + 2]) * inv, __uint_as_float(o[4 * i + 3]) * inv);
                     }
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_remote(lead(ctrl->o_free));
             }
-            ++u;
             it.next(a);
         }
         if (!ok && lane == 0) fail();
@@ -701,7 +694,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         __syncthreads();
         cluster_sync();
     }
-    if (warp == 1) {
+    if (warp == QK_WARP) {
         tc_fence_after();
         tmem_dealloc_pair(tmem, TMEM_COLS);
     }
