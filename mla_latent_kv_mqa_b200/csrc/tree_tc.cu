@@ -14,16 +14,16 @@
 // first half of N and lanes 64-127 the same rows against the second; a softmax thread owns a row against
 // one of the step's pages and exchanges the maximum with the three others of its row.
 //
-// Roles (13 of 16 warps a CTA).  One thread loads Q per tile and K, one V, in rings of 16 KB stages; two threads
+// Roles (16 warps a CTA).  One thread loads Q per tile and K, one V, in rings of 16 KB stages; two threads
 // of the even CTA issue the MMAs of S and of O for both CTAs, S of the next step while this one's
 // softmax runs.  (An MMA costs its thread about 60 clocks, the 64 that it runs, and a stage's wait and
 // commit another 170: one thread for both left the tensor cores idle for half the time.)  Eight warps do
 // the softmax in log2 units with a lazily moved maximum (O is rescaled when it grows by more than 8),
-// write P as the MMA's A operand, and at a tile's end write O; one warp cleans the V rows that some row
-// of the tile does not see.
+// write P as the MMA's A operand, and at a tile's end write O; four warps clean the V rows that some row
+// of the tile does not see (one warp took 25000 clocks a tile for it).
 //
 // Masks.  Steps before ctx need none.  In the others a row's thread selects by its node's bits.  P is 0
-// where a node does not see a token, and 0 times what such a row holds must be 0: the cleaning warp zeroes
+// where a node does not see a token, and 0 times what such a row holds must be 0: the cleaning warps zero
 // the rows behind the sequence, and the infinities and NaN of drafted rows (whoever sees such a row has
 // them in its scores already).  Committed rows are seen by every row of the tile.
 //
@@ -57,20 +57,22 @@ constexpr int K_STAGES = 4, V_STAGES = 3;
 constexpr int Q_OFF = 0, P_OFF = NCB * CB, K_OFF = P_OFF + SPG * CB, V_OFF = K_OFF + K_STAGES * STAGE;
 constexpr int DATA = V_OFF + V_STAGES * STAGE;
 constexpr int THREADS = 512;
-constexpr int LOAD_K_WARP = 0, LOAD_V_WARP = 1, QK_WARP = 2, PV_WARP = 3, SM_WARP0 = 4, CLEAN_WARP = 12;
-constexpr int SM_WARPS = 8, SM_THREADS = 32 * SM_WARPS;
+constexpr int LOAD_K_WARP = 0, LOAD_V_WARP = 1, QK_WARP = 2, PV_WARP = 3, SM_WARP0 = 4, CLEAN_WARP0 = 12;
+constexpr int SM_WARPS = 8, SM_THREADS = 32 * SM_WARPS, CLEAN_THREADS = THREADS - 32 * CLEAN_WARP0;
 constexpr uint32_t S_COL = 0, O_COL = 256, TMEM_COLS = 512;
 constexpr float RESCALE_LOG2 = 8.0f;
-constexpr int BAR_MAX = 1;
+constexpr int BAR_MAX = 1, BAR_CLEAN = 2;
 
 struct __align__(8) Ctrl {
     uint64_t k_full[K_STAGES], v_full[V_STAGES];    // even CTA: both CTAs' halves have landed (or were cleaned)
     uint64_t k_empty[K_STAGES], v_empty[V_STAGES];  // each CTA: the MMAs that read the stage are done
-    uint64_t land[V_STAGES];  // each CTA: a V stage that the cleaning warp has to go over has landed
+    uint64_t land[V_STAGES];  // each CTA: a V stage that the cleaning warps have to go over has landed
     uint64_t q_full, q_empty;
     uint64_t s_full[2], s_free[2];
     uint64_t p_full[SPG], p_free[SPG];  // a page of P: written / its MMAs done
-    uint64_t o_ok, pv_done;             // O read or rescaled as the step needs / the step's MMAs done
+    // By step parity: O read or rescaled as the step needs / the step's MMAs done.  A CTA may be a step ahead of
+    // its peer, so one barrier would take its arrivals for two steps as both CTAs' for one.
+    uint64_t o_ok[2], pv_done[2];
     uint32_t tmem_base, abort;
     int w_b, w_tile, w_step, w_n;
     long long scan_u[THREADS / 32];
@@ -118,6 +120,7 @@ struct Walk {
         if (left > 0) s = seq_of(a, b);
     }
     __device__ bool done() const { return left <= 0; }
+    __device__ int pages() const { return min(SPG, (s.L + PG - 1) / PG - step * SPG); }  // of this step
     __device__ bool last() const { return left == 1 || step == s.steps - 1; }
     __device__ void next(const TreeArgs &a) {
         first = last();
@@ -314,13 +317,13 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar(ctrl->s_full[i]), 1);
             mbar_init(bar(ctrl->s_free[i]), 2 * SM_WARPS);
+            mbar_init(bar(ctrl->o_ok[i]), 2 * SM_WARPS);
+            mbar_init(bar(ctrl->pv_done[i]), 1);
         }
         for (int i = 0; i < SPG; ++i) {
             mbar_init(bar(ctrl->p_full[i]), 2 * SM_WARPS / SPG);
             mbar_init(bar(ctrl->p_free[i]), 1);
         }
-        mbar_init(bar(ctrl->o_ok), 2 * SM_WARPS);
-        mbar_init(bar(ctrl->pv_done), 1);
         ctrl->abort = 0;
         fence_mbarrier_init_cluster();
     }
@@ -395,30 +398,29 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             int id[SPG];
 #pragma unroll
             for (int p = 0; p < SPG; ++p) id[p] = ids[p];
-            const int pg0 = it.step * SPG, ctx = it.s.ctx;
+            const int pg0 = it.step * SPG, ctx = it.s.ctx, np = it.pages();
             it.next(a);
             pages();
 #pragma unroll
             for (int p = 0; p < SPG; ++p) {
                 const bool clean = (pg0 + p + 1) * PG > ctx;
-                for (int nh = 0; ok && nh < 2; ++nh) {
+                for (int nh = 0; ok && p < np && nh < 2; ++nh) {
                     if (!(ok = wait(bar(ctrl->v_empty[st.i]), st.ph ^ 1u, abort_flag))) break;
                     const uint32_t dst = data_s + V_OFF + st.i * STAGE, full = lead(ctrl->v_full[st.i]);
                     const int z = nh * 4 + (int)rank * 2;
                     if (!clean) {
                         mbar_arrive_expect_tx_remote(full, STAGE);
                         tma_load_3d_pair(dst, &tm_v, 0, id[p] * PG, z, full);
-                    } else if (id[p] >= 0) {
+                    } else {
                         mbar_arrive_expect_tx(bar(ctrl->land[st.i]), STAGE);
                         tma_load_3d(dst, &tm_v, 0, id[p] * PG, z, bar(ctrl->land[st.i]));
-                    } else {
-                        mbar_arrive(bar(ctrl->land[st.i]));
                     }
                     st.adv(V_STAGES);
                 }
             }
         }
-        // the last arrivals on this CTA's barriers have come before it may leave (a unit fills every stage)
+        // the last arrivals on this CTA's barriers have come before it may leave (once per stage; a stage
+        // that no unit filled passes at once)
         if (ctrl->w_n > 0) {
             for (int i = 0; ok && i < (kw ? K_STAGES : V_STAGES); ++i) {
                 ok = wait(bar(kw ? ctrl->k_empty[st.i] : ctrl->v_empty[st.i]), st.ph ^ 1u, abort_flag);
@@ -463,11 +465,14 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         Walk it;
         it.init(a, &ctrl->w_b);
         Ring st{0, 0};
+        uint32_t p_ph = 0;  // a bit per page: a step's last pages may not be there
         bool ok = true;
         for (int u = 0; ok && !it.done(); ++u) {
-            if (!(ok = wait(bar(ctrl->o_ok), u & 1, abort_flag))) break;
-            for (int p = 0; ok && p < SPG; ++p) {
-                if (!(ok = wait(bar(ctrl->p_full[p]), u & 1, abort_flag))) break;
+            if (!(ok = wait(bar(ctrl->o_ok[u & 1]), (u >> 1) & 1, abort_flag))) break;
+            const int np = it.pages();
+            for (int p = 0; ok && p < np; ++p) {
+                if (!(ok = wait(bar(ctrl->p_full[p]), (p_ph >> p) & 1u, abort_flag))) break;
+                p_ph ^= 1u << p;
                 const uint32_t pb = data_s + P_OFF + p * CB;
                 for (int nh = 0; nh < 2; ++nh) {
                     if (!(ok = wait(bar(ctrl->v_full[st.i]), st.ph, abort_flag))) break;
@@ -483,52 +488,46 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 if (ok) mma_commit_pair(bar(ctrl->p_free[p]));
             }
             if (!ok) break;
-            mma_commit_pair(bar(ctrl->pv_done));
+            mma_commit_pair(bar(ctrl->pv_done[u & 1]));
             it.next(a);
         }
         if (!ok) fail();
-    } else if (warp == CLEAN_WARP) {  // ================= V rows not seen by all =================
+    } else if (warp >= CLEAN_WARP0) {  // ================= V rows not seen by all =================
+        const int t = threadIdx.x - CLEAN_WARP0 * 32;
         Walk it;
         it.init(a, &ctrl->w_b);
         Ring st{0, 0};
         uint32_t land_ph = 0;  // a bit per stage: only the stages that are cleaned use their barrier
         bool ok = true;
         while (ok && !it.done()) {
-            for (int v = 0; ok && v < 2 * SPG; ++v, st.adv(V_STAGES)) {
+            for (int v = 0; ok && v < 2 * it.pages(); ++v, st.adv(V_STAGES)) {
                 const int j0 = (it.step * SPG + (v >> 1)) * PG;
                 if (j0 + PG <= it.s.ctx) continue;
-                if (!(ok = __all_sync(0xffffffffu, wait(bar(ctrl->land[st.i]), (land_ph >> st.i) & 1u, abort_flag)))) break;
+                const bool good = wait(bar(ctrl->land[st.i]), (land_ph >> st.i) & 1u, abort_flag);
+                if (!(ok = !named_red_or(!good, BAR_CLEAN, CLEAN_THREADS))) break;
                 land_ph ^= 1u << st.i;
-                const uint32_t base = data_s + V_OFF + st.i * STAGE;
-                const int r0 = max(it.s.ctx - j0, 0);
-#pragma unroll 4
-                for (int i = r0 * 16 + lane; i < PG * 16; i += 32) {  // 16-byte chunks of the rows from ctx on
-                    const int row = i >> 4, c = i & 15;
-                    const uint32_t at = base + (c >> 3) * CB + row * 128 + (c & 7) * 16;
-                    uint32_t x[4] = {0u, 0u, 0u, 0u};
-                    if (j0 + row < it.s.L) {
-                        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                                     : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
-                                     : "r"(at));
-                        bool hit = false;
+                const uint32_t base = data_s + V_OFF + st.i * STAGE + (t & 8) / 8 * CB + (t & 7) * 16;
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            if ((x[k] & 0x7f80u) == 0x7f80u) {
-                                x[k] &= 0xffff0000u;
-                                hit = true;
-                            }
-                            if ((x[k] & 0x7f800000u) == 0x7f800000u) {
-                                x[k] &= 0xffffu;
-                                hit = true;
-                            }
-                        }
-                        if (!hit) continue;
+                for (int k = 0; k < PG * 16 / CLEAN_THREADS; ++k) {  // this thread's 16-byte chunk of every eighth row
+                    const int row = k * (CLEAN_THREADS / 16) + (t >> 4), j = j0 + row;
+                    const uint32_t at = base + row * 128;
+                    uint32_t x[4];
+                    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                 : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+                                 : "r"(at));
+                    bool hit = j >= it.s.L;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const bool lo = (x[i] & 0x7f80u) == 0x7f80u, hi = (x[i] & 0x7f800000u) == 0x7f800000u;
+                        hit |= lo | hi;
+                        x[i] &= (lo ? 0xffff0000u : 0xffffffffu) & (hi ? 0xffffu : 0xffffffffu);
+                        if (j >= it.s.L) x[i] = 0u;
                     }
-                    st_shared_v4(at, x[0], x[1], x[2], x[3]);
+                    if (hit && j >= it.s.ctx) st_shared_v4(at, x[0], x[1], x[2], x[3]);
                 }
                 fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_pair(lead(ctrl->v_full[st.i]));
+                asm volatile("bar.sync %0, %1;" ::"n"(BAR_CLEAN), "n"(CLEAN_THREADS) : "memory");
+                if (t == 0) mbar_arrive_pair(lead(ctrl->v_full[st.i]));
             }
             it.next(a);
         }
@@ -541,6 +540,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         Walk it;
         it.init(a, &ctrl->w_b);
         float m = -INFINITY, l = 0.f;
+        uint32_t p_ph = 1;
         bool ok = true, good = true;
         for (int u = 0; ok && !it.done(); ++u) {
             const int row = it.tile * TILE + (int)rank * HALF + r;  // of the sequence's (node, head) pairs
@@ -600,9 +600,12 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 v[j] = pack_bf16x2(p0, p1);
             }
             l = l * fac + ((s[0] + s[1]) + (s[2] + s[3]));
+            // Every thread waits for every step's MMAs in turn, two steps behind (by then they are done): a wait by
+            // parity tells two phases apart, not three.  The next vote hears of a failure.
+            if (u >= 2) good = wait(bar(ctrl->pv_done[sb]), ((u >> 1) & 1) ^ 1, abort_flag);
             // a moved maximum rescales O, once the step before is in it
             if (!it.first && __any_sync(0xffffffffu, fac != 1.f)) {
-                good = wait(bar(ctrl->pv_done), (u - 1) & 1, abort_flag);  // the next vote hears of a failure
+                good = good && wait(bar(ctrl->pv_done[sb ^ 1]), ((u - 1) >> 1) & 1, abort_flag);
                 tc_fence_after();
 #pragma unroll 1
                 for (int c = 0; c < 8; ++c) {
@@ -617,18 +620,21 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_pair(lead(ctrl->o_ok));
-            if (u > 0) good = good && wait(bar(ctrl->p_free[pg]), (u - 1) & 1, abort_flag);
+            if (lane == 0) mbar_arrive_pair(lead(ctrl->o_ok[sb]));
+            if (pg < it.pages()) {  // P is 0 behind the last page, and nothing multiplies it
+                good = good && wait(bar(ctrl->p_free[pg]), p_ph, abort_flag);
+                p_ph ^= 1u;
 #pragma unroll
-            for (int c = 0; c < PG / 8; ++c)  // eight tokens: one 16-byte chunk of P's row
-                st_shared_v4(p_row + ((c ^ (r & 7)) << 4), v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_pair(lead(ctrl->p_full[pg]));
+                for (int c = 0; c < PG / 8; ++c)  // eight tokens: one 16-byte chunk of P's row
+                    st_shared_v4(p_row + ((c ^ (r & 7)) << 4), v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_pair(lead(ctrl->p_full[pg]));
+            }
 
             if (it.last()) {
                 ctrl->sum[pg][r] = l;
-                good = good && wait(bar(ctrl->pv_done), u & 1, abort_flag);
+                good = good && wait(bar(ctrl->pv_done[sb]), (u >> 1) & 1, abort_flag);
                 if (named_red_or(!good, BAR_MAX, SM_THREADS)) {
                     ok = false;
                     break;
@@ -638,49 +644,63 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 const bool whole = it.seg0 == 0 && it.step == it.s.steps - 1;
                 const int slot = 2 * pair + (it.head ? 0 : 1);
                 const float inv = total == 0.f ? 0.f : 1.f / total;
-                const size_t grow = (size_t)it.s.t0 * a.n_h + row;
+                const int row0 = row - lane;  // this warp's 32 rows, of the sequence and of the CTA
+                const int crow0 = (warp & 1) * 32;
                 if (pg == 0) {
                     if (!whole) {
                         pl.m[slot * TILE + (int)rank * HALF + r] = m;
                         pl.l[slot * TILE + (int)rank * HALF + r] = total;
                     } else if (mine && a.lse) {
-                        a.lse[grow] = total == 0.f ? -INFINITY : (base + log2f(total)) * 0.69314718055994531f;
+                        a.lse[(size_t)it.s.t0 * a.n_h + row] =
+                            total == 0.f ? -INFINITY : (base + log2f(total)) * 0.69314718055994531f;
                     }
                 }
+                // O's rows pass through the warp's own rows of P (32 x 128 bytes, its MMAs are done), so that a
+                // store instruction writes four whole 128-byte lines instead of 16 bytes of 32 rows
+                const bool narrow = whole && a.out_bf16;
+                const size_t width = narrow ? DC * 2 : DC * 4;
+                char *dst = whole ? reinterpret_cast<char *>(a.o) + ((size_t)it.s.t0 * a.n_h + row0) * width
+                                  : reinterpret_cast<char *>(pl.o) + ((size_t)slot * TILE + rank * HALF + crow0) * width;
+                dst += (cg * 256 + half * 128) * (narrow ? 2 : 4);
+                const int rows_left = whole ? it.s.n * a.n_h - row0 : 32;
+                const float mul = whole ? inv : 1.f;
 #pragma unroll 1
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t o[32];
-                    tmem_ld32(tmem + lane_base + O_COL + cg * 128 + c * 32, o);
-                    tmem_wait_ld();
-                    const int d = cg * 256 + half * 128 + c * 32;
-                    if (!whole) {
-                        float4 *dst = reinterpret_cast<float4 *>(pl.o + ((size_t)slot * TILE + rank * HALF + r) * DC + d);
+                for (int c = 0; c < (narrow ? 2 : 4); ++c) {
+#pragma unroll 1
+                    for (int k = 0; k < (narrow ? 4 : 2); ++k) {
+                        uint32_t o[16];
+                        tmem_ld16(tmem + lane_base + O_COL + cg * 128 + (c * (narrow ? 4 : 2) + k) * 16, o);
+                        tmem_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            dst[i] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
-                                                 __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
-                    } else if (mine && a.out_bf16) {
-                        uint4 *dst = reinterpret_cast<uint4 *>(reinterpret_cast<__nv_bfloat16 *>(a.o) + grow * DC + d);
+                        for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * mul);
+                        if (narrow) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            uint32_t w[4];
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                w[k] = pack_bf16x2(__uint_as_float(o[8 * i + 2 * k]) * inv, __uint_as_float(o[8 * i + 2 * k + 1]) * inv);
-                            dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+                            for (int i = 0; i < 8; ++i)
+                                o[i] = pack_bf16x2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1]));
                         }
-                    } else if (mine) {
-                        float4 *dst = reinterpret_cast<float4 *>(reinterpret_cast<float *>(a.o) + grow * DC + d);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            dst[i] = make_float4(__uint_as_float(o[4 * i]) * inv, __uint_as_float(o[4 * i + 1]) * inv,
-                                                 __uint_as_float(o[4 * i + 2]) * inv, __uint_as_float(o[4 * i + 3]) * inv);
+                        for (int i = 0; i < 4; ++i)
+                            if (i < 2 || !narrow)
+                                st_shared_v4(p_row + ((((narrow ? 2 : 4) * k + i) ^ (r & 7)) << 4), o[4 * i], o[4 * i + 1],
+                                             o[4 * i + 2], o[4 * i + 3]);
                     }
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int rr = 4 * i + (lane >> 3), ch = lane & 7;
+                        uint32_t x[4];
+                        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                     : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+                                     : "r"(p_row + (rr - lane) * 128 + ((ch ^ (rr & 7)) << 4)));
+                        if (rr < rows_left)
+                            *reinterpret_cast<uint4 *>(dst + rr * width + c * 128 + ch * 16) = make_uint4(x[0], x[1], x[2], x[3]);
+                    }
+                    __syncwarp();
                 }
             }
             it.next(a);
         }
-        if (!ok && lane == 0) fail();
+        if (!(ok && good)) fail();
     }
 
     __syncwarp();
