@@ -435,6 +435,8 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         it.init(a, &ctrl->w_b);
         Ring st{0, 0};
         uint32_t q_ph = 0;
+        constexpr uint32_t HI = sdesc_sw128_hi(1024);
+        const uint32_t q_lo = sdesc_sw128_lo(data_s + Q_OFF, 16), k_lo = sdesc_sw128_lo(data_s + K_OFF, 16);
         bool ok = true;
         for (int u = 0; ok && !it.done(); ++u) {
             const int sb = u & 1;
@@ -443,14 +445,14 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 q_ph ^= 1u;
             }
             if (!(ok = wait(bar(ctrl->s_free[sb]), ((u >> 1) & 1) ^ 1, abort_flag))) break;
+            const uint32_t d = tmem + S_COL + sb * 128;
+#pragma unroll 1
             for (int cb = 0; cb < NCB; ++cb) {
                 if (!(ok = wait(bar(ctrl->k_full[st.i]), st.ph, abort_flag))) break;
                 tc_fence_after();
-                const uint32_t kb = data_s + K_OFF + st.i * STAGE, qb = data_s + Q_OFF + cb * CB;
+                const uint32_t kl = k_lo + st.i * (STAGE >> 4), ql = q_lo + cb * (CB >> 4);
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    mma_ss_pair(tmem + S_COL + sb * 128, sdesc_sw128(qb + k * 32, 16, 1024),
-                                sdesc_sw128(kb + k * 32, 16, 1024), idesc, (cb | k) != 0);
+                for (int k = 0; k < 4; ++k) mma_ss_pair(d, ql + 2 * k, kl + 2 * k, HI, idesc, (cb | k) != 0);
                 mma_commit_pair(bar(ctrl->k_empty[st.i]));
                 st.adv(K_STAGES);
             }
@@ -465,6 +467,8 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         Walk it;
         it.init(a, &ctrl->w_b);
         Ring st{0, 0};
+        constexpr uint32_t HI = sdesc_sw128_hi(1024);
+        const uint32_t p_lo = sdesc_sw128_lo(data_s + P_OFF, 16), v_lo = sdesc_sw128_lo(data_s + V_OFF, CB);
         uint32_t p_ph = 0;  // a bit per page: a step's last pages may not be there
         bool ok = true;
         for (int u = 0; ok && !it.done(); ++u) {
@@ -473,15 +477,16 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             for (int p = 0; ok && p < np; ++p) {
                 if (!(ok = wait(bar(ctrl->p_full[p]), (p_ph >> p) & 1u, abort_flag))) break;
                 p_ph ^= 1u << p;
-                const uint32_t pb = data_s + P_OFF + p * CB;
+                const uint32_t pl_ = p_lo + p * (CB >> 4);
+                const bool acc = !it.first || p > 0;
+#pragma unroll 1
                 for (int nh = 0; nh < 2; ++nh) {
                     if (!(ok = wait(bar(ctrl->v_full[st.i]), st.ph, abort_flag))) break;
                     tc_fence_after();
-                    const uint32_t vb = data_s + V_OFF + st.i * STAGE;
+                    const uint32_t vl = v_lo + st.i * (STAGE >> 4);
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        mma_ss_pair(tmem + O_COL + nh * 128, sdesc_sw128(pb + k * 32, 16, 1024),
-                                    sdesc_sw128(vb + k * 2048, CB, 1024), idesc, !it.first || (p | k) != 0);
+                        mma_ss_pair(tmem + O_COL + nh * 128, pl_ + 2 * k, vl + 128 * k, HI, idesc, acc || k > 0);
                     mma_commit_pair(bar(ctrl->v_empty[st.i]));
                     st.adv(V_STAGES);
                 }
