@@ -53,8 +53,9 @@ constexpr int TILE = 128, HALF = 64;              // rows of a tile, and of a CT
 constexpr int STEP = 256, SPG = STEP / PG;        // tokens and pages of a step
 constexpr int CB = PG * 128;                      // 64 rows x 64 bf16 columns, 128-byte swizzle
 constexpr int STAGE = 2 * CB;                     // K: two pages' column block; V: a page's 128 columns
-constexpr int K_STAGES = 4, V_STAGES = 3;
-constexpr int Q_OFF = 0, P_OFF = NCB * CB, K_OFF = P_OFF + SPG * CB, V_OFF = K_OFF + K_STAGES * STAGE;
+constexpr int K_STAGES = 4, V_STAGES = 4;
+constexpr int P_SLOTS = 2;                        // pages of P held at once
+constexpr int Q_OFF = 0, P_OFF = NCB * CB, K_OFF = P_OFF + P_SLOTS * CB, V_OFF = K_OFF + K_STAGES * STAGE;
 constexpr int DATA = V_OFF + V_STAGES * STAGE;
 constexpr int THREADS = 512;
 constexpr int LOAD_K_WARP = 0, LOAD_V_WARP = 1, QK_WARP = 2, PV_WARP = 3, SM_WARP0 = 4, CLEAN_WARP0 = 12;
@@ -122,7 +123,7 @@ struct Walk {
     __device__ bool done() const { return left <= 0; }
     __device__ int pages() const { return min(SPG, (s.L + PG - 1) / PG - step * SPG); }  // of this step
     __device__ bool last() const { return left == 1 || step == s.steps - 1; }
-    __device__ void next(const TreeArgs &a) {
+    __device__ __forceinline__ void next(const TreeArgs &a) {
         first = last();
         if (first) head = false;
         --left;
@@ -130,14 +131,21 @@ struct Walk {
             step = 0;
             if (++tile == s.tiles) {
                 tile = 0;
-                while (left > 0 && ++b < a.B) {
-                    s = seq_of(a, b);
-                    if (s.steps > 0 && s.tiles > 0) break;
-                }
-                if (b >= a.B) left = 0;
+                b = next_seq(a, b);
+                if (b < a.B) s = seq_of(a, b);
+                else left = 0;
             }
         }
         if (first) seg0 = step;
+    }
+    // The next sequence with units (B: none).  Out of line: the roles call it once a sequence and share the
+    // instruction cache.
+    static __device__ __noinline__ int next_seq(const TreeArgs &a, int b) {
+        while (++b < a.B) {
+            const Seq n = seq_of(a, b);
+            if (n.steps > 0 && n.tiles > 0) break;
+        }
+        return b;
     }
 };
 
@@ -477,7 +485,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             for (int p = 0; ok && p < np; ++p) {
                 if (!(ok = wait(bar(ctrl->p_full[p]), (p_ph >> p) & 1u, abort_flag))) break;
                 p_ph ^= 1u << p;
-                const uint32_t pl_ = p_lo + p * (CB >> 4);
+                const uint32_t pl_ = p_lo + (p & 1) * (CB >> 4);
                 const bool acc = !it.first || p > 0;
 #pragma unroll 1
                 for (int nh = 0; nh < 2; ++nh) {
@@ -541,11 +549,12 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         // thread: row r of the CTA against page pg of the step (64 columns of S), and 128 of O's columns
         const int r = (warp & 1) * 32 + lane, half = (warp >> 1) & 1, cg = (warp - SM_WARP0) >> 2, pg = 2 * half + cg;
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t p_row = data_s + P_OFF + (uint32_t)pg * CB + r * 128;
+        const uint32_t p_row = data_s + P_OFF + (uint32_t)(pg & 1) * CB + r * 128;
+        const uint32_t stage = data_s + P_OFF + (warp - SM_WARP0) * 2048;  // this warp's share of P, between tiles
         Walk it;
         it.init(a, &ctrl->w_b);
         float m = -INFINITY, l = 0.f;
-        uint32_t p_ph = 1;
+        int before = 0;  // steps so far that had the page pg ^ 2, which shares the slot of P
         bool ok = true, good = true;
         for (int u = 0; ok && !it.done(); ++u) {
             const int row = it.tile * TILE + (int)rank * HALF + r;  // of the sequence's (node, head) pairs
@@ -626,9 +635,12 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_pair(lead(ctrl->o_ok[sb]));
-            if (pg < it.pages()) {  // P is 0 behind the last page, and nothing multiplies it
-                good = good && wait(bar(ctrl->p_free[pg]), p_ph, abort_flag);
-                p_ph ^= 1u;
+            const int np = it.pages();
+            if (pg < np) {  // P is 0 behind the last page, and nothing multiplies it
+                // The slot's last user: page pg + 2 of the step before (a tile's first step finds all MMAs done),
+                // or page pg - 2 of this one.
+                if (pg >= 2 || !it.first)
+                    good = good && wait(bar(ctrl->p_free[pg ^ 2]), (before - (pg < 2)) & 1, abort_flag);
 #pragma unroll
                 for (int c = 0; c < PG / 8; ++c)  // eight tokens: one 16-byte chunk of P's row
                     st_shared_v4(p_row + ((c ^ (r & 7)) << 4), v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
@@ -636,6 +648,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 __syncwarp();
                 if (lane == 0) mbar_arrive_pair(lead(ctrl->p_full[pg]));
             }
+            before += (pg ^ 2) < np;
 
             if (it.last()) {
                 ctrl->sum[pg][r] = l;
@@ -660,8 +673,8 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                             total == 0.f ? -INFINITY : (base + log2f(total)) * 0.69314718055994531f;
                     }
                 }
-                // O's rows pass through the warp's own rows of P (32 x 128 bytes, its MMAs are done), so that a
-                // store instruction writes four whole 128-byte lines instead of 16 bytes of 32 rows
+                // O's rows pass through 2 KB of P (its MMAs are done) a warp, 64 bytes of each of the 32 rows at a time, so
+                // that a store instruction writes whole sectors of eight rows instead of 16 bytes of 32
                 const bool narrow = whole && a.out_bf16;
                 const size_t width = narrow ? DC * 2 : DC * 4;
                 char *dst = whole ? reinterpret_cast<char *>(a.o) + ((size_t)it.s.t0 * a.n_h + row0) * width
@@ -669,36 +682,36 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 dst += (cg * 256 + half * 128) * (narrow ? 2 : 4);
                 const int rows_left = whole ? it.s.n * a.n_h - row0 : 32;
                 const float mul = whole ? inv : 1.f;
+                const uint32_t mine_s = stage + lane * 64, key = (lane >> 1) & 3;
 #pragma unroll 1
-                for (int c = 0; c < (narrow ? 2 : 4); ++c) {
-#pragma unroll 1
-                    for (int k = 0; k < (narrow ? 4 : 2); ++k) {
-                        uint32_t o[16];
-                        tmem_ld16(tmem + lane_base + O_COL + cg * 128 + (c * (narrow ? 4 : 2) + k) * 16, o);
-                        tmem_wait_ld();
+                for (int c = 0; c < 8; ++c) {  // 16 of the 128 columns
+                    uint32_t o[16];
+                    tmem_ld16(tmem + lane_base + O_COL + cg * 128 + c * 16, o);
+                    tmem_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * mul);
-                        if (narrow) {
+                    for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * mul);
+                    if (narrow) {
 #pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                o[i] = pack_bf16x2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1]));
-                        }
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (i < 2 || !narrow)
-                                st_shared_v4(p_row + ((((narrow ? 2 : 4) * k + i) ^ (r & 7)) << 4), o[4 * i], o[4 * i + 1],
-                                             o[4 * i + 2], o[4 * i + 3]);
+                        for (int i = 0; i < 8; ++i)
+                            o[i] = pack_bf16x2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1]));
                     }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (i < 2 || !narrow)
+                            st_shared_v4(mine_s + ((((narrow ? 2 * (c & 1) : 0) + i) ^ key) << 4), o[4 * i], o[4 * i + 1],
+                                         o[4 * i + 2], o[4 * i + 3]);
+                    if (narrow && !(c & 1)) continue;
                     __syncwarp();
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int rr = 4 * i + (lane >> 3), ch = lane & 7;
+                    for (int i = 0; i < 4; ++i) {
+                        const int rr = 8 * i + (lane >> 2), ch = lane & 3;
                         uint32_t x[4];
                         asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                                      : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
-                                     : "r"(p_row + (rr - lane) * 128 + ((ch ^ (rr & 7)) << 4)));
+                                     : "r"(stage + rr * 64 + ((ch ^ ((rr >> 1) & 3)) << 4)));
                         if (rr < rows_left)
-                            *reinterpret_cast<uint4 *>(dst + rr * width + c * 128 + ch * 16) = make_uint4(x[0], x[1], x[2], x[3]);
+                            *reinterpret_cast<uint4 *>(dst + rr * width + (narrow ? c >> 1 : c) * 64 + ch * 16) =
+                                make_uint4(x[0], x[1], x[2], x[3]);
                     }
                     __syncwarp();
                 }

@@ -1,8 +1,8 @@
 """CPU model of the barriers between the MMA threads and the softmax warps of the tensor-core tree attention:
 two CTAs whose warps run at random speeds, mbarriers with an arrival count and a phase that waits tell by
 its parity, commits that arrive late and at different times in the two CTAs.  Every run must end, and no
-operand may be read before it is written nor overwritten before it is read.  The model fails where
-one barrier serves O in both step parities: a CTA that is a step ahead then completes its peer's phase."""
+operand may be read before it is written nor overwritten before it is read.  Mistakes planted in
+the model fail."""
 import random
 
 import pytest
@@ -30,18 +30,18 @@ class Deadlock(Exception):
     pass
 
 
-def run(seed, units, o_parities=2):
+def run(seed, units, planted=None):
     """units: (first, last, pages, rescale) per step."""
     rng = random.Random(seed)
     pair = lambda count: [Bar(count) for _ in range(CTAS)]
     s_full, s_free = [pair(1), pair(1)], [Bar(16), Bar(16)]
     p_full, p_free = [Bar(4) for _ in range(PAGES)], [pair(1) for _ in range(PAGES)]
-    o_ok = [Bar(16) for _ in range(o_parities)]
+    o_ok = [Bar(16), Bar(16)]
     pv_done = [pair(1), pair(1)]
     votes = [{"n": 0, "gen": 0} for _ in range(CTAS)]
     S = [None, None]                       # unit whose scores a buffer holds
     read_s = {}                            # unit -> warps that have read it
-    P = {}                                 # (cta, page, half) -> unit
+    P = {}                                 # (cta, slot, half) -> (unit, page): two slots hold four pages in turn
     ok_for = {}                            # unit -> warps past their O duties
     done = set()                           # units whose PV has run
     started = set()
@@ -60,20 +60,20 @@ def run(seed, units, o_parities=2):
     def pv():
         ph = [0] * PAGES
         for u, (first, last, pages, _) in enumerate(units):
-            while not o_ok[u % o_parities].passed(u // o_parities):
+            while not o_ok[u & 1].passed(u >> 1):
                 yield
             assert len(ok_for.get(u, ())) == 16, "PV before every warp was past O"
             for p in range(pages):
                 while not p_full[p].passed(ph[p]):
                     yield
                 ph[p] ^= 1
-                assert all(P.get((c, p, h)) == u for c in range(CTAS) for h in range(2)), "P not written"
+                assert all(P.get((c, p & 1, h)) == (u, p) for c in range(CTAS) for h in range(2)), "P not written"
                 tensor["pv"] += [("O", u, p), ("c", p_free[p])]
                 yield
             tensor["pv"] += [("end", u), ("c", pv_done[u & 1])]
 
     def softmax(cta, pg, h):
-        p_ph, me, vote = 1, (cta, pg, h), votes[cta]
+        before, me, vote = 0, (cta, pg, h), votes[cta]
 
         def ballot():
             gen = vote["gen"]
@@ -94,20 +94,22 @@ def run(seed, units, o_parities=2):
             if u >= 2:
                 while not pv_done[sb][cta].passed((u >> 1) ^ 1):
                     yield
-            if not first and rescale:
+            if not first and rescale and planted != 'rescale at once':
                 while not pv_done[sb ^ 1][cta].passed((u - 1) >> 1):
                     yield
+            if not first and rescale:
                 assert u - 1 in done, "O rescaled while the step before runs"
             ok_for.setdefault(u, set()).add(me)
-            o_ok[u % o_parities].arrive()
+            o_ok[u & 1].arrive()
             yield
             if pg < pages:
-                while not p_free[pg][cta].passed(p_ph):
+                wait = (pg >= 2 or not first) and planted != 'no wait for P'
+                while wait and not p_free[pg ^ 2][cta].passed(before - (pg < 2)):
                     yield
-                p_ph ^= 1
-                P[me] = u
+                P[cta, pg & 1, h] = u, pg
                 p_full[pg].arrive()
                 yield
+            before += (pg ^ 2) < pages
             if last:
                 while not pv_done[sb][cta].passed(u >> 1):
                     yield
@@ -124,7 +126,7 @@ def run(seed, units, o_parities=2):
                     S[op[1] & 1] = op[1]
                 elif op[0] == "O":
                     started.add(op[1])
-                    assert all(P.get((c, op[2], h)) == op[1] for c in range(CTAS) for h in range(2)), "P overwritten before it was read"
+                    assert all(P.get((c, op[2] & 1, h)) == op[1:] for c in range(CTAS) for h in range(2)), "P overwritten before it was read"
                 elif op[0] == "end":
                     done.add(op[1])
                 else:
@@ -170,11 +172,12 @@ def test_every_schedule_ends_and_keeps_the_order(seed):
     run(seed, batch(seed))
 
 
-def test_one_barrier_for_both_step_parities_fails():
+@pytest.mark.parametrize("planted", ["no wait for P", "rescale at once"])
+def test_planted_mistakes_fail(planted):
     bad = 0
-    for seed in range(60):
+    for seed in range(40):
         try:
-            run(seed, batch(seed), o_parities=1)
+            run(seed, batch(seed), planted)
         except (AssertionError, Deadlock):
             bad += 1
-    assert bad > 0
+    assert bad > 30
