@@ -407,7 +407,8 @@ mla_status_t mla_tree_append(const mla_dims_t *dims, int T, const void *c_kv, co
  *     o_lat = sum_j softmax(s)_j c_j,       lse = ln sum_j exp(s_j).
  * A node that sees no token (no committed one and an empty mask row) gets o_lat = 0, lse = -inf.
  * The mask is taken as it is: any set of drafted tokens, not only ancestors.
- * What a masked token's row holds does not matter, infinities and NaN included.
+ * What a masked token's row holds does not matter, infinities and NaN included: a token of weight 0
+ * (masked, or a score of -inf) is no part of the sums.
  *   cu_nodes    [B+1], total_nodes, max_nodes: a host-side upper bound of the n_b
  *   q_abs       [total_nodes, n_h, d_c+d_r] act dtype (from mla_absorb_q)
  *   cache, block_table, seq_lens, max_seq_len: as for mla_decode; seq_lens[b] in [n_b, max_seq_len]

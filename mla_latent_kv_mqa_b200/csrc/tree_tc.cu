@@ -34,6 +34,8 @@
 // Every wait is bounded (2 s).  On give-up both CTAs' abort flags are set, MLA_ERR_DEVICE_TIMEOUT is
 // recorded, and both CTAs stay until copies and MMAs in flight have had time to land.
 #include <cudaTypedefs.h>
+#include <float.h>
+#include <limits.h>
 #include <math.h>
 
 #include <mutex>
@@ -53,10 +55,21 @@ constexpr int TILE = 128, HALF = 64;              // rows of a tile, and of a CT
 constexpr int STEP = 256, SPG = STEP / PG;        // tokens and pages of a step
 constexpr int CB = PG * 128;                      // 64 rows x 64 bf16 columns, 128-byte swizzle
 constexpr int STAGE = 2 * CB;                     // K: two pages' column block; V: a page's 128 columns
-constexpr int K_STAGES = 4, V_STAGES = 4;
+constexpr int MAX_STAGES = 4;
 constexpr int P_SLOTS = 2;                        // pages of P held at once
-constexpr int Q_OFF = 0, P_OFF = NCB * CB, K_OFF = P_OFF + P_SLOTS * CB, V_OFF = K_OFF + K_STAGES * STAGE;
-constexpr int DATA = V_OFF + V_STAGES * STAGE;
+constexpr int Q_OFF = 0, P_OFF = NCB * CB, K_OFF = P_OFF + P_SLOTS * CB;
+constexpr int RAW = 8192, RAW_STAGES = 2;         // FP8: the codes of a stage, before their conversion
+// Shared memory and tensor memory of the bf16 (F8 = false) and FP8 kernels.
+template <bool F8>
+struct Lay {
+    static constexpr int k_stages = F8 ? 3 : 4, v_stages = F8 ? 3 : 4;
+    static constexpr int v_off = K_OFF + k_stages * STAGE;
+    static constexpr int kraw_off = v_off + v_stages * STAGE, vraw_off = kraw_off + RAW_STAGES * RAW;
+    static constexpr int data = F8 ? vraw_off + RAW_STAGES * RAW : kraw_off;
+    static constexpr int s_bufs = F8 ? 1 : 2;     // FP8: content and RoPE scores apart, one buffer of both
+};
+constexpr int DATA = Lay<false>::data;
+static_assert(Lay<true>::data == DATA, "one shared-memory size");
 constexpr int THREADS = 512;
 constexpr int LOAD_K_WARP = 0, LOAD_V_WARP = 1, QK_WARP = 2, PV_WARP = 3, SM_WARP0 = 4, CLEAN_WARP0 = 12;
 constexpr int SM_WARPS = 8, SM_THREADS = 32 * SM_WARPS, CLEAN_THREADS = THREADS - 32 * CLEAN_WARP0;
@@ -65,9 +78,10 @@ constexpr float RESCALE_LOG2 = 8.0f;
 constexpr int BAR_MAX = 1, BAR_CLEAN = 2;
 
 struct __align__(8) Ctrl {
-    uint64_t k_full[K_STAGES], v_full[V_STAGES];    // even CTA: both CTAs' halves have landed (or were cleaned)
-    uint64_t k_empty[K_STAGES], v_empty[V_STAGES];  // each CTA: the MMAs that read the stage are done
-    uint64_t land[V_STAGES];  // each CTA: a V stage that the cleaning warps have to go over has landed
+    uint64_t k_full[MAX_STAGES], v_full[MAX_STAGES];    // even CTA: both CTAs' halves are there (landed, cleaned, converted)
+    uint64_t k_empty[MAX_STAGES], v_empty[MAX_STAGES];  // each CTA: the MMAs that read the stage are done
+    uint64_t land[MAX_STAGES];  // each CTA: a V stage that the cleaning warps have to go over has landed
+    uint64_t kraw_full[RAW_STAGES], kraw_empty[RAW_STAGES], vraw_full[RAW_STAGES], vraw_empty[RAW_STAGES];  // FP8 codes
     uint64_t q_full, q_empty;
     uint64_t s_full[2], s_free[2];
     uint64_t p_full[SPG], p_free[SPG];  // a page of P: written / its MMAs done
@@ -78,6 +92,7 @@ struct __align__(8) Ctrl {
     int w_b, w_tile, w_step, w_n;
     long long scan_u[THREADS / 32];
     int scan_t[THREADS / 32];
+    __align__(16) float scale[SM_WARPS][2][PG];  // FP8: each softmax warp's page's scales, as they are and with 0 for infinities and NaN
     float top[2][SPG][HALF], sum[SPG][HALF];  // by step parity (a thread may be a step behind its partners), page, row
 };
 constexpr int SMEM = 1024 + DATA + (int)((sizeof(Ctrl) + 127) / 128 * 128);
@@ -282,6 +297,28 @@ __device__ __forceinline__ bool named_red_or(bool v, int id, int n) {
     return r != 0;
 }
 
+// Four e4m3 codes (low byte first) to four bf16 values, exactly: sign, exponent and mantissa moved to a
+// bf16's places make 2^-120 times the value (denormals too), which one exact product restores.  Nine
+// instructions for four codes; the hardware's conversions go through fp16 and fp32 at a quarter of the
+// rate.  Returns non-zero if a code is NaN (S.1111.111, which comes out as 480).
+__device__ __forceinline__ uint32_t e4m3x4_to_bf16x4(uint32_t w, uint32_t &lo, uint32_t &hi) {
+    const uint32_t top = ((w >> 4) & 0x07070707u) | (w & 0x80808080u), bot = (w << 4) & 0xf0f0f0f0u;
+    const uint32_t x = __byte_perm(bot, top, 0x5140), y = __byte_perm(bot, top, 0x7362);
+    const __nv_bfloat162 f = __nv_bfloat162(__ushort_as_bfloat16(0x7b80), __ushort_as_bfloat16(0x7b80));  // 2^120
+    const __nv_bfloat162 a = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&x), f);
+    const __nv_bfloat162 b = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&y), f);
+    lo = *reinterpret_cast<const uint32_t *>(&a);
+    hi = *reinterpret_cast<const uint32_t *>(&b);
+    return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+}
+// Two of the four codes w (the low or high ones) again, with NaN (or 0) in the places of `pair` whose code is NaN.
+__device__ __forceinline__ uint32_t e4m3_nan_pair(uint32_t w, int high, uint32_t pair, bool nan) {
+    const uint32_t hit = ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+    uint32_t m;  // each hit byte's sign, spread over its place
+    asm("prmt.b32 %0, %1, %1, %2;" : "=r"(m) : "r"(hit), "r"(high ? 0xbbaau : 0x9988u));
+    return (pair & ~m) | (nan ? m & 0x7fff7fffu : 0u);
+}
+
 // Which of the 32 tokens j .. j + 31 a node sees: all before ctx, its mask's bits from there, none behind L.
 __device__ __forceinline__ uint32_t sees32(const uint32_t *mask, int words, int j, int ctx, int L) {
     const int rem = L - j, k = j - ctx;
@@ -297,10 +334,15 @@ __device__ __forceinline__ uint32_t sees32(const uint32_t *mask, int words, int 
     return rem < 32 ? v & (0xffffffffu >> (32 - rem)) : v;
 }
 
+// tm_k, tm_v: column blocks of the bf16 cache; FP8: tm_k the RoPE keys, tm_v a page's codes as boxes of 128
+// columns, tm_c as boxes of 64 (unused in the bf16 kernel).
+template <bool F8>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-               const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ TreeArgs a,
-               const __grid_constant__ TreePlan pl) {
+               const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_c,
+               const __grid_constant__ TreeArgs a, const __grid_constant__ TreePlan pl) {
+    constexpr int K_STAGES = Lay<F8>::k_stages, V_STAGES = Lay<F8>::v_stages, V_OFF = Lay<F8>::v_off;
+    constexpr int S_BUFS = Lay<F8>::s_bufs;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_s = smem_u32(smem_raw), data_s = (raw_s + 1023u) & ~1023u;
     Ctrl *ctrl = reinterpret_cast<Ctrl *>(smem_raw + (data_s - raw_s) + DATA);
@@ -311,14 +353,18 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     const int pair = blockIdx.x >> 1, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < K_STAGES; ++i) {
+        for (int i = 0; i < MAX_STAGES; ++i) {
             mbar_init(bar(ctrl->k_full[i]), 2);
             mbar_init(bar(ctrl->k_empty[i]), 1);
-        }
-        for (int i = 0; i < V_STAGES; ++i) {
             mbar_init(bar(ctrl->v_full[i]), 2);
             mbar_init(bar(ctrl->v_empty[i]), 1);
             mbar_init(bar(ctrl->land[i]), 1);
+        }
+        for (int i = 0; i < RAW_STAGES; ++i) {
+            mbar_init(bar(ctrl->kraw_full[i]), 1);
+            mbar_init(bar(ctrl->kraw_empty[i]), 1);
+            mbar_init(bar(ctrl->vraw_full[i]), 1);
+            mbar_init(bar(ctrl->vraw_empty[i]), 1);
         }
         mbar_init(bar(ctrl->q_full), 2);
         mbar_init(bar(ctrl->q_empty), 1);
@@ -360,7 +406,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         Ring st{0, 0};
         uint32_t q_ph = 1;
         bool ok = true;
-        int ids[SPG];
+        int ids[SPG], raw = 0;  // FP8: code stages sent so far
         auto pages = [&]() {
 #pragma unroll
             for (int p = 0; p < SPG; ++p) {
@@ -380,6 +426,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             prefetch_tensormap(&tm_q);
             prefetch_tensormap(&tm_k);
             prefetch_tensormap(&tm_v);
+            if (F8) prefetch_tensormap(&tm_c);
             pages();
         }
         while (ok && kw && !it.done()) {  // Q per segment; K: the CTA's two pages, a column block a stage
@@ -393,12 +440,23 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             const int p0 = rank ? ids[2] : ids[0], p1 = rank ? ids[3] : ids[1];
             it.next(a);
             pages();  // of the next step: the table's latency passes under this one's loads
-            for (int cb = 0; cb < NCB; ++cb) {
+            if (F8) {  // the codes go to the converting warps, eight blocks; the RoPE keys are operands as they are
+                for (int cb = 0; ok && cb < NCB - 1; ++cb) {
+                    if (!(ok = wait(bar(ctrl->kraw_empty[raw & 1]), ((raw >> 1) & 1) ^ 1, abort_flag))) break;
+                    const uint32_t dst = data_s + Lay<F8>::kraw_off + (raw & 1) * RAW, land = bar(ctrl->kraw_full[raw & 1]);
+                    mbar_arrive_expect_tx(land, ((p0 >= 0) + (p1 >= 0)) * (RAW / 2));
+                    if (p0 >= 0) tma_load_2d(dst, &tm_c, cb * 64, p0 * PG, land);
+                    if (p1 >= 0) tma_load_2d(dst + RAW / 2, &tm_c, cb * 64, p1 * PG, land);
+                    ++raw;
+                    st.adv(K_STAGES);
+                }
+            }
+            for (int cb = F8 ? NCB - 1 : 0; ok && cb < NCB; ++cb) {
                 if (!(ok = wait(bar(ctrl->k_empty[st.i]), st.ph ^ 1u, abort_flag))) break;
                 const uint32_t dst = data_s + K_OFF + st.i * STAGE, full = lead(ctrl->k_full[st.i]);
                 mbar_arrive_expect_tx_remote(full, (p0 >= 0 ? CB : 0) + (p1 >= 0 ? CB : 0));
-                if (p0 >= 0) tma_load_3d_pair(dst, &tm_k, 0, p0 * PG, cb, full);
-                if (p1 >= 0) tma_load_3d_pair(dst + CB, &tm_k, 0, p1 * PG, cb, full);
+                if (p0 >= 0) tma_load_3d_pair(dst, &tm_k, 0, p0 * PG, F8 ? 0 : cb, full);
+                if (p1 >= 0) tma_load_3d_pair(dst + CB, &tm_k, 0, p1 * PG, F8 ? 0 : cb, full);
                 st.adv(K_STAGES);
             }
         }
@@ -413,6 +471,15 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             for (int p = 0; p < SPG; ++p) {
                 const bool clean = (pg0 + p + 1) * PG > ctx;
                 for (int nh = 0; ok && p < np && nh < 2; ++nh) {
+                    if (F8) {
+                        if (!(ok = wait(bar(ctrl->vraw_empty[raw & 1]), ((raw >> 1) & 1) ^ 1, abort_flag))) break;
+                        const uint32_t land = bar(ctrl->vraw_full[raw & 1]);
+                        mbar_arrive_expect_tx(land, RAW);
+                        tma_load_2d(data_s + Lay<F8>::vraw_off + (raw & 1) * RAW, &tm_v, nh * 256 + (int)rank * 128, id[p] * PG, land);
+                        ++raw;
+                        st.adv(V_STAGES);
+                        continue;
+                    }
                     if (!(ok = wait(bar(ctrl->v_empty[st.i]), st.ph ^ 1u, abort_flag))) break;
                     const uint32_t dst = data_s + V_OFF + st.i * STAGE, full = lead(ctrl->v_full[st.i]);
                     const int z = nh * 4 + (int)rank * 2;
@@ -447,20 +514,22 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         const uint32_t q_lo = sdesc_sw128_lo(data_s + Q_OFF, 16), k_lo = sdesc_sw128_lo(data_s + K_OFF, 16);
         bool ok = true;
         for (int u = 0; ok && !it.done(); ++u) {
-            const int sb = u & 1;
+            const int sb = u % S_BUFS;
             if (it.first) {
                 if (!(ok = wait(bar(ctrl->q_full), q_ph, abort_flag))) break;
                 q_ph ^= 1u;
             }
-            if (!(ok = wait(bar(ctrl->s_free[sb]), ((u >> 1) & 1) ^ 1, abort_flag))) break;
-            const uint32_t d = tmem + S_COL + sb * 128;
+            if (!(ok = wait(bar(ctrl->s_free[sb]), ((u / S_BUFS) & 1) ^ 1, abort_flag))) break;
 #pragma unroll 1
             for (int cb = 0; cb < NCB; ++cb) {
                 if (!(ok = wait(bar(ctrl->k_full[st.i]), st.ph, abort_flag))) break;
                 tc_fence_after();
                 const uint32_t kl = k_lo + st.i * (STAGE >> 4), ql = q_lo + cb * (CB >> 4);
+                const bool rope = F8 && cb == NCB - 1;  // FP8: the RoPE part of the scores apart, it takes no scale
+                const uint32_t d = tmem + S_COL + (F8 ? (rope ? 128 : 0) : sb * 128);
+                const bool acc = cb != 0 && !rope;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) mma_ss_pair(d, ql + 2 * k, kl + 2 * k, HI, idesc, (cb | k) != 0);
+                for (int k = 0; k < 4; ++k) mma_ss_pair(d, ql + 2 * k, kl + 2 * k, HI, idesc, acc || k > 0);
                 mma_commit_pair(bar(ctrl->k_empty[st.i]));
                 st.adv(K_STAGES);
             }
@@ -505,6 +574,62 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             it.next(a);
         }
         if (!ok) fail();
+    } else if (F8 && warp >= CLEAN_WARP0) {  // ================= FP8: codes to bf16 tiles =================
+        // Two warps convert K's stages, two V's (cleaning drafted rows on the way).
+        const bool kw = warp < CLEAN_WARP0 + 2;
+        const int t = (warp & 1) * 32 + lane, id = kw ? BAR_CLEAN : BAR_CLEAN + 1;
+        const int stages = kw ? K_STAGES : V_STAGES;
+        uint64_t *full = kw ? ctrl->k_full : ctrl->v_full, *empty = kw ? ctrl->k_empty : ctrl->v_empty;
+        uint64_t *raw_full = kw ? ctrl->kraw_full : ctrl->vraw_full, *raw_empty = kw ? ctrl->kraw_empty : ctrl->vraw_empty;
+        const uint32_t raw0 = data_s + (kw ? Lay<F8>::kraw_off : Lay<F8>::vraw_off), st0 = data_s + (kw ? K_OFF : V_OFF);
+        Walk it;
+        it.init(a, &ctrl->w_b);
+        Ring st{0, 0};
+        int raw = 0;
+        bool ok = true;
+        while (ok && !it.done()) {
+            const int n = kw ? NCB - 1 : 2 * it.pages();
+            for (int i = 0; i < n; ++i, ++raw, st.adv(stages)) {
+                const bool good = wait(bar(raw_full[raw & 1]), (raw >> 1) & 1, abort_flag) &&
+                                  wait(bar(empty[st.i]), st.ph ^ 1u, abort_flag);
+                if (!(ok = !named_red_or(!good, id, 64))) break;
+                const uint32_t src = raw0 + (raw & 1) * RAW, dst = st0 + st.i * STAGE;
+                const int j0 = (it.step * SPG + (i >> 1)) * PG;             // V: the page's first token
+                const int keep_nan = kw ? INT_MAX : it.s.ctx - j0, keep = kw ? INT_MAX : it.s.L - j0;  // rows before
+#pragma unroll 2
+                for (int k = 0; k < 8; ++k) {  // 16 codes of row `row` of 64: columns 16 c of block (K: page) `b`
+                    const int x = t + 64 * k, c = x & 3, row = (x >> 2) & 63, b = x >> 8;
+                    uint32_t w[4];
+                    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                                 : "r"(src + (kw ? b * (RAW / 2) + row * 64 : row * 128 + b * 64) + c * 16));
+                    uint32_t o[8];
+                    uint32_t nan = 0;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) nan |= e4m3x4_to_bf16x4(w[q], o[2 * q], o[2 * q + 1]);
+                    if (nan) {  // NaN, or 0 in a drafted row of V
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) o[q] = e4m3_nan_pair(w[q >> 1], q & 1, o[q], row < keep_nan);
+                    }
+                    if (row >= keep) {
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) o[q] = 0u;
+                    }
+                    const uint32_t at = dst + b * CB + row * 128;
+                    st_shared_v4(at + (((2 * c) ^ (row & 7)) << 4), o[0], o[1], o[2], o[3]);
+                    st_shared_v4(at + (((2 * c + 1) ^ (row & 7)) << 4), o[4], o[5], o[6], o[7]);
+                }
+                fence_proxy_async_smem();
+                asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory");
+                if (t == 0) {
+                    mbar_arrive_pair(lead(full[st.i]));
+                    mbar_arrive(bar(raw_empty[raw & 1]));
+                }
+            }
+            if (kw) st.adv(stages);  // the RoPE keys' stage, which the loader fills
+            it.next(a);
+        }
+        if (!ok && lane == 0) fail();
     } else if (warp >= CLEAN_WARP0) {  // ================= V rows not seen by all =================
         const int t = threadIdx.x - CLEAN_WARP0 * 32;
         Walk it;
@@ -556,22 +681,64 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         float m = -INFINITY, l = 0.f;
         int before = 0;  // steps so far that had the page pg ^ 2, which shares the slot of P
         bool ok = true, good = true;
+        float sc0 = 0.f, sc1 = 0.f;
+        float(*scales)[PG] = ctrl->scale[warp - SM_WARP0];
+        auto load_scales = [&](const Walk &w) {
+            sc0 = sc1 = 0.f;
+            const int g = w.step * SPG + pg;
+            if (w.done() || g * PG >= w.s.L) return;
+            const int blk = a.bt[(size_t)w.b * a.max_blocks + g];
+            if (blk < 0 || blk >= a.num_blocks) return;  // the loader reports it
+            const float *src = a.kv_scale + (size_t)blk * PG + lane;
+            sc0 = __ldg(src);
+            sc1 = __ldg(src + 32);
+        };
+        if (F8) load_scales(it);
         for (int u = 0; ok && !it.done(); ++u) {
             const int row = it.tile * TILE + (int)rank * HALF + r;  // of the sequence's (node, head) pairs
             const bool mine = row < it.s.n * a.n_h;
-            const int sb = u & 1;
-            good = good && wait(bar(ctrl->s_full[sb]), (u >> 1) & 1, abort_flag);
+            const int sb = u & 1, buf = u % S_BUFS;
+            good = __all_sync(0xffffffffu, good && wait(bar(ctrl->s_full[buf]), (u / S_BUFS) & 1, abort_flag));
             tc_fence_after();
             uint32_t v[PG];
+            if (F8) {
+                scales[0][lane] = sc0;
+                scales[0][lane + 32] = sc1;
+                scales[1][lane] = fabsf(sc0) <= FLT_MAX ? sc0 : 0.f;
+                scales[1][lane + 32] = fabsf(sc1) <= FLT_MAX ? sc1 : 0.f;
+                __syncwarp();
+            }
             if (good) {
+                const uint32_t sa = tmem + lane_base + S_COL + buf * 128 + cg * PG;
+                if (F8) {  // content scores times the tokens' scales, and the RoPE scores
 #pragma unroll
-                for (int c = 0; c < 2; ++c)
-                    tmem_ld32(tmem + lane_base + S_COL + sb * 128 + cg * PG + c * 32,
-                              *reinterpret_cast<uint32_t(*)[32]>(v + 32 * c));
-                tmem_wait_ld();
+                    for (int c = 0; c < PG / 16; ++c) {
+                        uint32_t x[16], y[16];
+                        tmem_ld16(sa + c * 16, x);
+                        tmem_ld16(sa + 128 + c * 16, y);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 16; j += 4) {
+                            const float4 sc = *reinterpret_cast<const float4 *>(&scales[0][16 * c + j]);
+                            v[16 * c + j] = __float_as_uint(fmaf(__uint_as_float(x[j]), sc.x, __uint_as_float(y[j])));
+                            v[16 * c + j + 1] = __float_as_uint(fmaf(__uint_as_float(x[j + 1]), sc.y, __uint_as_float(y[j + 1])));
+                            v[16 * c + j + 2] = __float_as_uint(fmaf(__uint_as_float(x[j + 2]), sc.z, __uint_as_float(y[j + 2])));
+                            v[16 * c + j + 3] = __float_as_uint(fmaf(__uint_as_float(x[j + 3]), sc.w, __uint_as_float(y[j + 3])));
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) tmem_ld32(sa + c * 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32 * c));
+                    tmem_wait_ld();
+                }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_pair(lead(ctrl->s_free[sb]));
+                if (lane == 0) mbar_arrive_pair(lead(ctrl->s_free[buf]));
+            }
+            if (F8) {  // the next step's scales: the table's and their latency pass under this step
+                Walk ahead = it;
+                ahead.next(a);
+                load_scales(ahead);
             }
             const int j0 = it.step * STEP + pg * PG;
             if (j0 + PG > it.s.ctx) {
@@ -611,7 +778,12 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 const float p0 = ex2(fmaf(__uint_as_float(v[2 * j]), a.scale_log2, -base));
                 const float p1 = ex2(fmaf(__uint_as_float(v[2 * j + 1]), a.scale_log2, -base));
                 s[j & 3] += p0 + p1;
-                v[j] = pack_bf16x2(p0, p1);
+                if (F8) {  // the value product is over the codes: their scales go into P
+                    const float2 sc = *reinterpret_cast<const float2 *>(&scales[1][2 * j]);
+                    v[j] = pack_bf16x2(p0 * sc.x, p1 * sc.y);
+                } else {
+                    v[j] = pack_bf16x2(p0, p1);
+                }
             }
             l = l * fac + ((s[0] + s[1]) + (s[2] + s[3]));
             // Every thread waits for every step's MMAs in turn, two steps behind (by then they are done): a wait by
@@ -807,7 +979,8 @@ tree_tc_join_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ 
     }
 }
 
-// Pairs that run at once on the current device (0: it cannot be queried), looked up once.
+// Pairs that run at once on the current device (0: it cannot be queried), looked up once.  Both kernels
+// have the same launch shape and shared memory.
 int tree_pairs() {
     static int known[64];
     static std::mutex mu;
@@ -815,26 +988,29 @@ int tree_pairs() {
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
     std::lock_guard<std::mutex> lk(mu);
     if (known[dev]) return known[dev];
-    if (cudaFuncSetAttribute(tree_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM) != cudaSuccess) return 0;
-    int sms = 148;
+    int sms = 148, most = 0;
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2 * (sms / 2));
-    cfg.blockDim = dim3(THREADS);
-    cfg.dynamicSmemBytes = SMEM;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = 2;
-    attr.val.clusterDim.y = 1;
-    attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, tree_tc_kernel, &cfg) != cudaSuccess || n < 1) {
-        cudaGetLastError();
-        n = sms / 2;
+    for (auto kern : {tree_tc_kernel<false>, tree_tc_kernel<true>}) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM) != cudaSuccess) return 0;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(2 * (sms / 2));
+        cfg.blockDim = dim3(THREADS);
+        cfg.dynamicSmemBytes = SMEM;
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = 2;
+        attr.val.clusterDim.y = 1;
+        attr.val.clusterDim.z = 1;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        int n = 0;
+        if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) {
+            cudaGetLastError();
+            n = sms / 2;
+        }
+        if (most == 0 || n < most) most = n;
     }
-    return known[dev] = n;
+    return known[dev] = most;
 }
 
 size_t tree_tc_layout(int pairs, int B, char *base, TreePlan *pl) {
@@ -859,7 +1035,7 @@ size_t tree_tc_layout(int pairs, int B, char *base, TreePlan *pl) {
 
 bool tree_tc_supported(const mla_dims_t &d) {
     return d.d_c == DC && d.d_r == ROW - DC && d.page_size == PG && d.act_dtype == MLA_DTYPE_BF16 &&
-           d.kv_dtype == MLA_DTYPE_BF16 && !(d.flags & MLA_FLAG_SIMT_DECODE);
+           (d.kv_dtype == MLA_DTYPE_BF16 || d.kv_dtype == MLA_DTYPE_FP8_E4M3) && !(d.flags & MLA_FLAG_SIMT_DECODE);
 }
 
 size_t tree_tc_workspace_bytes(int B) {
@@ -873,11 +1049,15 @@ cudaError_t launch_tree_tc(const mla_dims_t &d, const TreeArgs &a, void *ws, cud
     TreePlan pl;
     tree_tc_layout(pairs, a.B, reinterpret_cast<char *>(ws), &pl);
     const uint64_t pool_rows = (uint64_t)a.num_blocks * PG, q_rows = (uint64_t)a.T * a.n_h;
-    CUtensorMap tm_q, tm_k, tm_v;
-    if (!tmap_bf16_colblocks(&tm_q, a.q_abs, q_rows, ROW, ROW * 2, HALF, NCB) ||
-        !tmap_bf16_colblocks(&tm_k, a.kv_pool, pool_rows, ROW, ROW * 2, PG, 1) ||
-        !tmap_bf16_colblocks(&tm_v, a.kv_pool, pool_rows, ROW, ROW * 2, PG, 2))
-        return cudaErrorInvalidValue;
+    const bool f8 = d.kv_dtype == MLA_DTYPE_FP8_E4M3;
+    CUtensorMap tm_q, tm_k, tm_v, tm_c;
+    const bool maps = f8 ? tmap_bf16_colblocks(&tm_k, a.kr_pool, pool_rows, ROW - DC, (ROW - DC) * 2, PG, 1) &&
+                               tmap_u8_rows(&tm_v, a.kv_pool, DC, pool_rows, DC, 128, PG) &&
+                               tmap_u8_rows(&tm_c, a.kv_pool, DC, pool_rows, DC, 64, PG)
+                         : tmap_bf16_colblocks(&tm_k, a.kv_pool, pool_rows, ROW, ROW * 2, PG, 1) &&
+                               tmap_bf16_colblocks(&tm_v, a.kv_pool, pool_rows, ROW, ROW * 2, PG, 2);
+    if (!maps || !tmap_bf16_colblocks(&tm_q, a.q_abs, q_rows, ROW, ROW * 2, HALF, NCB)) return cudaErrorInvalidValue;
+    if (!f8) tm_c = tm_v;
     cudaLaunchAttribute pdl;
     pdl.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     pdl.val.programmaticStreamSerializationAllowed = 1;
@@ -888,7 +1068,8 @@ cudaError_t launch_tree_tc(const mla_dims_t &d, const TreeArgs &a, void *ws, cud
     cfg.stream = st;
     cfg.attrs = &pdl;
     cfg.numAttrs = 1;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, tree_tc_kernel, tm_q, tm_k, tm_v, a, pl);
+    cudaError_t e = f8 ? cudaLaunchKernelEx(&cfg, tree_tc_kernel<true>, tm_q, tm_k, tm_v, tm_c, a, pl)
+                       : cudaLaunchKernelEx(&cfg, tree_tc_kernel<false>, tm_q, tm_k, tm_v, tm_c, a, pl);
     if (e != cudaSuccess) return e;
     const int64_t tiles = a.B + q_rows / TILE;  // at most: a sequence's last tile may be part-filled
     cfg.gridDim = dim3((unsigned)tiles, TILE / JOIN_ROWS);

@@ -434,3 +434,28 @@ def test_other_streams_and_a_captured_step():
     torch.cuda.synchronize()
     b.q, b.ctx = q, np.array([84, 640, 31])
     b.check((o, lse))
+
+
+@pytest.mark.parametrize("flags", [0, 1])
+def test_every_fp8_code(flags):
+    """All 256 codes, denormals among them, exactly; a NaN code reaches who sees it."""
+    b = Batch([250], [6], kv="fp8", flags=flags, heads=24, seed=31)
+    codes = torch.arange(256, device="cuda", dtype=torch.uint8)
+    codes[(codes & 0x7F) == 0x7F] = 0
+    rows = torch.stack([codes.roll(7 * i) for i in range(256)])
+    j = torch.arange(256, device="cuda")
+    b.cache.kv_pool[b.owned[0][j // 64], j % 64] = torch.cat([rows, rows.flip(1)], 1)
+    b.cache.kv_scale[b.owned[0][j // 64], j % 64] = torch.rand(256, device="cuda") * 0.02 + 1e-4
+    b.check(b.decode())
+    b.cache.kv_pool[b.owned[0][0], 5, 77] = 0xFF
+    o, lse = b.decode()
+    assert torch.isnan(o).all() and torch.isnan(lse).all()
+    b.cache.kv_pool[b.owned[0][0], 5, 77] = 3
+    for bad in (float("nan"), float("inf")):
+        b.cache.kv_scale[b.owned[0][252 // 64], 252 % 64] = bad          # node 2: its descendants alone
+        o, lse = b.decode()
+        sees = torch.from_numpy(b.see[0][:, 2]).cuda()
+        assert torch.isfinite(o[~sees]).all()
+        # an infinite scale makes the score +inf or -inf, by the sign of q . code: weight NaN, or 0 and no part of o
+        assert not torch.isfinite(lse[sees]).any() if bad != bad else not torch.isfinite(lse[sees]).all()
+    no_error()
