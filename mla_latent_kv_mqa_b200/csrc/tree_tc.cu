@@ -70,9 +70,11 @@ struct Lay {
 };
 constexpr int DATA = Lay<false>::data;
 static_assert(Lay<true>::data == DATA, "one shared-memory size");
-constexpr int THREADS = 512;
+template <bool F8>
+constexpr int THREADS = F8 ? 640 : 512;
+constexpr int MAX_WARPS = 20;
 constexpr int LOAD_K_WARP = 0, LOAD_V_WARP = 1, QK_WARP = 2, PV_WARP = 3, SM_WARP0 = 4, CLEAN_WARP0 = 12;
-constexpr int SM_WARPS = 8, SM_THREADS = 32 * SM_WARPS, CLEAN_THREADS = THREADS - 32 * CLEAN_WARP0;
+constexpr int SM_WARPS = 8, SM_THREADS = 32 * SM_WARPS, CLEAN_THREADS = 128;  // FP8: two such groups, for K and for V
 constexpr uint32_t S_COL = 0, O_COL = 256, TMEM_COLS = 512;
 constexpr float RESCALE_LOG2 = 8.0f;
 constexpr int BAR_MAX = 1, BAR_CLEAN = 2;
@@ -90,8 +92,8 @@ struct __align__(8) Ctrl {
     uint64_t o_ok[2], pv_done[2];
     uint32_t tmem_base, abort;
     int w_b, w_tile, w_step, w_n;
-    long long scan_u[THREADS / 32];
-    int scan_t[THREADS / 32];
+    long long scan_u[MAX_WARPS];
+    int scan_t[MAX_WARPS];
     __align__(16) float scale[SM_WARPS][2][PG];  // FP8: each softmax warp's page's scales, as they are and with 0 for infinities and NaN
     float top[2][SPG][HALF], sum[SPG][HALF];  // by step parity (a thread may be a step behind its partners), page, row
 };
@@ -185,6 +187,7 @@ __device__ __forceinline__ int pair_of_unit(long long u, long long U, int pairs)
 
 // The pair's run: every CTA scans the batch's tiles and units (two passes where the batch is larger than
 // the block); pair 0 also leaves the offsets for the join.  One sequence that is no tree refuses all.
+template <int THREADS>
 __device__ __noinline__ void schedule(const TreeArgs &a, const TreePlan &pl, int pair, uint32_t rank, Ctrl *c) {
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     auto block_scan = [&](long long &u, int &t, long long &all_u, int &all_t) {  // inclusive
@@ -337,7 +340,7 @@ __device__ __forceinline__ uint32_t sees32(const uint32_t *mask, int words, int 
 // tm_k, tm_v: column blocks of the bf16 cache; FP8: tm_k the RoPE keys, tm_v a page's codes as boxes of 128
 // columns, tm_c as boxes of 64 (unused in the bf16 kernel).
 template <bool F8>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS<F8>, 1)
 tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_c,
                const __grid_constant__ TreeArgs a, const __grid_constant__ TreePlan pl) {
@@ -391,7 +394,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     tc_fence_after();
     pdl_trigger();
     pdl_wait();  // inputs are read from here on
-    schedule(a, pl, pair, rank, ctrl);
+    schedule<THREADS<F8>>(a, pl, pair, rank, ctrl);
     const uint32_t tmem = ctrl->tmem_base;
     auto fail = [&]() {
         *abort_flag = 1;
@@ -575,9 +578,9 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         }
         if (!ok) fail();
     } else if (F8 && warp >= CLEAN_WARP0) {  // ================= FP8: codes to bf16 tiles =================
-        // Two warps convert K's stages, two V's (cleaning drafted rows on the way).
-        const bool kw = warp < CLEAN_WARP0 + 2;
-        const int t = (warp & 1) * 32 + lane, id = kw ? BAR_CLEAN : BAR_CLEAN + 1;
+        // Four warps convert K's stages, four V's (cleaning drafted rows on the way).
+        const bool kw = warp < CLEAN_WARP0 + 4;
+        const int t = (warp & 3) * 32 + lane, id = kw ? BAR_CLEAN : BAR_CLEAN + 1;
         const int stages = kw ? K_STAGES : V_STAGES;
         uint64_t *full = kw ? ctrl->k_full : ctrl->v_full, *empty = kw ? ctrl->k_empty : ctrl->v_empty;
         uint64_t *raw_full = kw ? ctrl->kraw_full : ctrl->vraw_full, *raw_empty = kw ? ctrl->kraw_empty : ctrl->vraw_empty;
@@ -592,35 +595,40 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             for (int i = 0; i < n; ++i, ++raw, st.adv(stages)) {
                 const bool good = wait(bar(raw_full[raw & 1]), (raw >> 1) & 1, abort_flag) &&
                                   wait(bar(empty[st.i]), st.ph ^ 1u, abort_flag);
-                if (!(ok = !named_red_or(!good, id, 64))) break;
                 const uint32_t src = raw0 + (raw & 1) * RAW, dst = st0 + st.i * STAGE;
                 const int j0 = (it.step * SPG + (i >> 1)) * PG;             // V: the page's first token
                 const int keep_nan = kw ? INT_MAX : it.s.ctx - j0, keep = kw ? INT_MAX : it.s.L - j0;  // rows before
-#pragma unroll 2
-                for (int k = 0; k < 8; ++k) {  // 16 codes of row `row` of 64: columns 16 c of block (K: page) `b`
-                    const int x = t + 64 * k, c = x & 3, row = (x >> 2) & 63, b = x >> 8;
-                    uint32_t w[4];
-                    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                                 : "r"(src + (kw ? b * (RAW / 2) + row * 64 : row * 128 + b * 64) + c * 16));
-                    uint32_t o[8];
-                    uint32_t nan = 0;
+                // A thread takes four chunks of 16 codes, columns 16 c of two rows of two blocks; its loads come before
+                // its stores, each of which would hold the next load back.
+                const int c = t & 3, row0 = t >> 2;
+                const uint32_t src_t = src + row0 * (kw ? 64 : 128) + c * 16;
+                const uint32_t dst0 = dst + row0 * 128 + (((2 * c) ^ (row0 & 7)) << 4), dst1 = dst + row0 * 128 + (((2 * c + 1) ^ (row0 & 7)) << 4);
+                const bool tail = keep < PG;
+                uint32_t w[4][4];
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) nan |= e4m3x4_to_bf16x4(w[q], o[2 * q], o[2 * q + 1]);
+                for (int k = 0; k < 4; ++k)  // block (K: page) k / 2, rows row0 and row0 + 32
+                    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                 : "=r"(w[k][0]), "=r"(w[k][1]), "=r"(w[k][2]), "=r"(w[k][3])
+                                 : "r"(src_t + (kw ? (k >> 1) * (RAW / 2) + (k & 1) * 2048 : (k >> 1) * 64 + (k & 1) * 4096)));
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int row = row0 + 32 * (k & 1);
+                    uint32_t o[8], nan = 0;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) nan |= e4m3x4_to_bf16x4(w[k][q], o[2 * q], o[2 * q + 1]);
                     if (nan) {  // NaN, or 0 in a drafted row of V
 #pragma unroll
-                        for (int q = 0; q < 8; ++q) o[q] = e4m3_nan_pair(w[q >> 1], q & 1, o[q], row < keep_nan);
+                        for (int q = 0; q < 8; ++q) o[q] = e4m3_nan_pair(w[k][q >> 1], q & 1, o[q], row < keep_nan);
                     }
-                    if (row >= keep) {
+                    if (tail && row >= keep) {
 #pragma unroll
                         for (int q = 0; q < 8; ++q) o[q] = 0u;
                     }
-                    const uint32_t at = dst + b * CB + row * 128;
-                    st_shared_v4(at + (((2 * c) ^ (row & 7)) << 4), o[0], o[1], o[2], o[3]);
-                    st_shared_v4(at + (((2 * c + 1) ^ (row & 7)) << 4), o[4], o[5], o[6], o[7]);
+                    st_shared_v4(dst0 + (k >> 1) * CB + (k & 1) * 4096, o[0], o[1], o[2], o[3]);
+                    st_shared_v4(dst1 + (k >> 1) * CB + (k & 1) * 4096, o[4], o[5], o[6], o[7]);
                 }
                 fence_proxy_async_smem();
-                asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory");
+                if (!(ok = !named_red_or(!good, id, CLEAN_THREADS))) break;
                 if (t == 0) {
                     mbar_arrive_pair(lead(full[st.i]));
                     mbar_arrive(bar(raw_empty[raw & 1]));
@@ -712,18 +720,18 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 const uint32_t sa = tmem + lane_base + S_COL + buf * 128 + cg * PG;
                 if (F8) {  // content scores times the tokens' scales, and the RoPE scores
 #pragma unroll
-                    for (int c = 0; c < PG / 16; ++c) {
-                        uint32_t x[16], y[16];
-                        tmem_ld16(sa + c * 16, x);
-                        tmem_ld16(sa + 128 + c * 16, y);
+                    for (int c = 0; c < PG / 8; ++c) {
+                        uint32_t x[8], y[8];
+                        tmem_ld8(sa + c * 8, x);
+                        tmem_ld8(sa + 128 + c * 8, y);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int j = 0; j < 16; j += 4) {
-                            const float4 sc = *reinterpret_cast<const float4 *>(&scales[0][16 * c + j]);
-                            v[16 * c + j] = __float_as_uint(fmaf(__uint_as_float(x[j]), sc.x, __uint_as_float(y[j])));
-                            v[16 * c + j + 1] = __float_as_uint(fmaf(__uint_as_float(x[j + 1]), sc.y, __uint_as_float(y[j + 1])));
-                            v[16 * c + j + 2] = __float_as_uint(fmaf(__uint_as_float(x[j + 2]), sc.z, __uint_as_float(y[j + 2])));
-                            v[16 * c + j + 3] = __float_as_uint(fmaf(__uint_as_float(x[j + 3]), sc.w, __uint_as_float(y[j + 3])));
+                        for (int j = 0; j < 8; j += 4) {
+                            const float4 sc = *reinterpret_cast<const float4 *>(&scales[0][8 * c + j]);
+                            v[8 * c + j] = __float_as_uint(fmaf(__uint_as_float(x[j]), sc.x, __uint_as_float(y[j])));
+                            v[8 * c + j + 1] = __float_as_uint(fmaf(__uint_as_float(x[j + 1]), sc.y, __uint_as_float(y[j + 1])));
+                            v[8 * c + j + 2] = __float_as_uint(fmaf(__uint_as_float(x[j + 2]), sc.z, __uint_as_float(y[j + 2])));
+                            v[8 * c + j + 3] = __float_as_uint(fmaf(__uint_as_float(x[j + 3]), sc.w, __uint_as_float(y[j + 3])));
                         }
                     }
                 } else {
@@ -994,7 +1002,7 @@ int tree_pairs() {
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM) != cudaSuccess) return 0;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(2 * (sms / 2));
-        cfg.blockDim = dim3(THREADS);
+        cfg.blockDim = dim3(kern == tree_tc_kernel<true> ? THREADS<true> : THREADS<false>);
         cfg.dynamicSmemBytes = SMEM;
         cudaLaunchAttribute attr;
         attr.id = cudaLaunchAttributeClusterDimension;
@@ -1063,7 +1071,7 @@ cudaError_t launch_tree_tc(const mla_dims_t &d, const TreeArgs &a, void *ws, cud
     pdl.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * pairs);
-    cfg.blockDim = dim3(THREADS);
+    cfg.blockDim = dim3(f8 ? THREADS<true> : THREADS<false>);
     cfg.dynamicSmemBytes = SMEM;
     cfg.stream = st;
     cfg.attrs = &pdl;
