@@ -156,8 +156,9 @@ cache_keep_kernel(const __grid_constant__ KeepArgs a, const __grid_constant__ Po
 // Any dims and cache type, and the cross-check of the tensor-core kernel.  A block takes one node, 8
 // of its heads (a warp each) and one segment of its tokens; the online softmax runs in log2 units.
 // A masked token's value is never multiplied: its weight is skipped, not zero, so that what a
-// sibling's row holds cannot reach this node.
-constexpr int kHeads = 8, kTile = 32, kMaxCols = 32;  // d_c <= 1024
+// sibling's row holds cannot reach this node.  NC: columns of o a lane holds; the smallest of 4, 16 and 32
+// that covers d_c (with 32 for all, the toy layer's 4 columns cost a loop of 32: 28 us a call, now 13).
+constexpr int kHeads = 8, kTile = 32;
 
 template <int KV>  // 0 = f32 pool, 1 = bf16 pool, 2 = fp8 content pool + bf16 RoPE pool
 __device__ __forceinline__ float load_cache(const TreeArgs &a, size_t slot, int k) {
@@ -171,7 +172,7 @@ __device__ __forceinline__ float load_cache(const TreeArgs &a, size_t slot, int 
     return __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(a.kr_pool)[slot * d_r + (k - d_c)]);
 }
 
-template <typename Ta, int KV>
+template <typename Ta, int KV, int NC>
 __global__ void __launch_bounds__(kHeads * 32)
 tree_simt_kernel(const __grid_constant__ TreeArgs a, int seg_len, int n_split, TreePartials part) {
     extern __shared__ float smem[];
@@ -193,27 +194,25 @@ tree_simt_kernel(const __grid_constant__ TreeArgs a, int seg_len, int n_split, T
     const size_t pr = ((size_t)split * a.T + t) * a.n_h + h;  // this warp's partial row
     const uint32_t *mask = a.mask + (size_t)t * a.mask_words;
 
-    for (int i = threadIdx.x; i < kHeads * row; i += blockDim.x) {
-        const int g = i / row, k = i % row;
-        q_s[i] = h0 + g < a.n_h ? to_f32(reinterpret_cast<const Ta *>(a.q_abs)[((size_t)t * a.n_h + h0 + g) * row + k]) : 0.f;
-    }
-    float o[kMaxCols];
+    for (int k = lane; k < row; k += 32)
+        q_s[warp * row + k] = h < a.n_h ? to_f32(reinterpret_cast<const Ta *>(a.q_abs)[((size_t)t * a.n_h + h) * row + k]) : 0.f;
+    float o[NC];
 #pragma unroll
-    for (int q = 0; q < kMaxCols; ++q) o[q] = 0.f;
+    for (int q = 0; q < NC; ++q) o[q] = 0.f;
     float m = -INFINITY, l = 0.f;
     for (int j0 = j_begin; j0 < j_end; j0 += kTile) {
         __syncthreads();
-        for (int i = threadIdx.x; i < kTile * row; i += blockDim.x) {
-            const int jj = i / row, k = i % row, j = j0 + jj;
-            float v = 0.f;
+#pragma unroll
+        for (int i = 0; i < kTile / kHeads; ++i) {  // a warp's four tokens
+            const int jj = warp + i * kHeads, j = j0 + jj;
+            int blk = -1;
             if (j < j_end) {
-                const int blk = a.bt[(size_t)b * a.max_blocks + j / a.page];
-                if (blk >= 0 && blk < a.num_blocks)
-                    v = load_cache<KV>(a, (size_t)blk * a.page + j % a.page, k);
-                else if (k == 0)
-                    record_error(a.err, kErrBadBlock);
+                blk = a.bt[(size_t)b * a.max_blocks + j / a.page];
+                if ((blk < 0 || blk >= a.num_blocks) && lane == 0) record_error(a.err, kErrBadBlock);
             }
-            kv_s[jj * kv_stride + k] = v;
+            const bool have = blk >= 0 && blk < a.num_blocks;
+            const size_t slot = (size_t)blk * a.page + j % a.page;
+            for (int k = lane; k < row; k += 32) kv_s[jj * kv_stride + k] = have ? load_cache<KV>(a, slot, k) : 0.f;
         }
         __syncthreads();
         if (h >= a.n_h) continue;
@@ -234,19 +233,19 @@ tree_simt_kernel(const __grid_constant__ TreeArgs a, int seg_len, int n_split, T
         l = l * corr + ps;
         m = m_new;
 #pragma unroll
-        for (int q = 0; q < kMaxCols; ++q) o[q] *= corr;
+        for (int q = 0; q < NC; ++q) o[q] *= corr;
         for (int jj = 0; jj < kTile; ++jj) {
             const float pj = __shfl_sync(0xffffffffu, p, jj);
             if (pj == 0.f) continue;
             const float *kvr = kv_s + jj * kv_stride;
 #pragma unroll
-            for (int q = 0; q < kMaxCols; ++q)
+            for (int q = 0; q < NC; ++q)
                 if (lane + 32 * q < a.d_c) o[q] = fmaf(pj, kvr[lane + 32 * q], o[q]);
         }
     }
     if (h >= a.n_h) return;
 #pragma unroll
-    for (int q = 0; q < kMaxCols; ++q)
+    for (int q = 0; q < NC; ++q)
         if (lane + 32 * q < a.d_c) part.o[pr * a.d_c + lane + 32 * q] = o[q];
     if (lane == 0) {
         part.m[pr] = m;
@@ -327,14 +326,21 @@ cudaError_t launch_tree_simt(const mla_dims_t &d, const TreeArgs &a, void *ws, c
             e = cudaGetLastError();
         }
     };
+#define MLA_TREE_SIMT(TA, KV)                                           \
+    do {                                                                \
+        if (d.d_c <= 128) run(tree_simt_kernel<TA, KV, 4>);             \
+        else if (d.d_c <= 512) run(tree_simt_kernel<TA, KV, 16>);       \
+        else run(tree_simt_kernel<TA, KV, 32>);                         \
+    } while (0)
     const bool ab = d.act_dtype == MLA_DTYPE_BF16;
     if (d.kv_dtype == MLA_DTYPE_F32) {
-        if (ab) run(tree_simt_kernel<__nv_bfloat16, 0>); else run(tree_simt_kernel<float, 0>);
+        if (ab) MLA_TREE_SIMT(__nv_bfloat16, 0); else MLA_TREE_SIMT(float, 0);
     } else if (d.kv_dtype == MLA_DTYPE_BF16) {
-        if (ab) run(tree_simt_kernel<__nv_bfloat16, 1>); else run(tree_simt_kernel<float, 1>);
+        if (ab) MLA_TREE_SIMT(__nv_bfloat16, 1); else MLA_TREE_SIMT(float, 1);
     } else {
-        if (ab) run(tree_simt_kernel<__nv_bfloat16, 2>); else run(tree_simt_kernel<float, 2>);
+        if (ab) MLA_TREE_SIMT(__nv_bfloat16, 2); else MLA_TREE_SIMT(float, 2);
     }
+#undef MLA_TREE_SIMT
     if (e != cudaSuccess) return e;
     const dim3 jg(a.T, d.n_h);
     if (a.out_bf16) tree_join_kernel<__nv_bfloat16><<<jg, kJoinThreads, 0, st>>>(a, pl.n_split, part);

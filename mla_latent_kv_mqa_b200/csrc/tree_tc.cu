@@ -79,7 +79,7 @@ constexpr uint32_t S_COL = 0, O_COL = 256, TMEM_COLS = 512;
 constexpr float RESCALE_LOG2 = 8.0f;
 constexpr int BAR_MAX = 1, BAR_CLEAN = 2;
 
-struct __align__(8) Ctrl {
+struct __align__(16) Ctrl {
     uint64_t k_full[MAX_STAGES], v_full[MAX_STAGES];    // even CTA: both CTAs' halves are there (landed, cleaned, converted)
     uint64_t k_empty[MAX_STAGES], v_empty[MAX_STAGES];  // each CTA: the MMAs that read the stage are done
     uint64_t land[MAX_STAGES];  // each CTA: a V stage that the cleaning warps have to go over has landed
@@ -94,7 +94,7 @@ struct __align__(8) Ctrl {
     int w_b, w_tile, w_step, w_n;
     long long scan_u[MAX_WARPS];
     int scan_t[MAX_WARPS];
-    __align__(16) float scale[SM_WARPS][2][PG];  // FP8: each softmax warp's page's scales, as they are and with 0 for infinities and NaN
+    alignas(16) float scale[SM_WARPS][2][PG];  // FP8: each softmax warp's page's scales, as they are and with 0 for infinities and NaN
     float top[2][SPG][HALF], sum[SPG][HALF];  // by step parity (a thread may be a step behind its partners), page, row
 };
 constexpr int SMEM = 1024 + DATA + (int)((sizeof(Ctrl) + 127) / 128 * 128);
@@ -909,8 +909,9 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
 }
 
 // Joins the tiles that lie in several pairs' runs: o = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s, a warp
-// per row.  Rows of a sequence without steps (a bad length) are 0 and -inf.
-constexpr int JOIN_ROWS = 8;
+// per row.  The lanes find the row's slots and weights side by side, so that the partial rows are read
+// without waiting for one another.  Rows of a sequence without steps (a bad length) are 0 and -inf.
+constexpr int JOIN_ROWS = 8, JOIN_MAX = 4;  // slots a lane; up to 128 pairs
 __global__ void __launch_bounds__(JOIN_ROWS * 32)
 tree_tc_join_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ TreePlan pl) {
     pdl_wait();
@@ -932,34 +933,47 @@ tree_tc_join_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ 
         c1 = pair_of_unit(u0 + s.steps - 1, U, pl.pairs);
         if (c0 == c1) return;
     }
-    auto slot_of = [&](int c) {  // -1: the pair has no units
-        if (unit_start(c, U, pl.pairs) == unit_start(c + 1, U, pl.pairs)) return -1;
-        return 2 * c + (c == c0 && unit_start(c0, U, pl.pairs) != u0 ? 1 : 0);
-    };
-    float M = -INFINITY;
-    for (int c = c0; c <= c1; ++c) {
-        const int sl = slot_of(c);
-        if (sl >= 0) M = fmaxf(M, pl.m[sl * TILE + rr]);
+    const bool behind = s.steps > 0 && unit_start(c0, U, pl.pairs) != u0;  // the tile is not its first pair's first
+    const int n = c1 - c0 + 1;
+    float m[JOIN_MAX], l = 0.f, M = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < JOIN_MAX; ++k) {
+        const int i = k * 32 + lane, c = c0 + i;
+        m[k] = -INFINITY;
+        if (i < n && unit_start(c, U, pl.pairs) != unit_start(c + 1, U, pl.pairs))  // a pair without units left nothing
+            m[k] = pl.m[(2 * c + (i == 0 && behind)) * TILE + rr];
+        M = fmaxf(M, m[k]);
     }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
     const float base = M == -INFINITY ? 0.f : M;
-    float l = 0.f, acc[16];
+#pragma unroll
+    for (int k = 0; k < JOIN_MAX; ++k) {
+        const int i = k * 32 + lane;
+        m[k] = exp2f(m[k] - base);  // the slot's weight
+        if (m[k] != 0.f) l += m[k] * pl.l[(2 * (c0 + i) + (i == 0 && behind)) * TILE + rr];
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    float acc[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) acc[i] = 0.f;
-    for (int c = c0; c <= c1; ++c) {
-        const int sl = slot_of(c);
-        if (sl < 0) continue;
-        const float ms = pl.m[sl * TILE + rr], ls = pl.l[sl * TILE + rr];
-        const float w = exp2f(ms - base);
-        l += w * ls;
-        if (w == 0.f) continue;
-        const float4 *src = reinterpret_cast<const float4 *>(pl.o + ((size_t)sl * TILE + rr) * DC);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float4 x = src[i * 32 + lane];
-            acc[4 * i] = fmaf(w, x.x, acc[4 * i]);
-            acc[4 * i + 1] = fmaf(w, x.y, acc[4 * i + 1]);
-            acc[4 * i + 2] = fmaf(w, x.z, acc[4 * i + 2]);
-            acc[4 * i + 3] = fmaf(w, x.w, acc[4 * i + 3]);
+    for (int k = 0; k < JOIN_MAX; ++k) {
+#pragma unroll 2
+        for (int i = 0; i < 32 && k * 32 + i < n; ++i) {
+            const float w = __shfl_sync(0xffffffffu, m[k], i);
+            if (w == 0.f) continue;
+            const int sl = 2 * (c0 + k * 32 + i) + (k == 0 && i == 0 && behind);
+            const float4 *src = reinterpret_cast<const float4 *>(pl.o + ((size_t)sl * TILE + rr) * DC);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const float4 x = src[q * 32 + lane];
+                acc[4 * q] = fmaf(w, x.x, acc[4 * q]);
+                acc[4 * q + 1] = fmaf(w, x.y, acc[4 * q + 1]);
+                acc[4 * q + 2] = fmaf(w, x.z, acc[4 * q + 2]);
+                acc[4 * q + 3] = fmaf(w, x.w, acc[4 * q + 3]);
+            }
         }
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -1008,7 +1022,7 @@ int tree_pairs() {
         }
         if (most == 0 || n < most) most = n;
     }
-    return known[dev] = most;
+    return known[dev] = most < 32 * JOIN_MAX ? most : 32 * JOIN_MAX;
 }
 
 size_t tree_tc_layout(int pairs, int B, char *base, TreePlan *pl) {

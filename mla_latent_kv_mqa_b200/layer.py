@@ -72,6 +72,14 @@ class PagedLatentCache:
         self.kv_pool, self.kr_pool, self.kv_scale = kv_pool, kr_pool, kv_scale
         return self
 
+    def pool(self) -> N.mla_pool_t:
+        """The buffers as mla_cache_keep and mla_cache_copy_pages take them."""
+        known = self.__dict__.get("_pool")
+        if known is None or known[0] is not self.kv_pool or known[1] is not self.kr_pool or known[2] is not self.kv_scale:
+            known = self._pool = (self.kv_pool, self.kr_pool, self.kv_scale,
+                                  N.make_pool(self.kv_pool, self.kr_pool, self.kv_scale))
+        return known[3]
+
     @property
     def nbytes(self) -> int:
         n = self.kv_pool.numel() * self.kv_pool.element_size()
@@ -79,6 +87,29 @@ class PagedLatentCache:
             n += self.kr_pool.numel() * self.kr_pool.element_size()
             n += self.kv_scale.numel() * self.kv_scale.element_size()
         return n
+
+
+class Workspace:
+    """Device scratch for calls of one kind: a buffer per stream, so that calls on two streams do not meet in one,
+    grown by doubling.  An outgrown buffer is kept, as a captured graph may hold its address."""
+
+    def __init__(self, device):
+        self.device = device
+        self._sizes, self._by_stream, self._kept = {}, {}, []
+
+    def get(self, key, stream, size):
+        """A buffer of at least ``size()`` bytes, which depends on ``key`` alone."""
+        need = self._sizes.get(key)
+        if need is None:
+            need = self._sizes[key] = max(256, size())
+        handle = N._stream(stream)
+        buf = self._by_stream.get(handle)
+        if buf is None or buf.numel() < need:
+            if buf is not None:
+                self._kept.append(buf)
+                need = max(need, 2 * buf.numel())
+            buf = self._by_stream[handle] = torch.empty(need, dtype=torch.uint8, device=self.device)
+        return buf
 
 
 class MLADecodeLayer:
@@ -93,7 +124,7 @@ class MLADecodeLayer:
         self._ws = None
         self._ws_key = None
         self._pf_ws = None
-        self._tree_ws = None
+        self._tree_ws = Workspace(self.device)
 
     # -- the four calls ----------------------------------------------------------------------
     def append(self, cache: PagedLatentCache, c_kv, k_r, seq_idx, pos, block_table, stream=None):
@@ -191,9 +222,10 @@ class MLADecodeLayer:
                           max_blocks, cache.num_blocks, cache.kv_pool, cache.kr_pool, cache.kv_scale, stream)
 
     def decode_tree(self, cache: PagedLatentCache, q_abs, block_table, seq_lens, trees, max_seq_len,
-                    out_dtype="f32", o_lat=None, lse=None, stream=None):
+                    out_dtype="f32", o_lat=None, lse=None, stream=None, workspace=None):
         """Every drafted node over the committed tokens and the nodes its mask names; returns
-        (o_lat [nodes, n_h, d_c], lse [nodes, n_h])."""
+        (o_lat [nodes, n_h, d_c], lse [nodes, n_h]).  Without ``workspace`` (uint8 tensor) the layer's own for the
+        stream is used; captured graphs that may replay at the same time need one each."""
         d = self.dims
         B, max_blocks = block_table.shape
         T = trees.total_nodes
@@ -204,12 +236,12 @@ class MLADecodeLayer:
             o_lat = torch.empty((T, d.n_h, d.d_c), dtype=TORCH_ACT[dt], device=q_abs.device)
         if lse is None:
             lse = torch.empty((T, d.n_h), dtype=torch.float32, device=q_abs.device)
-        n = N.mla_decode_tree_workspace_size(d, B, T, max_seq_len)
-        if self._tree_ws is None or self._tree_ws.numel() < n:
-            self._tree_ws = torch.empty(max(n, 256), dtype=torch.uint8, device=q_abs.device)
+        if workspace is None:
+            workspace = self._tree_ws.get((B, T, max_seq_len), stream,
+                                          lambda: N.mla_decode_tree_workspace_size(d, B, T, max_seq_len))
         N.mla_decode_tree(d, B, trees.cu_nodes, T, trees.max_nodes, q_abs, cache.kv_pool, cache.kr_pool,
                           cache.kv_scale, block_table, max_blocks, cache.num_blocks, seq_lens, max_seq_len,
-                          trees.mask, trees.mask_words, self._tree_ws, self._tree_ws.numel(), o_lat, dt, lse, stream)
+                          trees.mask, trees.mask_words, workspace, workspace.numel(), o_lat, dt, lse, stream)
         return o_lat, lse
 
     def out_proj(self, o_lat, out_dtype="f32", out=None, stream=None):

@@ -131,17 +131,22 @@ def library() -> ctypes.CDLL:
 
 
 def _ptr(x):
-    if x is None:
-        return None
-    if isinstance(x, int):
+    if x is None or type(x) is int:
         return x
     return x.data_ptr()
 
 
+_torch = None
+
+
 def _stream(stream):
-    if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+    if stream is None:  # torch's current stream, its handle without a Stream object (a call's largest host cost)
+        global _torch
+        if _torch is None:
+            import torch
+            torch.cuda.current_stream()  # CUDA is up
+            _torch = torch
+        return _torch._C._cuda_getCurrentRawStream(_torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -269,9 +274,13 @@ def mla_decode_tree(dims, B, cu_nodes, total_nodes, max_nodes, q_abs, kv_pool, k
            "mla_decode_tree")
 
 
+def make_pool(kv_pool, kr_pool=None, kv_scale=None) -> mla_pool_t:
+    return mla_pool_t(_ptr(kv_pool), _ptr(kr_pool), _ptr(kv_scale))
+
+
 def make_pools(pools):
-    """Array of mla_pool_t from (kv_pool, kr_pool, kv_scale) triples (tensors, addresses or None)."""
-    return (mla_pool_t * len(pools))(*[mla_pool_t(_ptr(a), _ptr(b), _ptr(c)) for a, b, c in pools])
+    """Array of mla_pool_t from mla_pool_t's or (kv_pool, kr_pool, kv_scale) triples (tensors, addresses or None)."""
+    return (mla_pool_t * len(pools))(*[p if isinstance(p, mla_pool_t) else make_pool(*p) for p in pools])
 
 
 def mla_cache_keep(dims, pools, B, cu_nodes, total_nodes, block_table, max_blocks_per_seq, num_blocks, seq_lens, keep,

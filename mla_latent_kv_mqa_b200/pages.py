@@ -16,6 +16,7 @@ from __future__ import annotations
 import torch
 
 from . import native as N
+from .layer import Workspace
 
 
 class PagedSequences:
@@ -27,21 +28,18 @@ class PagedSequences:
         self.num_blocks = int(num_blocks)
         self._table = N.make_page_table(page_size, num_seqs, max_blocks, num_blocks, self.block_table, self.refs,
                                         self.seq_lens)
-        self._ws = None
+        self._ws = Workspace(self.block_table.device)
         self._i32 = i32
 
-    def _workspace(self, n: int):
-        need = N.mla_pages_workspace_size(self._table, n)
-        if self._ws is None or self._ws.numel() < need:
-            self._ws = torch.empty(max(need, 256), dtype=torch.uint8, device=self.block_table.device)
-        return self._ws
+    def _workspace(self, n: int, stream):
+        return self._ws.get(n, stream, lambda: N.mla_pages_workspace_size(self._table, n))
 
     def fork(self, parent, child, stream=None):
         """Sequence child[i] becomes a copy of parent[i]; all parents are read before any child changes."""
         if parent.numel() != child.numel():
             raise ValueError("fork: a parent for every child")
         n = parent.numel()
-        ws = self._workspace(n)
+        ws = self._workspace(n, stream)
         N.mla_pages_fork(self._table, n, parent, child, ws, ws.numel(), stream)
 
     def grow(self, new_lens, seqs=None, stream=None):
@@ -50,7 +48,7 @@ class PagedSequences:
         n = new_lens.numel()
         if seqs is not None and seqs.numel() != n:
             raise ValueError("grow: a length for every sequence")
-        ws = self._workspace(n)
+        ws = self._workspace(n, stream)
         moves, count = torch.empty((n, 2), **self._i32), torch.empty(1, **self._i32)
         N.mla_pages_grow(self._table, n, seqs, new_lens, moves, count, ws, ws.numel(), stream)
         return moves, count
@@ -63,7 +61,7 @@ class PagedSequences:
 
     def compact(self, stream=None):
         """The pages in use take the lowest ids; returns the page copies to make, for copy_pages."""
-        ws = self._workspace(0)
+        ws = self._workspace(0, stream)
         moves, count = torch.empty((self.num_blocks // 2, 2), **self._i32), torch.empty(1, **self._i32)
         N.mla_pages_compact(self._table, moves, count, ws, ws.numel(), stream)
         return moves, count
@@ -71,5 +69,5 @@ class PagedSequences:
     def copy_pages(self, caches, moves, stream=None):
         """Copy the pages ``moves`` = (pairs, number) names, in every cache."""
         pairs, count = moves
-        pools = N.make_pools([(c.kv_pool, c.kr_pool, c.kv_scale) for c in caches])
+        pools = N.make_pools([c.pool() for c in caches])
         N.mla_cache_copy_pages(caches[0].dims, pools, self.num_blocks, pairs, count, pairs.shape[0], stream)

@@ -50,7 +50,7 @@ class DraftTrees:
         B, max_blocks = block_table.shape
         if new_lens is None:
             new_lens = torch.empty(B, dtype=torch.int32, device=block_table.device)
-        pools = N.make_pools([(c.kv_pool, c.kr_pool, c.kv_scale) for c in caches])
+        pools = N.make_pools([c.pool() for c in caches])
         N.mla_cache_keep(caches[0].dims, pools, B, self.cu_nodes, self.total_nodes, block_table, max_blocks,
                          caches[0].num_blocks, seq_lens, keep, num_keep, keep.shape[1], new_lens, stream)
         return new_lens

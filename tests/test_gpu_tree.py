@@ -334,7 +334,7 @@ def test_padding_rows_stay_and_nothing_depends_on_the_workspace(flags):
     b = Batch([100, 0, 700], [6, 0, 3], flags=flags, pad=4, seed=9, heads=32)
     first = b.decode()
     for fill in (0, 0xFF):
-        b.layer._tree_ws.fill_(fill)
+        b.layer._tree_ws._by_stream[torch.cuda.current_stream().cuda_stream].fill_(fill)
         o = torch.full_like(first[0], 3.0)
         lse = torch.full_like(first[1], 4.0)
         b.decode(o_lat=o, lse=lse)
