@@ -19,8 +19,9 @@ __device__ __forceinline__ int pages_of(int len, int page) { return len / page +
 constexpr int kForkThreads = 128;
 
 __global__ void __launch_bounds__(kForkThreads)
-fork_read_kernel(const __grid_constant__ PageTable p, int n, const int32_t *__restrict__ parent,
-                 const int32_t *__restrict__ child, int32_t *__restrict__ lens, int32_t *__restrict__ rows) {
+fork_read_kernel(const __grid_constant__ PageTable p, int n, const int32_t *parent,
+                 const int32_t *child, int32_t *lens, int32_t *rows) {
+    dependent_start();
     const int i = blockIdx.x, s = parent[i], c = child[i];
     bool bad = s < 0 || s >= p.num_seqs || c < 0 || c >= p.num_seqs;
     for (int k = threadIdx.x; k < n; k += kForkThreads) bad |= k != i && child[k] == c;  // a child once
@@ -47,8 +48,9 @@ fork_read_kernel(const __grid_constant__ PageTable p, int n, const int32_t *__re
 }
 
 __global__ void __launch_bounds__(kForkThreads)
-fork_write_kernel(const __grid_constant__ PageTable p, const int32_t *__restrict__ child,
-                  const int32_t *__restrict__ lens, const int32_t *__restrict__ rows) {
+fork_write_kernel(const __grid_constant__ PageTable p, const int32_t *child,
+                  const int32_t *lens, const int32_t *rows) {
+    dependent_start();
     const int i = blockIdx.x, len = lens[i];
     if (len < 0) return;
     const int c = child[i], np = pages_of(len, p.page);
@@ -63,8 +65,9 @@ fork_write_kernel(const __grid_constant__ PageTable p, const int32_t *__restrict
 
 // ---- mla_pages_trim --------------------------------------------------------------------------
 __global__ void __launch_bounds__(kForkThreads)
-trim_kernel(const __grid_constant__ PageTable p, const int32_t *__restrict__ seqs,
-            const int32_t *__restrict__ new_lens) {
+trim_kernel(const __grid_constant__ PageTable p, const int32_t *seqs,
+            const int32_t *new_lens) {
+    dependent_start();
     const int i = blockIdx.x, s = seqs ? seqs[i] : i, len = new_lens[i];
     if (s < 0 || s >= p.num_seqs || len < 0) {
         if (threadIdx.x == 0) record_error(p.err, len < 0 ? kErrBadSeqLen : kErrBadSeqIndex);
@@ -124,15 +127,16 @@ struct GrowWs {
     int32_t *want;    // [n] pages wanted; bit 30: the first of them is a copy
     int32_t *free_;   // [num_blocks] the free pages taken
 };
-constexpr int kWantCopy = 1 << 30;
+constexpr int kWantCopy = 1 << 30, kFewPages = 8, kSearch = 8;
 
 __global__ void __launch_bounds__(kPlanThreads)
-grow_kernel(const __grid_constant__ PageTable p, int n, const int32_t *__restrict__ seqs,
-            const int32_t *__restrict__ new_lens, int32_t *moves, int32_t *num_moves,
+grow_kernel(const __grid_constant__ PageTable p, int n, const int32_t *seqs,
+            const int32_t *new_lens, int32_t *moves, int32_t *num_moves,
             const __grid_constant__ GrowWs ws) {
+    dependent_start();
     __shared__ ScanScratch scan;
     __shared__ int err_code;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31;
     if (tid == 0) err_code = 0;
     __syncthreads();
     auto seq = [&](int i) { return seqs ? seqs[i] : i; };
@@ -176,20 +180,35 @@ grow_kernel(const __grid_constant__ PageTable p, int n, const int32_t *__restric
         }
     }
     __syncthreads();
-    // 1: wants, a warp per entry
-    for (int i = warp; i < n; i += kPlanThreads / 32) {
-        const int s = seq(i), cur = p.seq_lens[s], len = new_lens[i];
-        int want = 0;
-        if (len > cur) {
-            for (int k = pages_of(cur, p.page) + lane; k < pages_of(len, p.page); k += 32) want += *entry(s, k) < 0;
+    // 1: wants, a thread per entry (its loads run beside the others'); a warp where an entry grows by many pages
+    for (int i0 = 0; i0 < n; i0 += kPlanThreads) {
+        const int i = i0 + tid;
+        int s = 0, cur = 0, len = 0, want = 0;
+        if (i < n) {
+            s = seq(i);
+            cur = p.seq_lens[s];
+            len = new_lens[i];
+        }
+        const int lo = pages_of(cur, p.page), hi = len > cur ? pages_of(len, p.page) : lo;
+        const bool few = hi - lo <= kFewPages;
+        if (few)
+            for (int k = lo; k < hi; ++k) want += *entry(s, k) < 0;
+        for (unsigned many = __ballot_sync(0xffffffffu, !few); many; many &= many - 1) {
+            const int who = __ffs(many) - 1;
+            const int ws_ = __shfl_sync(0xffffffffu, s, who), wlo = __shfl_sync(0xffffffffu, lo, who), whi = __shfl_sync(0xffffffffu, hi, who);
+            int w = 0;
+            for (int k = wlo + lane; k < whi; k += 32) w += *entry(ws_, k) < 0;
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) want += __shfl_xor_sync(0xffffffffu, want, o);
-            if (cur % p.page) {
+            for (int o = 16; o > 0; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
+            if (lane == who) want = w;
+        }
+        if (i < n) {
+            if (len > cur && cur % p.page) {
                 const int v = *entry(s, cur / p.page);
                 if (ws.count[v] < p.refs[v] || ws.last[v] != i) want = (want + 1) | kWantCopy;
             }
+            ws.want[i] = want;
         }
-        if (lane == 0) ws.want[i] = want;
     }
     __syncthreads();
     int total = 0, copies = 0;
@@ -201,13 +220,16 @@ grow_kernel(const __grid_constant__ PageTable p, int n, const int32_t *__restric
         block_exclusive((w & kWantCopy) != 0, &scan, &sum);
         copies += sum;
     }
-    // 2: the lowest free pages
+    // 2: the lowest free pages, kSearch consecutive ids a thread at a time
     int found = 0;
-    for (int v0 = 0; v0 < p.num_blocks && found < total; v0 += kPlanThreads) {
-        const int v = v0 + tid, is_free = v < p.num_blocks && p.refs[v] == 0;
+    for (int v0 = 0; v0 < p.num_blocks && found < total; v0 += kPlanThreads * kSearch) {
+        const int v1 = v0 + tid * kSearch;
+        unsigned mine = 0;
+#pragma unroll
+        for (int k = 0; k < kSearch; ++k) mine |= (unsigned)(v1 + k < p.num_blocks && p.refs[v1 + k] == 0) << k;
         int sum;
-        const int at = found + block_exclusive(is_free, &scan, &sum);
-        if (is_free && at < total) ws.free_[at] = v;
+        int at = found + block_exclusive(__popc(mine), &scan, &sum);
+        for (; mine && at < total; mine &= mine - 1) ws.free_[at++] = v1 + __ffs(mine) - 1;
         found += sum;
     }
     if (found < total) {
@@ -217,47 +239,57 @@ grow_kernel(const __grid_constant__ PageTable p, int n, const int32_t *__restric
         }
         return;
     }
-    // 3: hand them out, a warp per entry; want[] becomes the first page's place among the free ones
+    // 3: hand them out in the entries' order
+    __syncthreads();
     int page0 = 0, move0 = 0;
     for (int i0 = 0; i0 < n; i0 += kPlanThreads) {
         const int i = i0 + tid, w = i < n ? ws.want[i] : 0;
         int sum_p, sum_m;
-        const int at = page0 + block_exclusive(w & ~kWantCopy, &scan, &sum_p);
+        int at = page0 + block_exclusive(w & ~kWantCopy, &scan, &sum_p);
         const int mv = move0 + block_exclusive((w & kWantCopy) != 0, &scan, &sum_m);
         page0 += sum_p;
         move0 += sum_m;
+        int s = 0, cur = 0, len = 0;
         if (i < n) {
-            ws.want[i] = at;
-            if (w & kWantCopy) {  // the first page: a copy of the shared one
-                const int s = seq(i), to = ws.free_[at];
-                int32_t *e = entry(s, p.seq_lens[s] / p.page);
-                const int v = *e;
-                moves[2 * mv] = v;
-                moves[2 * mv + 1] = to;
-                *e = to;
-                atomicSub(&p.refs[v], 1);
-                p.refs[to] = 1;
-                ws.want[i] = at + 1;
+            s = seq(i);
+            cur = p.seq_lens[s];
+            len = new_lens[i];
+        }
+        if (w & kWantCopy) {  // the first page: a copy of the shared one
+            const int to = ws.free_[at++];
+            int32_t *e = entry(s, cur / p.page);
+            const int v = *e;
+            moves[2 * mv] = v;
+            moves[2 * mv + 1] = to;
+            *e = to;
+            atomicSub(&p.refs[v], 1);
+            p.refs[to] = 1;
+        }
+        const int lo = pages_of(cur, p.page), hi = len > cur ? pages_of(len, p.page) : lo;
+        const bool few = hi - lo <= kFewPages;
+        if (few)
+            for (int k = lo; k < hi; ++k)
+                if (*entry(s, k) < 0) {
+                    const int to = ws.free_[at++];
+                    *entry(s, k) = to;
+                    p.refs[to] = 1;
+                }
+        for (unsigned many = __ballot_sync(0xffffffffu, !few); many; many &= many - 1) {
+            const int who = __ffs(many) - 1;
+            const int ws_ = __shfl_sync(0xffffffffu, s, who), wlo = __shfl_sync(0xffffffffu, lo, who), whi = __shfl_sync(0xffffffffu, hi, who);
+            int wat = __shfl_sync(0xffffffffu, at, who);
+            for (int k0 = wlo; k0 < whi; k0 += 32) {
+                const bool open = k0 + lane < whi && *entry(ws_, k0 + lane) < 0;
+                const unsigned set = __ballot_sync(0xffffffffu, open);
+                if (open) {
+                    const int to = ws.free_[wat + __popc(set & ((1u << lane) - 1u))];
+                    *entry(ws_, k0 + lane) = to;
+                    p.refs[to] = 1;
+                }
+                wat += __popc(set);
             }
         }
-    }
-    __syncthreads();
-    for (int i = warp; i < n; i += kPlanThreads / 32) {
-        const int s = seq(i), cur = p.seq_lens[s], len = new_lens[i];
-        int at = ws.want[i];
-        const int hi = pages_of(len, p.page);
-        for (int k0 = pages_of(cur, p.page); k0 < hi; k0 += 32) {
-            const bool open = k0 + lane < hi && *entry(s, k0 + lane) < 0;
-            const unsigned who = __ballot_sync(0xffffffffu, open);
-            if (open) {
-                const int to = ws.free_[at + __popc(who & ((1u << lane) - 1u))];
-                *entry(s, k0 + lane) = to;
-                p.refs[to] = 1;
-            }
-            at += __popc(who);
-        }
-        __syncwarp();
-        if (lane == 0 && len > cur) p.seq_lens[s] = len;
+        if (len > cur) p.seq_lens[s] = len;
     }
     if (tid == 0) *num_moves = copies;
 }
@@ -268,24 +300,32 @@ grow_kernel(const __grid_constant__ PageTable p, int n, const int32_t *__restric
 __global__ void __launch_bounds__(kPlanThreads)
 compact_plan_kernel(const __grid_constant__ PageTable p, int32_t *moves, int32_t *num_moves, int32_t *used_out,
                     int32_t *to) {
+    dependent_start();
     __shared__ ScanScratch scan;
     const int tid = threadIdx.x;
-    int mine = 0, used;
-    for (int v = tid; v < p.num_blocks; v += kPlanThreads) mine += p.refs[v] > 0;
-    block_exclusive(mine, &scan, &used);
+    int count = 0, used;
+    for (int v = tid; v < p.num_blocks; v += kPlanThreads) count += p.refs[v] > 0;
+    block_exclusive(count, &scan, &used);
     int holes = 0, movers = 0;
-    for (int v0 = 0; v0 < p.num_blocks; v0 += kPlanThreads) {
-        const int v = v0 + tid;
-        const bool live = v < p.num_blocks && p.refs[v] > 0;
-        const int hole = v < used && !live, mover = live && v >= used;
+    for (int v0 = 0; v0 < p.num_blocks; v0 += kPlanThreads * kSearch) {  // kSearch consecutive ids a thread
+        const int v1 = v0 + tid * kSearch;
+        unsigned live = 0, there = 0;
+#pragma unroll
+        for (int k = 0; k < kSearch; ++k) {
+            live |= (unsigned)(v1 + k < p.num_blocks && p.refs[v1 + k] > 0) << k;
+            there |= (unsigned)(v1 + k < p.num_blocks) << k;
+        }
+        const int in_front = min(max(used - v1, 0), kSearch);  // of these ids, those among the first `used`
+        const unsigned front = (1u << in_front) - 1u;
+        unsigned hole = ~live & there & front, mover = live & ~front;
         int sum;
-        const int h = holes + block_exclusive(hole, &scan, &sum);
+        int h = holes + block_exclusive(__popc(hole), &scan, &sum);
         holes += sum;
-        const int m = movers + block_exclusive(mover, &scan, &sum);
+        int m = movers + block_exclusive(__popc(mover), &scan, &sum);
         movers += sum;
-        if (hole) moves[2 * h + 1] = v;
-        if (mover) moves[2 * m] = v;
-        else if (v >= used && v < p.num_blocks) to[v] = -1;
+        for (unsigned dead = ~live & there & ~front; dead; dead &= dead - 1) to[v1 + __ffs(dead) - 1] = -1;
+        for (; hole; hole &= hole - 1) moves[2 * h++ + 1] = v1 + __ffs(hole) - 1;
+        for (; mover; mover &= mover - 1) moves[2 * m++] = v1 + __ffs(mover) - 1;
     }
     __syncthreads();
     for (int k = tid; k < movers; k += kPlanThreads) {
@@ -302,8 +342,9 @@ compact_plan_kernel(const __grid_constant__ PageTable p, int32_t *moves, int32_t
 
 constexpr int kFollowThreads = 256;
 __global__ void __launch_bounds__(kFollowThreads)
-compact_follow_kernel(const __grid_constant__ PageTable p, const int32_t *__restrict__ used_in,
-                      const int32_t *__restrict__ to) {
+compact_follow_kernel(const __grid_constant__ PageTable p, const int32_t *used_in,
+                      const int32_t *to) {
+    dependent_start();
     const int used = *used_in;
     const size_t n = (size_t)p.num_seqs * p.max_blocks;
     for (size_t i = (size_t)blockIdx.x * kFollowThreads + threadIdx.x; i < n; i += (size_t)gridDim.x * kFollowThreads) {
@@ -327,9 +368,27 @@ struct CopyArgs {
     unsigned *err;
 };
 
+// Piece `piece` of a page of `cols` elements.
+template <typename V>
+__device__ __forceinline__ void copy_part(char *part, int cols, int s, int d, int piece, int pieces) {
+    const int c0 = (int)((int64_t)cols * piece / pieces), c1 = (int)((int64_t)cols * (piece + 1) / pieces);
+    const V *src = reinterpret_cast<const V *>(part) + (size_t)s * cols;
+    V *dst = reinterpret_cast<V *>(part) + (size_t)d * cols;
+    for (int c = c0 + threadIdx.x; c < c1; c += kCopyThreads * kInFlight) {
+        V v[kInFlight];
+#pragma unroll
+        for (int i = 0; i < kInFlight; ++i)
+            if (c + i * kCopyThreads < c1) v[i] = src[c + i * kCopyThreads];
+#pragma unroll
+        for (int i = 0; i < kInFlight; ++i)
+            if (c + i * kCopyThreads < c1) dst[c + i * kCopyThreads] = v[i];
+    }
+}
+
 template <typename V>
 __global__ void __launch_bounds__(kCopyThreads)
 copy_pages_kernel(const __grid_constant__ CopyArgs a, const __grid_constant__ PoolSet pools) {
+    dependent_start();
     const int count = a.num_moves ? min(max(*a.num_moves, 0), a.max_moves) : a.max_moves;
     const int64_t work = (int64_t)count * a.num_pools * a.pieces;
     for (int64_t w = blockIdx.x; w < work; w += gridDim.x) {
@@ -342,21 +401,11 @@ copy_pages_kernel(const __grid_constant__ CopyArgs a, const __grid_constant__ Po
             continue;
         }
         if (s == d) continue;
-#pragma unroll
-        for (int part = 0; part < kPoolParts; ++part) {
-            const int cols = pools.row_bytes[part] / (int)sizeof(V);  // a page's bytes
-            const int c0 = (int)((int64_t)cols * piece / a.pieces), c1 = (int)((int64_t)cols * (piece + 1) / a.pieces);
-            const V *src = reinterpret_cast<const V *>(pools.pool[q].part[part]) + (size_t)s * cols;
-            V *dst = reinterpret_cast<V *>(pools.pool[q].part[part]) + (size_t)d * cols;
-            for (int c = c0 + threadIdx.x; c < c1; c += kCopyThreads * kInFlight) {
-                V v[kInFlight];
-#pragma unroll
-                for (int i = 0; i < kInFlight; ++i)
-                    if (c + i * kCopyThreads < c1) v[i] = src[c + i * kCopyThreads];
-#pragma unroll
-                for (int i = 0; i < kInFlight; ++i)
-                    if (c + i * kCopyThreads < c1) dst[c + i * kCopyThreads] = v[i];
-            }
+        const PoolRef &pool = pools.pool[q];
+        copy_part<V>(pool.part[0], pools.row_bytes[0] / (int)sizeof(V), s, d, piece, a.pieces);
+        if (pools.row_bytes[1]) {
+            copy_part<V>(pool.part[1], pools.row_bytes[1] / (int)sizeof(V), s, d, piece, a.pieces);
+            copy_part<uint32_t>(pool.part[2], pools.row_bytes[2] / 4, s, d, piece, a.pieces);
         }
     }
 }
@@ -398,31 +447,30 @@ size_t pages_workspace_bytes(const PageTable &p, int n) { return pages_ws(p, n, 
 cudaError_t launch_pages_fork(const PageTable &p, int n, const int32_t *parent, const int32_t *child, void *ws,
                               cudaStream_t st) {
     const PagesWs s = pages_ws(p, n, ws);
-    fork_read_kernel<<<n, kForkThreads, 0, st>>>(p, n, parent, child, s.a, s.e);
-    fork_write_kernel<<<n, kForkThreads, 0, st>>>(p, child, s.a, s.e);
-    return cudaGetLastError();
+    const cudaError_t e = launch_dependent(fork_read_kernel, dim3(n), kForkThreads, 0, st, p, n, parent, child, s.a, s.e);
+    return e != cudaSuccess ? e : launch_dependent(fork_write_kernel, dim3(n), kForkThreads, 0, st, p, child, s.a, s.e);
 }
 
 cudaError_t launch_pages_grow(const PageTable &p, int n, const int32_t *seqs, const int32_t *new_lens, int32_t *moves,
                               int32_t *num_moves, void *ws, cudaStream_t st) {
     const PagesWs s = pages_ws(p, n, ws);
-    grow_kernel<<<1, kPlanThreads, 0, st>>>(p, n, seqs, new_lens, moves, num_moves, GrowWs{s.a, s.b, s.c, s.d, s.e});
-    return cudaGetLastError();
+    return launch_dependent(grow_kernel, dim3(1), kPlanThreads, 0, st, p, n, seqs, new_lens, moves, num_moves,
+                            GrowWs{s.a, s.b, s.c, s.d, s.e});
 }
 
 cudaError_t launch_pages_trim(const PageTable &p, int n, const int32_t *seqs, const int32_t *new_lens,
                               cudaStream_t st) {
-    trim_kernel<<<n, kForkThreads, 0, st>>>(p, seqs, new_lens);
-    return cudaGetLastError();
+    return launch_dependent(trim_kernel, dim3(n), kForkThreads, 0, st, p, seqs, new_lens);
 }
 
 cudaError_t launch_pages_compact(const PageTable &p, int32_t *moves, int32_t *num_moves, void *ws, cudaStream_t st) {
     const PagesWs s = pages_ws(p, 0, ws);
-    compact_plan_kernel<<<1, kPlanThreads, 0, st>>>(p, moves, num_moves, s.a, s.b);
+    const cudaError_t e = launch_dependent(compact_plan_kernel, dim3(1), kPlanThreads, 0, st, p, moves, num_moves, s.a, s.b);
+    if (e != cudaSuccess) return e;
     const size_t n = (size_t)p.num_seqs * p.max_blocks, blocks = (n + kFollowThreads - 1) / kFollowThreads;
     const int most = 4 * sm_count();
-    compact_follow_kernel<<<blocks < (size_t)most ? (int)blocks : most, kFollowThreads, 0, st>>>(p, s.a, s.b);
-    return cudaGetLastError();
+    return launch_dependent(compact_follow_kernel, dim3(blocks < (size_t)most ? (int)blocks : most), kFollowThreads, 0, st,
+                            p, s.a, s.b);
 }
 
 cudaError_t launch_copy_pages(const mla_dims_t &d, int num_pools, const mla_pool_t *pools, int num_blocks,
@@ -434,10 +482,10 @@ cudaError_t launch_copy_pages(const mla_dims_t &d, int num_pools, const mla_pool
         const CopyArgs a{moves, num_moves, max_moves, num_blocks, n, 3, device_error_word()};
         const int64_t work = (int64_t)max_moves * n * a.pieces, most = 8 * sm_count();
         const int grid = (int)(work < most ? work : most);
-        if (v == 16) copy_pages_kernel<uint4><<<grid, kCopyThreads, 0, st>>>(a, set);
-        else if (v == 4) copy_pages_kernel<uint32_t><<<grid, kCopyThreads, 0, st>>>(a, set);
-        else copy_pages_kernel<uint8_t><<<grid, kCopyThreads, 0, st>>>(a, set);
-        const cudaError_t e = cudaGetLastError();
+        const cudaError_t e = launch_dependent(v == 16  ? copy_pages_kernel<uint4>
+                                               : v == 4 ? copy_pages_kernel<uint32_t>
+                                                        : copy_pages_kernel<uint8_t>,
+                                               dim3(grid), kCopyThreads, 0, st, a, set);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;

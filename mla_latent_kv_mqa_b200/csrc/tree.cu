@@ -24,10 +24,11 @@ namespace {
 constexpr int kPrepThreads = 128;
 
 __global__ void __launch_bounds__(kPrepThreads)
-tree_prepare_kernel(int B, const int32_t *__restrict__ cu, int T, const int32_t *__restrict__ parent,
-                    const int32_t *__restrict__ seq_lens, int words, uint32_t *__restrict__ mask,
-                    int32_t *__restrict__ pos, int32_t *__restrict__ slot, int32_t *__restrict__ seq_idx,
+tree_prepare_kernel(int B, const int32_t *cu, int T, const int32_t *parent,
+                    const int32_t *seq_lens, int words, uint32_t *mask,
+                    int32_t *pos, int32_t *slot, int32_t *seq_idx,
                     unsigned *err) {
+    dependent_start();
     __shared__ int16_t up[kMaxTreeNodes];
     const int b = blockIdx.x;
     if (b == B) {
@@ -94,8 +95,25 @@ struct KeepArgs {
 };
 
 template <typename V>
+__device__ __forceinline__ void keep_part(char *part, int cols, const int64_t *rows, int nk) {
+    V *base = reinterpret_cast<V *>(part);
+    for (int c = threadIdx.x; c < cols; c += kKeepThreads) {
+        for (int i0 = 0; i0 < nk; i0 += kBatch) {
+            V v[kBatch];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i)
+                if (i0 + i < nk && rows[2 * (i0 + i)] >= 0) v[i] = base[rows[2 * (i0 + i)] * cols + c];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i)
+                if (i0 + i < nk && rows[2 * (i0 + i)] >= 0) base[rows[2 * (i0 + i) + 1] * cols + c] = v[i];
+        }
+    }
+}
+
+template <typename V>
 __global__ void __launch_bounds__(kKeepThreads)
 cache_keep_kernel(const __grid_constant__ KeepArgs a, const __grid_constant__ PoolSet pools) {
+    dependent_start();
     extern __shared__ int64_t rows[];  // per kept node: source and destination row of the pool, -1: nothing to move
     const int b = blockIdx.x;
     TreeSpan sp;
@@ -134,21 +152,10 @@ cache_keep_kernel(const __grid_constant__ KeepArgs a, const __grid_constant__ Po
     }
     if (bad || bad_len || bad_block) return;
     const PoolRef &p = pools.pool[blockIdx.y];
-#pragma unroll
-    for (int part = 0; part < kPoolParts; ++part) {
-        const int cols = pools.row_bytes[part] / (int)sizeof(V);
-        V *base = reinterpret_cast<V *>(p.part[part]);
-        for (int c = threadIdx.x; c < cols; c += kKeepThreads) {
-            for (int i0 = 0; i0 < nk; i0 += kBatch) {
-                V v[kBatch];
-#pragma unroll
-                for (int i = 0; i < kBatch; ++i)
-                    if (i0 + i < nk && rows[2 * (i0 + i)] >= 0) v[i] = base[rows[2 * (i0 + i)] * cols + c];
-#pragma unroll
-                for (int i = 0; i < kBatch; ++i)
-                    if (i0 + i < nk && rows[2 * (i0 + i)] >= 0) base[rows[2 * (i0 + i) + 1] * cols + c] = v[i];
-            }
-        }
+    keep_part<V>(p.part[0], pools.row_bytes[0] / (int)sizeof(V), rows, nk);
+    if (pools.row_bytes[1]) {
+        keep_part<V>(p.part[1], pools.row_bytes[1] / (int)sizeof(V), rows, nk);
+        keep_part<uint32_t>(p.part[2], 1, rows, nk);
     }
 }
 
@@ -175,6 +182,7 @@ __device__ __forceinline__ float load_cache(const TreeArgs &a, size_t slot, int 
 template <typename Ta, int KV, int NC>
 __global__ void __launch_bounds__(kHeads * 32)
 tree_simt_kernel(const __grid_constant__ TreeArgs a, int seg_len, int n_split, TreePartials part) {
+    dependent_start();
     extern __shared__ float smem[];
     const int row = a.d_c + a.d_r, kv_stride = row + 1;  // padding: lanes read different rows
     float *q_s = smem, *kv_s = smem + kHeads * row;
@@ -259,6 +267,7 @@ constexpr int kJoinThreads = 128;
 template <typename To>
 __global__ void __launch_bounds__(kJoinThreads)
 tree_join_kernel(const __grid_constant__ TreeArgs a, int n_split, TreePartials part) {
+    dependent_start();
     const int t = blockIdx.x, h = blockIdx.y;
     TreeSpan sp;
     if (tree_of_node(a.cu, a.B, a.T, a.max_nodes, t, &sp) < 0) return;
@@ -322,8 +331,7 @@ cudaError_t launch_tree_simt(const mla_dims_t &d, const TreeArgs &a, void *ws, c
     auto run = [&](auto kern) {
         e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e == cudaSuccess) {
-            kern<<<grid, kHeads * 32, smem, st>>>(a, pl.seg_len, pl.n_split, part);
-            e = cudaGetLastError();
+            e = launch_dependent(kern, grid, kHeads * 32, smem, st, a, pl.seg_len, pl.n_split, part);
         }
     };
 #define MLA_TREE_SIMT(TA, KV)                                           \
@@ -343,17 +351,15 @@ cudaError_t launch_tree_simt(const mla_dims_t &d, const TreeArgs &a, void *ws, c
 #undef MLA_TREE_SIMT
     if (e != cudaSuccess) return e;
     const dim3 jg(a.T, d.n_h);
-    if (a.out_bf16) tree_join_kernel<__nv_bfloat16><<<jg, kJoinThreads, 0, st>>>(a, pl.n_split, part);
-    else tree_join_kernel<float><<<jg, kJoinThreads, 0, st>>>(a, pl.n_split, part);
-    return cudaGetLastError();
+    return launch_dependent(a.out_bf16 ? tree_join_kernel<__nv_bfloat16> : tree_join_kernel<float>, jg, kJoinThreads, 0,
+                            st, a, pl.n_split, part);
 }
 
 cudaError_t launch_tree_prepare(int B, const int32_t *cu, int T, const int32_t *parent, const int32_t *seq_lens,
                                 int words, uint32_t *mask, int32_t *pos, int32_t *slot, int32_t *seq_idx,
                                 cudaStream_t st) {
-    tree_prepare_kernel<<<B + 1, kPrepThreads, 0, st>>>(B, cu, T, parent, seq_lens, words, mask, pos, slot, seq_idx,
-                                                        device_error_word());
-    return cudaGetLastError();
+    return launch_dependent(tree_prepare_kernel, dim3(B + 1), kPrepThreads, 0, st, B, cu, T, parent, seq_lens, words,
+                            mask, pos, slot, seq_idx, device_error_word());
 }
 
 cudaError_t launch_cache_keep(const mla_dims_t &d, int num_pools, const mla_pool_t *pools, int B, const int32_t *cu,
@@ -369,10 +375,10 @@ cudaError_t launch_cache_keep(const mla_dims_t &d, int num_pools, const mla_pool
         const int v = make_pool_set(d, 1, pools + p0, n, &set);
         if (p0 > 0) a.new_lens = nullptr;
         const dim3 grid(B, n);
-        if (v == 16) cache_keep_kernel<uint4><<<grid, kKeepThreads, smem, st>>>(a, set);
-        else if (v == 4) cache_keep_kernel<uint32_t><<<grid, kKeepThreads, smem, st>>>(a, set);
-        else cache_keep_kernel<uint8_t><<<grid, kKeepThreads, smem, st>>>(a, set);
-        const cudaError_t e = cudaGetLastError();
+        const cudaError_t e = launch_dependent(v == 16  ? cache_keep_kernel<uint4>
+                                               : v == 4 ? cache_keep_kernel<uint32_t>
+                                                        : cache_keep_kernel<uint8_t>,
+                                               grid, kKeepThreads, smem, st, a, set);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;

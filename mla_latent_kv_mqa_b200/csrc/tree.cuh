@@ -69,21 +69,43 @@ struct PoolSet {
     PoolRef pool[kPoolsPerLaunch];
 };
 // Fills *set for rows of `tokens` tokens (1, or a page); returns the widest of 16, 4 and 1 bytes that
-// divides every row and base address.
+// divides every row and base address of the first two parts (the scales are moved as they are, 4 bytes each).
 inline int make_pool_set(const mla_dims_t &d, int tokens, const mla_pool_t *pools, int n, PoolSet *set) {
     const bool fp8 = d.kv_dtype == MLA_DTYPE_FP8_E4M3;
     const int es = d.kv_dtype == MLA_DTYPE_F32 ? 4 : 2;
     set->row_bytes[0] = tokens * (fp8 ? d.d_c : (d.d_c + d.d_r) * es);
     set->row_bytes[1] = tokens * (fp8 ? d.d_r * 2 : 0);
     set->row_bytes[2] = tokens * (fp8 ? 4 : 0);
-    uintptr_t all = (uintptr_t)set->row_bytes[0] | (uintptr_t)set->row_bytes[1] | (uintptr_t)set->row_bytes[2];
+    uintptr_t all = (uintptr_t)set->row_bytes[0] | (uintptr_t)set->row_bytes[1];
     for (int i = 0; i < n; ++i) {
         set->pool[i].part[0] = reinterpret_cast<char *>(pools[i].kv_pool);
         set->pool[i].part[1] = reinterpret_cast<char *>(pools[i].kr_pool);
         set->pool[i].part[2] = reinterpret_cast<char *>(pools[i].kv_scale);
-        for (int k = 0; k < (fp8 ? 3 : 1); ++k) all |= reinterpret_cast<uintptr_t>(set->pool[i].part[k]);
+        for (int k = 0; k < (fp8 ? 2 : 1); ++k) all |= reinterpret_cast<uintptr_t>(set->pool[i].part[k]);
     }
     return all % 16 == 0 ? 16 : all % 4 == 0 ? 4 : 1;
+}
+
+// A launch as a programmatic dependent of the kernel before it on the stream: the kernel starts with
+// griddepcontrol.wait, so that only its set-up overlaps that kernel.
+template <typename... P, typename... A>
+inline cudaError_t launch_dependent(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, A... args) {
+    cudaLaunchAttribute pdl;
+    pdl.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    pdl.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = &pdl;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, P(args)...);
+}
+// At the start of such a kernel: dependents of its own may be set up, and what came before is complete.
+__device__ __forceinline__ void dependent_start() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // ---- launchers ---------------------------------------------------------------------------------

@@ -688,8 +688,8 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             const int blk = a.bt[(size_t)w.b * a.max_blocks + g];
             if (blk < 0 || blk >= a.num_blocks) return;  // the loader reports it
             const float *src = a.kv_scale + (size_t)blk * PG + lane;
-            sc0 = __ldg(src);
-            sc1 = __ldg(src + 32);
+            sc0 = src[0];
+            sc1 = src[32];
         };
         if (F8) load_scales(it);
         for (int u = 0; ok && !it.done(); ++u) {
