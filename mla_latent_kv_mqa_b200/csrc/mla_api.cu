@@ -388,7 +388,7 @@ static bool tree_sizes_ok(const mla_dims_t *dims, int B, int total_nodes, int ma
 
 size_t mla_decode_tree_workspace_size(const mla_dims_t *dims, int B, int total_nodes, int max_seq_len) {
     if (check_dims(dims) != MLA_OK || !tree_sizes_ok(dims, B, total_nodes, max_seq_len)) return 0;
-    if (tree_tc_supported(*dims)) return tree_tc_workspace_bytes(B);
+    if (tree_tc_supported(*dims)) return tree_tc_workspace_bytes(*dims, B, total_nodes);
     return tree_simt_workspace_bytes(*dims, total_nodes, max_seq_len) + 256;
 }
 

@@ -113,7 +113,7 @@ size_t tree_simt_workspace_bytes(const mla_dims_t &d, int T, int max_seq_len);
 cudaError_t launch_tree_simt(const mla_dims_t &d, const TreeArgs &a, void *ws, cudaStream_t st);
 // Tensor cores: d_c = 512, d_r = 64, 64-token pages, bf16 activations.
 bool tree_tc_supported(const mla_dims_t &d);
-size_t tree_tc_workspace_bytes(int B);
+size_t tree_tc_workspace_bytes(const mla_dims_t &d, int B, int T);
 cudaError_t launch_tree_tc(const mla_dims_t &d, const TreeArgs &a, void *ws, cudaStream_t st);
 cudaError_t launch_tree_prepare(int B, const int32_t *cu, int T, const int32_t *parent, const int32_t *seq_lens,
                                 int words, uint32_t *mask, int32_t *pos, int32_t *slot, int32_t *seq_idx,

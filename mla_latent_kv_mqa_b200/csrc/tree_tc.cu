@@ -91,7 +91,8 @@ struct __align__(16) Ctrl {
     // its peer, so one barrier would take its arrivals for two steps as both CTAs' for one.
     uint64_t o_ok[2], pv_done[2];
     uint32_t tmem_base, abort;
-    int w_b, w_tile, w_step, w_n;
+    int w_b, w_tile, w_step, w_n, w_tg;
+    long long w_units;  // of the batch
     long long scan_u[MAX_WARPS];
     int scan_t[MAX_WARPS];
     alignas(16) float scale[SM_WARPS][2][PG];  // FP8: each softmax warp's page's scales, as they are and with 0 for infinities and NaN
@@ -100,11 +101,14 @@ struct __align__(16) Ctrl {
 constexpr int SMEM = 1024 + DATA + (int)((sizeof(Ctrl) + 127) / 128 * 128);
 static_assert(SMEM <= 232448, "shared memory per block");
 
-// A batch in units, for the join: unit_off[b], tile_off[b] of every sequence, totals at [B].
+// What the join reads: the batch's units and tiles, and for every tile its first row, its rows, the first
+// pair that had steps of it and how many pairs from there (0: none, a bad length; negative: that pair began
+// with another tile).
 struct TreePlan {
-    long long *unit_off;
-    int *tile_off;
-    float *o, *m, *l;  // [2 pairs][128][512], [2 pairs][128]
+    long long *units;
+    int *tiles;
+    int4 *tile;
+    float *o, *m, *l;  // [2 pairs][128 / 8][512][8 rows], [2 pairs][128 rows]
     int pairs;
 };
 
@@ -125,7 +129,7 @@ __device__ __forceinline__ Seq seq_of(const TreeArgs &a, int b) {
 // Walks a pair's units; every role walks the same ones.
 struct Walk {
     Seq s;
-    int b, tile, step, left;
+    int b, tile, step, left, tg;  // tg: the tile's number in the batch
     bool first;  // of its segment (a run of one tile's steps)
     bool head;   // the segment is the pair's first
     int seg0;    // the segment's first step
@@ -134,6 +138,7 @@ struct Walk {
         tile = w[1];
         step = seg0 = w[2];
         left = w[3];
+        tg = w[4];
         first = head = true;
         if (left > 0) s = seq_of(a, b);
     }
@@ -146,23 +151,28 @@ struct Walk {
         --left;
         if (++step == s.steps) {
             step = 0;
+            ++tg;
             if (++tile == s.tiles) {
                 tile = 0;
-                b = next_seq(a, b);
+                const int2 to = next_seq(a, b);
+                b = to.x;
+                tg += to.y;
                 if (b < a.B) s = seq_of(a, b);
                 else left = 0;
             }
         }
         if (first) seg0 = step;
     }
-    // The next sequence with units (B: none).  Out of line: the roles call it once a sequence and share the
-    // instruction cache.
-    static __device__ __noinline__ int next_seq(const TreeArgs &a, int b) {
+    // The next sequence with units (B: none) and the tiles in between.  Out of line: the roles call it once a
+    // sequence and share the instruction cache.
+    static __device__ __noinline__ int2 next_seq(const TreeArgs &a, int b) {
+        int skipped = 0;
         while (++b < a.B) {
             const Seq n = seq_of(a, b);
             if (n.steps > 0 && n.tiles > 0) break;
+            skipped += n.tiles;
         }
-        return b;
+        return make_int2(b, skipped);
     }
 };
 
@@ -186,7 +196,8 @@ __device__ __forceinline__ int pair_of_unit(long long u, long long U, int pairs)
 }
 
 // The pair's run: every CTA scans the batch's tiles and units (two passes where the batch is larger than
-// the block); pair 0 also leaves the offsets for the join.  One sequence that is no tree refuses all.
+// the block); pair 0 also leaves the offsets for the join.  One sequence that is no tree refuses all: no
+// units, and no tiles for the join.
 template <int THREADS>
 __device__ __noinline__ void schedule(const TreeArgs &a, const TreePlan &pl, int pair, uint32_t rank, Ctrl *c) {
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
@@ -224,63 +235,77 @@ __device__ __noinline__ void schedule(const TreeArgs &a, const TreePlan &pl, int
     const bool report = pair == 0 && rank == 0;
     if (tid == 0) c->w_n = 0;
     bool bad = false, bad_len = false;
-    long long U = 0;
-    for (int b0 = 0; b0 < a.B; b0 += THREADS) {
-        const int b = b0 + tid;
-        long long u = 0, all_u;
-        int t = 0, all_t;
-        if (b < a.B) {
-            TreeSpan sp;
-            if (!tree_span(a.cu, b, a.B, a.T, a.max_nodes, &sp)) {
-                bad = true;
-            } else {
-                const Seq s = seq_of(a, b);
-                bad_len |= s.n > 0 && s.steps == 0;
-                u = (long long)s.tiles * s.steps;
+    auto read = [&](int b, Seq &q, long long &u, int &t) {  // sequence b's units and tiles; 0 behind the batch
+        u = 0;
+        t = 0;
+        TreeSpan sp;
+        if (b >= a.B) return;
+        if (!tree_span(a.cu, b, a.B, a.T, a.max_nodes, &sp)) {
+            bad = true;
+            return;
+        }
+        q = seq_of(a, b);
+        bad_len |= q.n > 0 && q.steps == 0;
+        t = q.tiles;
+        u = (long long)t * q.steps;
+    };
+    // Sequence b with `mine` units up to the inclusive sums u1 and t1: the pair's start if it lies there.
+    auto place = [&](int b, const Seq &q, long long u1, long long mine, int t1, long long U, bool refuse) {
+        const long long s0 = unit_start(pair, U, pl.pairs), s1 = unit_start(pair + 1, U, pl.pairs), u0 = u1 - mine;
+        if (b >= a.B) return;
+        if (!refuse && mine > 0 && u0 <= s0 && s0 < u1 && s1 > s0) {
+            c->w_b = b;
+            c->w_tile = (int)((s0 - u0) / q.steps);
+            c->w_step = (int)((s0 - u0) % q.steps);
+            c->w_n = (int)(s1 - s0);
+            c->w_tg = t1 - q.tiles + c->w_tile;
+            c->w_units = U;
+        }
+        if (report) {
+            if (!refuse && q.steps == 0)  // nobody's: the join writes 0 and -inf
+                for (int t = 0; t < q.tiles; ++t)
+                    pl.tile[t1 - q.tiles + t] = make_int4(q.t0 * a.n_h + t * TILE, q.n * a.n_h - t * TILE, 0, 0);
+            if (b == a.B - 1) {
+                *pl.units = refuse ? 0 : U;
+                *pl.tiles = refuse ? 0 : t1;
             }
         }
-        block_scan(u, t, all_u, all_t);
-        U += all_u;
-    }
-    bad = __syncthreads_or(bad);
-    if (bad) U = 0;
-    if (report && (bad || bad_len)) record_error(a.err, bad ? kErrBadTree : kErrBadSeqLen);
-    const long long s0 = unit_start(pair, U, pl.pairs), s1 = unit_start(pair + 1, U, pl.pairs);
-    long long cu = 0;
-    int ct = 0;
-    for (int b0 = 0; b0 < a.B; b0 += THREADS) {
-        const int b = b0 + tid;
-        Seq s;
-        long long u = 0, all_u;
-        int t = 0, all_t;
-        if (b < a.B && !bad) {
-            s = seq_of(a, b);
-            u = (long long)s.tiles * s.steps;
-            t = s.tiles;
-        }
+    };
+    Seq q = {};
+    if (a.B <= THREADS) {  // one pass, every length read once
+        long long u, all_u;
+        int t, all_t;
+        read(tid, q, u, t);
         const long long mine = u;
-        const int mine_t = t;
         block_scan(u, t, all_u, all_t);
-        const long long u0 = cu + u - mine;
-        if (b < a.B) {
-            if (mine > 0 && u0 <= s0 && s0 < u0 + mine && s1 > s0) {
-                c->w_b = b;
-                c->w_tile = (int)((s0 - u0) / s.steps);
-                c->w_step = (int)((s0 - u0) % s.steps);
-                c->w_n = (int)(s1 - s0);
-            }
-            if (report) {
-                pl.unit_off[b] = u0;
-                pl.tile_off[b] = ct + t - mine_t;
-            }
+        bad = __syncthreads_or(bad);
+        place(tid, q, u, mine, t, bad ? 0 : all_u, bad);
+    } else {
+        long long U = 0;
+        for (int b0 = 0; b0 < a.B; b0 += THREADS) {
+            long long u, all_u;
+            int t, all_t;
+            read(b0 + tid, q, u, t);
+            block_scan(u, t, all_u, all_t);
+            U += all_u;
         }
-        cu += all_u;
-        ct += all_t;
+        bad = __syncthreads_or(bad);
+        const bool refuse = bad;
+        long long cu = 0;
+        int ct = 0;
+        for (int b0 = 0; b0 < a.B; b0 += THREADS) {
+            long long u, all_u;
+            int t, all_t;
+            read(b0 + tid, q, u, t);
+            const long long mine = u;
+            block_scan(u, t, all_u, all_t);
+            place(b0 + tid, q, cu + u, mine, ct + t, refuse ? 0 : U, refuse);
+            cu += all_u;
+            ct += all_t;
+        }
+        bad = refuse;
     }
-    if (report && tid == 0) {
-        pl.unit_off[a.B] = U;
-        pl.tile_off[a.B] = ct;
-    }
+    if (report && (bad || bad_len)) record_error(a.err, bad ? kErrBadTree : kErrBadSeqLen);
     __syncthreads();
 }
 
@@ -641,7 +666,6 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 const int j0 = (it.step * SPG + (v >> 1)) * PG;
                 if (j0 + PG <= it.s.ctx) continue;
                 const bool good = wait(bar(ctrl->land[st.i]), (land_ph >> st.i) & 1u, abort_flag);
-                if (!(ok = !named_red_or(!good, BAR_CLEAN, CLEAN_THREADS))) break;
                 land_ph ^= 1u << st.i;
                 const uint32_t base = data_s + V_OFF + st.i * STAGE + (t & 8) / 8 * CB + (t & 7) * 16;
 #pragma unroll
@@ -662,7 +686,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     if (hit && j >= it.s.ctx) st_shared_v4(at, x[0], x[1], x[2], x[3]);
                 }
                 fence_proxy_async_smem();
-                asm volatile("bar.sync %0, %1;" ::"n"(BAR_CLEAN), "n"(CLEAN_THREADS) : "memory");
+                if (!(ok = !named_red_or(!good, BAR_CLEAN, CLEAN_THREADS))) break;
                 if (t == 0) mbar_arrive_pair(lead(ctrl->v_full[st.i]));
             }
             it.next(a);
@@ -832,8 +856,17 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 const bool whole = it.seg0 == 0 && it.step == it.s.steps - 1;
                 const int slot = 2 * pair + (it.head ? 0 : 1);
                 const float inv = total == 0.f ? 0.f : 1.f / total;
-                const int row0 = row - lane;  // this warp's 32 rows, of the sequence and of the CTA
-                const int crow0 = (warp & 1) * 32;
+                const int row0 = row - lane;  // this warp's first row of the sequence
+                if (it.seg0 == 0 && rank == 0 && warp == SM_WARP0 && lane == 0) {  // the tile's first segment tells the join
+                    const int rest = it.s.steps - 1 - it.step;  // steps behind this segment: the pairs that hold them
+                    int n = 1;
+                    if (rest > 0) {
+                        const long long U = ctrl->w_units, u1 = unit_start(pair + 1, U, pl.pairs) + rest - 1;
+                        n = pair_of_unit(u1, U, pl.pairs) - pair + 1;
+                    }
+                    pl.tile[it.tg] = make_int4(it.s.t0 * a.n_h + it.tile * TILE, it.s.n * a.n_h - it.tile * TILE, pair,
+                                               it.head ? n : -n);
+                }
                 if (pg == 0) {
                     if (!whole) {
                         pl.m[slot * TILE + (int)rank * HALF + r] = m;
@@ -843,47 +876,57 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                             total == 0.f ? -INFINITY : (base + log2f(total)) * 0.69314718055994531f;
                     }
                 }
-                // O's rows pass through 2 KB of P (its MMAs are done) a warp, 64 bytes of each of the 32 rows at a time, so
-                // that a store instruction writes whole sectors of eight rows instead of 16 bytes of 32
-                const bool narrow = whole && a.out_bf16;
-                const size_t width = narrow ? DC * 2 : DC * 4;
-                char *dst = whole ? reinterpret_cast<char *>(a.o) + ((size_t)it.s.t0 * a.n_h + row0) * width
-                                  : reinterpret_cast<char *>(pl.o) + ((size_t)slot * TILE + rank * HALF + crow0) * width;
-                dst += (cg * 256 + half * 128) * (narrow ? 2 : 4);
-                const int rows_left = whole ? it.s.n * a.n_h - row0 : 32;
-                const float mul = whole ? inv : 1.f;
-                const uint32_t mine_s = stage + lane * 64, key = (lane >> 1) & 3;
+                if (!whole) {  // partial rows: [slot][row / 8][column][row % 8]; a warp's store is a column of 32 rows
+                    float *dst = pl.o + (((size_t)slot * (TILE / 8) + ((int)rank * HALF + r) / 8) * DC + cg * 256 + half * 128) * 8 + (r & 7);
 #pragma unroll 1
-                for (int c = 0; c < 8; ++c) {  // 16 of the 128 columns
-                    uint32_t o[16];
-                    tmem_ld16(tmem + lane_base + O_COL + cg * 128 + c * 16, o);
-                    tmem_wait_ld();
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t o[32];
+                        tmem_ld32(tmem + lane_base + O_COL + cg * 128 + c * 32, o);
+                        tmem_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * mul);
-                    if (narrow) {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            o[i] = pack_bf16x2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1]));
+                        for (int i = 0; i < 32; ++i) __stcg(dst + (c * 32 + i) * 8, __uint_as_float(o[i]));
                     }
+                } else {
+                    // O's rows pass through 2 KB of P (its MMAs are done) a warp, 64 bytes of each of the 32 rows at a
+                    // time, so that a store instruction writes whole sectors of eight rows, not 16 bytes of 32
+                    const bool narrow = a.out_bf16;
+                    const size_t width = narrow ? DC * 2 : DC * 4;
+                    char *dst = reinterpret_cast<char *>(a.o) + ((size_t)it.s.t0 * a.n_h + row0) * width +
+                                (cg * 256 + half * 128) * (narrow ? 2 : 4);
+                    const int rows_left = it.s.n * a.n_h - row0;
+                    const uint32_t mine_s = stage + lane * 64, key = (lane >> 1) & 3;
+#pragma unroll 1
+                    for (int c = 0; c < 8; ++c) {  // 16 of the 128 columns
+                        uint32_t o[16];
+                        tmem_ld16(tmem + lane_base + O_COL + cg * 128 + c * 16, o);
+                        tmem_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (i < 2 || !narrow)
-                            st_shared_v4(mine_s + ((((narrow ? 2 * (c & 1) : 0) + i) ^ key) << 4), o[4 * i], o[4 * i + 1],
-                                         o[4 * i + 2], o[4 * i + 3]);
-                    if (narrow && !(c & 1)) continue;
-                    __syncwarp();
+                        for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * inv);
+                        if (narrow) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int rr = 8 * i + (lane >> 2), ch = lane & 3;
-                        uint32_t x[4];
-                        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                                     : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
-                                     : "r"(stage + rr * 64 + ((ch ^ ((rr >> 1) & 3)) << 4)));
-                        if (rr < rows_left)
-                            *reinterpret_cast<uint4 *>(dst + rr * width + (narrow ? c >> 1 : c) * 64 + ch * 16) =
-                                make_uint4(x[0], x[1], x[2], x[3]);
+                            for (int i = 0; i < 8; ++i)
+                                o[i] = pack_bf16x2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1]));
+                        }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (i < 2 || !narrow)
+                                st_shared_v4(mine_s + ((((narrow ? 2 * (c & 1) : 0) + i) ^ key) << 4), o[4 * i], o[4 * i + 1],
+                                             o[4 * i + 2], o[4 * i + 3]);
+                        if (narrow && !(c & 1)) continue;
+                        __syncwarp();
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int rr = 8 * i + (lane >> 2), ch = lane & 3;
+                            uint32_t x[4];
+                            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                         : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+                                         : "r"(stage + rr * 64 + ((ch ^ ((rr >> 1) & 3)) << 4)));
+                            if (rr < rows_left)
+                                *reinterpret_cast<uint4 *>(dst + rr * width + (narrow ? c >> 1 : c) * 64 + ch * 16) =
+                                    make_uint4(x[0], x[1], x[2], x[3]);
+                        }
+                        __syncwarp();
                     }
-                    __syncwarp();
                 }
             }
             it.next(a);
@@ -908,86 +951,92 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     }
 }
 
-// Joins the tiles that lie in several pairs' runs: o = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s, a warp
-// per row.  The lanes find the row's slots and weights side by side, so that the partial rows are read
-// without waiting for one another.  Rows of a sequence without steps (a bad length) are 0 and -inf.
-constexpr int JOIN_ROWS = 8, JOIN_MAX = 4;  // slots a lane; up to 128 pairs
-__global__ void __launch_bounds__(JOIN_ROWS * 32)
+// Joins the tiles that lie in several pairs' runs: o = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s.  A block
+// takes eight rows, 16 contiguous KB of a slot's partials; a thread four of the rows in four columns.  The
+// block finds the slots and weights of its rows side by side first, so that the partials are read without
+// waiting for one another, and turns the sums in shared memory to write whole rows.  Rows of a sequence without steps (a bad length) are 0 and -inf.
+constexpr int JOIN_ROWS = 8, JOIN_THREADS = 256, JOIN_SLOTS = 128, JOIN_PAD = DC + 4;
+__global__ void __launch_bounds__(JOIN_THREADS)
 tree_tc_join_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ TreePlan pl) {
+    __shared__ __align__(16) float weight[JOIN_SLOTS][JOIN_ROWS];
+    __shared__ __align__(16) float sums[JOIN_ROWS][JOIN_PAD];
+    __shared__ int slots[JOIN_SLOTS];
+    pdl_trigger();
     pdl_wait();
-    const int g = blockIdx.x, lane = threadIdx.x & 31;
-    if (g >= pl.tile_off[a.B]) return;
-    int lo = 0, hi = a.B;  // the last b with tile_off[b] <= g: the one that holds it, empty ones come before
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (pl.tile_off[mid] <= g) lo = mid;
-        else hi = mid;
+    const int g = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (g >= *pl.tiles) return;
+    const int4 t = pl.tile[g];
+    const long long U = *pl.units;
+    const int r0 = blockIdx.y * JOIN_ROWS, left = t.y, c0 = t.z, n = abs(t.w);
+    if (r0 >= left || n == 1) return;
+    for (int i = tid; i < n; i += JOIN_THREADS) {
+        const int c = c0 + i;  // a pair without units left nothing; the first pair may have begun with another tile
+        slots[i] = unit_start(c, U, pl.pairs) == unit_start(c + 1, U, pl.pairs) ? -1 : 2 * c + (i == 0 && t.w < 0);
     }
-    const Seq s = seq_of(a, lo);
-    const int tile = g - pl.tile_off[lo], rr = blockIdx.y * JOIN_ROWS + (threadIdx.x >> 5), row = tile * TILE + rr;
-    if (row >= s.n * a.n_h) return;
-    const long long U = pl.unit_off[a.B], u0 = pl.unit_off[lo] + (long long)tile * s.steps;
-    int c0 = 0, c1 = -1;
-    if (s.steps > 0) {
-        c0 = pair_of_unit(u0, U, pl.pairs);
-        c1 = pair_of_unit(u0 + s.steps - 1, U, pl.pairs);
-        if (c0 == c1) return;
-    }
-    const bool behind = s.steps > 0 && unit_start(c0, U, pl.pairs) != u0;  // the tile is not its first pair's first
-    const int n = c1 - c0 + 1;
-    float m[JOIN_MAX], l = 0.f, M = -INFINITY;
-#pragma unroll
-    for (int k = 0; k < JOIN_MAX; ++k) {
-        const int i = k * 32 + lane, c = c0 + i;
-        m[k] = -INFINITY;
-        if (i < n && unit_start(c, U, pl.pairs) != unit_start(c + 1, U, pl.pairs))  // a pair without units left nothing
-            m[k] = pl.m[(2 * c + (i == 0 && behind)) * TILE + rr];
-        M = fmaxf(M, m[k]);
+    __syncthreads();
+    // a warp per row: its maximum, weights and sum
+    const size_t grow = (size_t)t.x + r0 + warp;
+    float M = -INFINITY, l = 0.f;
+    for (int i = lane; i < n; i += 32) {
+        const float m = slots[i] < 0 ? -INFINITY : pl.m[slots[i] * TILE + r0 + warp];
+        if (i < 32 && slots[i] >= 0) l = pl.l[slots[i] * TILE + r0 + warp];  // on its way beside m
+        weight[i][warp] = m;
+        M = fmaxf(M, m);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
     const float base = M == -INFINITY ? 0.f : M;
-#pragma unroll
-    for (int k = 0; k < JOIN_MAX; ++k) {
-        const int i = k * 32 + lane;
-        m[k] = exp2f(m[k] - base);  // the slot's weight
-        if (m[k] != 0.f) l += m[k] * pl.l[(2 * (c0 + i) + (i == 0 && behind)) * TILE + rr];
+    float sum = 0.f;
+    for (int i = lane; i < n; i += 32) {
+        const float w = exp2f(weight[i][warp] - base);
+        weight[i][warp] = w;
+        if (w != 0.f) sum += w * (i < 32 ? l : pl.l[slots[i] * TILE + r0 + warp]);
     }
+    l = sum;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    float acc[16];
+    __syncwarp();
+    if (l != 0.f) {
+        for (int i = lane; i < n; i += 32) weight[i][warp] /= l;
+    }
+    if (a.lse && lane == 0 && r0 + warp < left) a.lse[grow] = l == 0.f ? -INFINITY : (base + log2f(l)) * 0.69314718055994531f;
+    __syncthreads();
+    const int quad = (tid & 1) * 4, col = tid >> 1;  // rows quad .. quad + 3, columns col + 128 k
+    float4 acc[4];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) acc[i] = 0.f;
-#pragma unroll
-    for (int k = 0; k < JOIN_MAX; ++k) {
+    for (int k = 0; k < 4; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 2
-        for (int i = 0; i < 32 && k * 32 + i < n; ++i) {
-            const float w = __shfl_sync(0xffffffffu, m[k], i);
-            if (w == 0.f) continue;
-            const int sl = 2 * (c0 + k * 32 + i) + (k == 0 && i == 0 && behind);
-            const float4 *src = reinterpret_cast<const float4 *>(pl.o + ((size_t)sl * TILE + rr) * DC);
+    for (int i = 0; i < n; ++i) {
+        if (slots[i] < 0) continue;
+        const float4 w = *reinterpret_cast<const float4 *>(&weight[i][quad]);
+        const float4 *src = reinterpret_cast<const float4 *>(
+            pl.o + (((size_t)slots[i] * (TILE / 8) + r0 / 8) * DC + col) * 8 + quad);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const float4 x = src[q * 32 + lane];
-                acc[4 * q] = fmaf(w, x.x, acc[4 * q]);
-                acc[4 * q + 1] = fmaf(w, x.y, acc[4 * q + 1]);
-                acc[4 * q + 2] = fmaf(w, x.z, acc[4 * q + 2]);
-                acc[4 * q + 3] = fmaf(w, x.w, acc[4 * q + 3]);
-            }
+        for (int k = 0; k < 4; ++k) {
+            const float4 x = __ldcg(src + k * 128 * 2);
+            acc[k].x = w.x == 0.f ? acc[k].x : fmaf(w.x, x.x, acc[k].x);
+            acc[k].y = w.y == 0.f ? acc[k].y : fmaf(w.y, x.y, acc[k].y);
+            acc[k].z = w.z == 0.f ? acc[k].z : fmaf(w.z, x.z, acc[k].z);
+            acc[k].w = w.w == 0.f ? acc[k].w : fmaf(w.w, x.w, acc[k].w);
         }
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    const size_t grow = (size_t)s.t0 * a.n_h + row;
-    if (a.lse && lane == 0) a.lse[grow] = l == 0.f ? -INFINITY : (base + log2f(l)) * 0.69314718055994531f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int k = 0; k < 4; ++k) {
+        sums[quad][col + 128 * k] = acc[k].x;
+        sums[quad + 1][col + 128 * k] = acc[k].y;
+        sums[quad + 2][col + 128 * k] = acc[k].z;
+        sums[quad + 3][col + 128 * k] = acc[k].w;
+    }
+    __syncthreads();
+    if (r0 + warp >= left) return;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {  // a warp per row
+        const float4 x = *reinterpret_cast<const float4 *>(&sums[warp][4 * lane + 128 * k]);
         if (a.out_bf16)
-            reinterpret_cast<uint2 *>(reinterpret_cast<__nv_bfloat16 *>(a.o) + grow * DC)[i * 32 + lane] =
-                make_uint2(pack_bf16x2(acc[4 * i] * inv, acc[4 * i + 1] * inv),
-                           pack_bf16x2(acc[4 * i + 2] * inv, acc[4 * i + 3] * inv));
+            reinterpret_cast<uint2 *>(reinterpret_cast<__nv_bfloat16 *>(a.o) + grow * DC)[lane + 32 * k] =
+                make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
         else
-            reinterpret_cast<float4 *>(reinterpret_cast<float *>(a.o) + grow * DC)[i * 32 + lane] =
-                make_float4(acc[4 * i] * inv, acc[4 * i + 1] * inv, acc[4 * i + 2] * inv, acc[4 * i + 3] * inv);
+            reinterpret_cast<float4 *>(reinterpret_cast<float *>(a.o) + grow * DC)[lane + 32 * k] = x;
     }
 }
 
@@ -1022,10 +1071,13 @@ int tree_pairs() {
         }
         if (most == 0 || n < most) most = n;
     }
-    return known[dev] = most < 32 * JOIN_MAX ? most : 32 * JOIN_MAX;
+    return known[dev] = most < JOIN_SLOTS ? most : JOIN_SLOTS;
 }
 
-size_t tree_tc_layout(int pairs, int B, char *base, TreePlan *pl) {
+// Tiles of a batch at most: a sequence's last one may be part-filled.
+int64_t tree_tiles(int B, int64_t rows) { return B + rows / TILE; }
+
+size_t tree_tc_layout(int pairs, int B, int64_t rows, char *base, TreePlan *pl) {
     size_t off = 0;
     auto take = [&](size_t bytes) {
         char *p = base ? base + off : nullptr;
@@ -1034,8 +1086,9 @@ size_t tree_tc_layout(int pairs, int B, char *base, TreePlan *pl) {
     };
     TreePlan t;
     t.pairs = pairs;
-    t.unit_off = reinterpret_cast<long long *>(take(((size_t)B + 1) * sizeof(long long)));
-    t.tile_off = reinterpret_cast<int *>(take(((size_t)B + 1) * sizeof(int)));
+    t.units = reinterpret_cast<long long *>(take(sizeof(long long)));
+    t.tiles = reinterpret_cast<int *>(take(sizeof(int)));
+    t.tile = reinterpret_cast<int4 *>(take((size_t)tree_tiles(B, rows) * sizeof(int4)));
     t.o = reinterpret_cast<float *>(take((size_t)2 * pairs * TILE * DC * sizeof(float)));
     t.m = reinterpret_cast<float *>(take((size_t)2 * pairs * TILE * sizeof(float)));
     t.l = reinterpret_cast<float *>(take((size_t)2 * pairs * TILE * sizeof(float)));
@@ -1050,16 +1103,16 @@ bool tree_tc_supported(const mla_dims_t &d) {
            (d.kv_dtype == MLA_DTYPE_BF16 || d.kv_dtype == MLA_DTYPE_FP8_E4M3) && !(d.flags & MLA_FLAG_SIMT_DECODE);
 }
 
-size_t tree_tc_workspace_bytes(int B) {
+size_t tree_tc_workspace_bytes(const mla_dims_t &d, int B, int T) {
     const int pairs = tree_pairs();
-    return pairs < 1 ? 0 : tree_tc_layout(pairs, B, nullptr, nullptr);
+    return pairs < 1 ? 0 : tree_tc_layout(pairs, B, (int64_t)T * d.n_h, nullptr, nullptr);
 }
 
 cudaError_t launch_tree_tc(const mla_dims_t &d, const TreeArgs &a, void *ws, cudaStream_t st) {
     const int pairs = tree_pairs();
     if (pairs < 1) return cudaErrorNotSupported;
     TreePlan pl;
-    tree_tc_layout(pairs, a.B, reinterpret_cast<char *>(ws), &pl);
+    tree_tc_layout(pairs, a.B, (int64_t)a.T * a.n_h, reinterpret_cast<char *>(ws), &pl);
     const uint64_t pool_rows = (uint64_t)a.num_blocks * PG, q_rows = (uint64_t)a.T * a.n_h;
     const bool f8 = d.kv_dtype == MLA_DTYPE_FP8_E4M3;
     CUtensorMap tm_q, tm_k, tm_v, tm_c;
@@ -1083,9 +1136,8 @@ cudaError_t launch_tree_tc(const mla_dims_t &d, const TreeArgs &a, void *ws, cud
     cudaError_t e = f8 ? cudaLaunchKernelEx(&cfg, tree_tc_kernel<true>, tm_q, tm_k, tm_v, tm_c, a, pl)
                        : cudaLaunchKernelEx(&cfg, tree_tc_kernel<false>, tm_q, tm_k, tm_v, tm_c, a, pl);
     if (e != cudaSuccess) return e;
-    const int64_t tiles = a.B + q_rows / TILE;  // at most: a sequence's last tile may be part-filled
-    cfg.gridDim = dim3((unsigned)tiles, TILE / JOIN_ROWS);
-    cfg.blockDim = dim3(JOIN_ROWS * 32);
+    cfg.gridDim = dim3((unsigned)tree_tiles(a.B, (int64_t)q_rows), TILE / JOIN_ROWS);
+    cfg.blockDim = dim3(JOIN_THREADS);
     cfg.dynamicSmemBytes = 0;
     return cudaLaunchKernelEx(&cfg, tree_tc_join_kernel, a, pl);
 }
