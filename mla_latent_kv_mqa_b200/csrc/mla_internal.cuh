@@ -48,8 +48,10 @@ struct RopeFreqs {
     double base;
     int d_r;
 };
-inline RopeFreqs make_rope_freqs(double base, int d_r) {
-    RopeFreqs f = {};
+inline const RopeFreqs &make_rope_freqs(double base, int d_r) {
+    thread_local RopeFreqs f = {};  // the last one asked for: a model's calls ask for the same, 32 pow each
+    if (f.base == base && f.d_r == d_r) return f;
+    f = {};
     f.base = base;
     f.d_r = d_r;
     for (int k = 0; k < kRopeTab && k < d_r / 2; ++k) f.inv_freq[k] = pow(base, -(double)(2 * k) / (double)d_r);

@@ -112,6 +112,11 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
                      : "memory");
 }
+__device__ __forceinline__ float ld_cluster_f32(uint32_t remote_addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(remote_addr) : "memory");
+    return v;
+}
 // 16-byte store into another CTA's shared memory; completes `bytes` on its mbarrier.
 __device__ __forceinline__ void st_async_v4(uint32_t remote_addr, uint32_t a, uint32_t b, uint32_t c,
                                             uint32_t d, uint32_t remote_bar) {

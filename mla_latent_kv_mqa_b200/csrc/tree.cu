@@ -11,6 +11,7 @@
 #include <math.h>
 
 #include "mla_internal.cuh"
+#include "sm100.cuh"
 #include "tree.cuh"
 
 namespace mla {
@@ -179,7 +180,7 @@ __device__ __forceinline__ float load_cache(const TreeArgs &a, size_t slot, int 
     return __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(a.kr_pool)[slot * d_r + (k - d_c)]);
 }
 
-template <typename Ta, int KV, int NC>
+template <typename Ta, int KV, int NC, bool JOIN>
 __global__ void __launch_bounds__(kHeads * 32)
 tree_simt_kernel(const __grid_constant__ TreeArgs a, int seg_len, int n_split, TreePartials part) {
     dependent_start();
@@ -251,18 +252,65 @@ tree_simt_kernel(const __grid_constant__ TreeArgs a, int seg_len, int n_split, T
                 if (lane + 32 * q < a.d_c) o[q] = fmaf(pj, kvr[lane + 32 * q], o[q]);
         }
     }
-    if (h >= a.n_h) return;
+    if (!JOIN) {
+        if (h >= a.n_h) return;
+#pragma unroll
+        for (int q = 0; q < NC; ++q)
+            if (lane + 32 * q < a.d_c) part.o[pr * a.d_c + lane + 32 * q] = o[q];
+        if (lane == 0) {
+            part.m[pr] = m;
+            part.l[pr] = l;
+        }
+        return;
+    }
+    // The segments' blocks are a cluster: each leaves (o, m, l) in the place of its queries, and joins its
+    // share of the columns over all of them.
 #pragma unroll
     for (int q = 0; q < NC; ++q)
-        if (lane + 32 * q < a.d_c) part.o[pr * a.d_c + lane + 32 * q] = o[q];
+        if (lane + 32 * q < a.d_c) q_s[warp * row + lane + 32 * q] = o[q];
     if (lane == 0) {
-        part.m[pr] = m;
-        part.l[pr] = l;
+        q_s[warp * row + a.d_c] = m;
+        q_s[warp * row + a.d_c + 1] = l;
     }
+    sm100::cluster_sync();
+    if (h < a.n_h) {
+        const uint32_t mine = sm100::smem_u32(q_s + warp * row);
+        float w = 0.f, mk = -INFINITY, lk = 0.f;  // lane k: segment k
+        if (lane < n_split) {
+            const uint32_t at = sm100::mapa(mine, lane) + 4 * a.d_c;
+            mk = sm100::ld_cluster_f32(at);
+            lk = sm100::ld_cluster_f32(at + 4);
+        }
+        float M = mk;
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+        const float base = M == -INFINITY ? 0.f : M;
+        w = exp2f(mk - base);
+        float total = w == 0.f ? 0.f : w * lk;
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
+        const float inv = total == 0.f ? 0.f : 1.f / total;
+        const size_t r = (size_t)t * a.n_h + h;
+        const int share = (a.d_c + n_split - 1) / n_split, c1 = min(a.d_c, share * (split + 1));
+        for (int c0 = share * split; c0 < c1; c0 += 32) {
+            float acc = 0.f;
+            for (int k = 0; k < n_split; ++k) {
+                const float wk = __shfl_sync(0xffffffffu, w, k);
+                if (wk != 0.f && c0 + lane < c1)
+                    acc = fmaf(wk, sm100::ld_cluster_f32(sm100::mapa(mine, k) + 4 * (c0 + lane)), acc);
+            }
+            if (c0 + lane < c1) {
+                if (a.out_bf16) reinterpret_cast<__nv_bfloat16 *>(a.o)[r * a.d_c + c0 + lane] = __float2bfloat16_rn(acc * inv);
+                else reinterpret_cast<float *>(a.o)[r * a.d_c + c0 + lane] = acc * inv;
+            }
+        }
+        if (a.lse && split == 0 && lane == 0) a.lse[r] = total == 0.f ? -INFINITY : (base + log2f(total)) * 0.69314718055994531f;
+    }
+    sm100::cluster_sync();  // no block leaves while another reads its sums
 }
 
-// Joins a row's segments: o = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s.  A segment without a
-// visible token (m = -inf) has weight 0 and is not read.
+// More segments than a cluster has blocks: joins a row's partials, o = sum_s 2^(m_s - M) o_s /
+// sum_s 2^(m_s - M) l_s.  A segment without a visible token (m = -inf) has weight 0 and is not read.
 constexpr int kJoinThreads = 128;
 template <typename To>
 __global__ void __launch_bounds__(kJoinThreads)
@@ -295,50 +343,66 @@ int sm_count() {
     return n;
 }
 
-// Segments of the token axis: enough blocks for four on every SM, a tile of tokens at least.
+// Segments of the token axis: enough blocks for four on every SM, a tile of tokens at least.  Up to
+// kClusterSegs of them are a cluster that joins them itself (one launch: 17 us a call of the toy layer became
+// 13); more only where even so many leave half of the SMs without a block.
+constexpr int kClusterSegs = 8;
 struct TreeSimtPlan {
     int n_split, seg_len;
+    bool join;  // in the cluster
 };
 TreeSimtPlan tree_simt_plan(const mla_dims_t &d, int T, int max_seq_len) {
-    const int64_t blocks = (int64_t)T * ((d.n_h + kHeads - 1) / kHeads), target = 4 * sm_count();
+    const int sms = sm_count();
+    const int64_t blocks = (int64_t)T * ((d.n_h + kHeads - 1) / kHeads), target = 4 * sms;
     const int tiles = (max_seq_len - 1) / kTile + 1;
     int64_t n = blocks > 0 ? (target + blocks - 1) / blocks : 1;
     if (n > tiles) n = tiles;
+    if (n > kClusterSegs && blocks * kClusterSegs * 2 >= sms) n = kClusterSegs;
     const int seg = (int)((tiles + n - 1) / n) * kTile;
-    return {(max_seq_len - 1) / seg + 1, seg};
+    const int n_split = (max_seq_len - 1) / seg + 1;
+    return {n_split, seg, n_split <= kClusterSegs};
 }
 
 }  // namespace
 
 size_t tree_simt_workspace_bytes(const mla_dims_t &d, int T, int max_seq_len) {
-    const size_t rows = (size_t)tree_simt_plan(d, T, max_seq_len).n_split * T * d.n_h;
+    const TreeSimtPlan pl = tree_simt_plan(d, T, max_seq_len);
+    if (pl.join) return 0;
+    const size_t rows = (size_t)pl.n_split * T * d.n_h;
     return align_up(rows * d.d_c * sizeof(float), 256) + 2 * align_up(rows * sizeof(float), 256);
 }
 
 cudaError_t launch_tree_simt(const mla_dims_t &d, const TreeArgs &a, void *ws, cudaStream_t st) {
     const TreeSimtPlan pl = tree_simt_plan(d, a.T, a.max_seq_len);
     const size_t rows = (size_t)pl.n_split * a.T * d.n_h;
-    char *w = reinterpret_cast<char *>(ws);
-    TreePartials part;
-    part.o = reinterpret_cast<float *>(w);
-    w += align_up(rows * d.d_c * sizeof(float), 256);
-    part.m = reinterpret_cast<float *>(w);
-    part.l = reinterpret_cast<float *>(w + align_up(rows * sizeof(float), 256));
+    TreePartials part = {};
+    if (!pl.join) {
+        char *w = reinterpret_cast<char *>(ws);
+        part.o = reinterpret_cast<float *>(w);
+        w += align_up(rows * d.d_c * sizeof(float), 256);
+        part.m = reinterpret_cast<float *>(w);
+        part.l = reinterpret_cast<float *>(w + align_up(rows * sizeof(float), 256));
+    }
     const int row = d.d_c + d.d_r;
     const size_t smem = sizeof(float) * ((size_t)kHeads * row + (size_t)kTile * (row + 1));
     const dim3 grid(a.T, pl.n_split, (d.n_h + kHeads - 1) / kHeads);
     cudaError_t e = cudaSuccess;
     auto run = [&](auto kern) {
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e == cudaSuccess) {
-            e = launch_dependent(kern, grid, kHeads * 32, smem, st, a, pl.seg_len, pl.n_split, part);
-        }
+        if (smem > 48 * 1024) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e == cudaSuccess)
+            e = launch_dependent_cluster(kern, grid, dim3(1, pl.join ? pl.n_split : 1, 1), kHeads * 32, smem, st, a,
+                                         pl.seg_len, pl.n_split, part);
     };
-#define MLA_TREE_SIMT(TA, KV)                                           \
-    do {                                                                \
-        if (d.d_c <= 128) run(tree_simt_kernel<TA, KV, 4>);             \
-        else if (d.d_c <= 512) run(tree_simt_kernel<TA, KV, 16>);       \
-        else run(tree_simt_kernel<TA, KV, 32>);                         \
+#define MLA_TREE_SIMT2(TA, KV, JOIN)                                          \
+    do {                                                                      \
+        if (d.d_c <= 128) run(tree_simt_kernel<TA, KV, 4, JOIN>);             \
+        else if (d.d_c <= 512) run(tree_simt_kernel<TA, KV, 16, JOIN>);       \
+        else run(tree_simt_kernel<TA, KV, 32, JOIN>);                         \
+    } while (0)
+#define MLA_TREE_SIMT(TA, KV)                                                 \
+    do {                                                                      \
+        if (pl.join) MLA_TREE_SIMT2(TA, KV, true);                            \
+        else MLA_TREE_SIMT2(TA, KV, false);                                   \
     } while (0)
     const bool ab = d.act_dtype == MLA_DTYPE_BF16;
     if (d.kv_dtype == MLA_DTYPE_F32) {
@@ -349,7 +413,8 @@ cudaError_t launch_tree_simt(const mla_dims_t &d, const TreeArgs &a, void *ws, c
         if (ab) MLA_TREE_SIMT(__nv_bfloat16, 2); else MLA_TREE_SIMT(float, 2);
     }
 #undef MLA_TREE_SIMT
-    if (e != cudaSuccess) return e;
+#undef MLA_TREE_SIMT2
+    if (e != cudaSuccess || pl.join) return e;
     const dim3 jg(a.T, d.n_h);
     return launch_dependent(a.out_bf16 ? tree_join_kernel<__nv_bfloat16> : tree_join_kernel<float>, jg, kJoinThreads, 0,
                             st, a, pl.n_split, part);

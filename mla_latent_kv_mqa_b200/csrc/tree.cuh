@@ -89,18 +89,27 @@ inline int make_pool_set(const mla_dims_t &d, int tokens, const mla_pool_t *pool
 // A launch as a programmatic dependent of the kernel before it on the stream: the kernel starts with
 // griddepcontrol.wait, so that only its set-up overlaps that kernel.
 template <typename... P, typename... A>
-inline cudaError_t launch_dependent(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, A... args) {
-    cudaLaunchAttribute pdl;
-    pdl.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    pdl.val.programmaticStreamSerializationAllowed = 1;
+inline cudaError_t launch_dependent_cluster(void (*kern)(P...), dim3 grid, dim3 cluster, int threads, size_t smem,
+                                            cudaStream_t st, A... args) {
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster.x;
+    attr[1].val.clusterDim.y = cluster.y;
+    attr[1].val.clusterDim.z = cluster.z;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
-    cfg.attrs = &pdl;
-    cfg.numAttrs = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster.x * cluster.y * cluster.z > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kern, P(args)...);
+}
+template <typename... P, typename... A>
+inline cudaError_t launch_dependent(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, A... args) {
+    return launch_dependent_cluster(kern, grid, dim3(1), threads, smem, st, args...);
 }
 // At the start of such a kernel: dependents of its own may be set up, and what came before is complete.
 __device__ __forceinline__ void dependent_start() {

@@ -233,9 +233,9 @@ class MLADecodeLayer:
         if q_abs.shape[0] != T or B != trees.B:
             raise ValueError("decode_tree: q_abs has a row per node, block_table one per tree")
         if o_lat is None:
-            o_lat = torch.empty((T, d.n_h, d.d_c), dtype=TORCH_ACT[dt], device=q_abs.device)
+            o_lat = q_abs.new_empty((T, d.n_h, d.d_c), dtype=TORCH_ACT[dt])
         if lse is None:
-            lse = torch.empty((T, d.n_h), dtype=torch.float32, device=q_abs.device)
+            lse = q_abs.new_empty((T, d.n_h), dtype=torch.float32)
         if workspace is None:
             workspace = self._tree_ws.get((B, T, max_seq_len), stream,
                                           lambda: N.mla_decode_tree_workspace_size(d, B, T, max_seq_len))

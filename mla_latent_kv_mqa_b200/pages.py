@@ -19,6 +19,31 @@ from . import native as N
 from .layer import Workspace
 
 
+class PageMoves:
+    """Page copies to make, on the device: ``pairs`` [most, 2] of (from, to) and their ``number`` [1].  One buffer
+    holds both; unpacks as (pairs, number)."""
+
+    def __init__(self, most: int, device):
+        self.most = most
+        self._buf = torch.empty((most + 1, 2), dtype=torch.int32, device=device)
+        self.pairs_ptr = self._buf.data_ptr()
+        self.number_ptr = self.pairs_ptr + 8 * most
+
+    @property
+    def pairs(self) -> torch.Tensor:
+        return self._buf[:self.most]
+
+    @property
+    def number(self) -> torch.Tensor:
+        return self._buf[self.most, :1]
+
+    def __iter__(self):
+        return iter((self.pairs, self.number))
+
+    def __getitem__(self, i):
+        return (self.pairs, self.number)[i]
+
+
 class PagedSequences:
     def __init__(self, page_size: int, num_seqs: int, max_blocks: int, num_blocks: int, device="cuda"):
         i32 = dict(dtype=torch.int32, device=device)
@@ -29,7 +54,6 @@ class PagedSequences:
         self._table = N.make_page_table(page_size, num_seqs, max_blocks, num_blocks, self.block_table, self.refs,
                                         self.seq_lens)
         self._ws = Workspace(self.block_table.device)
-        self._i32 = i32
 
     def _workspace(self, n: int, stream):
         return self._ws.get(n, stream, lambda: N.mla_pages_workspace_size(self._table, n))
@@ -43,15 +67,15 @@ class PagedSequences:
         N.mla_pages_fork(self._table, n, parent, child, ws, ws.numel(), stream)
 
     def grow(self, new_lens, seqs=None, stream=None):
-        """Sequences ``seqs`` (default: 0, 1, ...) grow to ``new_lens`` tokens; returns the page copies
-        to make as (moves [n, 2], their number [1]) on the device, for copy_pages."""
+        """Sequences ``seqs`` (default: 0, 1, ...) grow to ``new_lens`` tokens; returns the page copies to
+        make (PageMoves), for copy_pages."""
         n = new_lens.numel()
         if seqs is not None and seqs.numel() != n:
             raise ValueError("grow: a length for every sequence")
         ws = self._workspace(n, stream)
-        moves, count = torch.empty((n, 2), **self._i32), torch.empty(1, **self._i32)
-        N.mla_pages_grow(self._table, n, seqs, new_lens, moves, count, ws, ws.numel(), stream)
-        return moves, count
+        moves = PageMoves(n, self.block_table.device)
+        N.mla_pages_grow(self._table, n, seqs, new_lens, moves.pairs_ptr, moves.number_ptr, ws, ws.numel(), stream)
+        return moves
 
     def trim(self, new_lens, seqs=None, stream=None):
         """Sequences are cut to ``new_lens`` tokens (0: the sequence ends); their pages lose a holder."""
@@ -60,14 +84,18 @@ class PagedSequences:
         N.mla_pages_trim(self._table, new_lens.numel(), seqs, new_lens, stream)
 
     def compact(self, stream=None):
-        """The pages in use take the lowest ids; returns the page copies to make, for copy_pages."""
+        """The pages in use take the lowest ids; returns the page copies to make (PageMoves), for copy_pages."""
         ws = self._workspace(0, stream)
-        moves, count = torch.empty((self.num_blocks // 2, 2), **self._i32), torch.empty(1, **self._i32)
-        N.mla_pages_compact(self._table, moves, count, ws, ws.numel(), stream)
-        return moves, count
+        moves = PageMoves(self.num_blocks // 2, self.block_table.device)
+        N.mla_pages_compact(self._table, moves.pairs_ptr, moves.number_ptr, ws, ws.numel(), stream)
+        return moves
 
     def copy_pages(self, caches, moves, stream=None):
-        """Copy the pages ``moves`` = (pairs, number) names, in every cache."""
-        pairs, count = moves
+        """Copy the pages that ``moves`` names (PageMoves, or a pair of tensors like its), in every cache."""
         pools = N.make_pools([c.pool() for c in caches])
-        N.mla_cache_copy_pages(caches[0].dims, pools, self.num_blocks, pairs, count, pairs.shape[0], stream)
+        if isinstance(moves, PageMoves):
+            pairs, number, most = moves.pairs_ptr, moves.number_ptr, moves.most
+        else:
+            pairs, number = moves
+            most = pairs.shape[0]
+        N.mla_cache_copy_pages(caches[0].dims, pools, self.num_blocks, pairs, number, most, stream)

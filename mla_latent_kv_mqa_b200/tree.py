@@ -49,7 +49,7 @@ class DraftTrees:
         ascending) to behind the committed tokens, in every cache; returns the new lengths."""
         B, max_blocks = block_table.shape
         if new_lens is None:
-            new_lens = torch.empty(B, dtype=torch.int32, device=block_table.device)
+            new_lens = torch.empty_like(seq_lens)
         pools = N.make_pools([c.pool() for c in caches])
         N.mla_cache_keep(caches[0].dims, pools, B, self.cu_nodes, self.total_nodes, block_table, max_blocks,
                          caches[0].num_blocks, seq_lens, keep, num_keep, keep.shape[1], new_lens, stream)
