@@ -422,7 +422,10 @@ mla_status_t mla_tree_append(const mla_dims_t *dims, int T, const void *c_kv, co
  * cache, any number of heads and no MLA_FLAG_SIMT_DECODE (q_abs, pools and o_lat 16-byte aligned, or
  * MLA_ERR_INVALID_ARG); other shapes run on the CUDA cores.
  * Precision: operands as they are (FP8: the codes exactly, the scales in fp32), fp32 accumulation and
- * softmax; on the tensor cores P is rounded to bf16 for the value product, as in mla_decode.
+ * softmax.  On the tensor cores P is rounded to bf16 for the value product, as in mla_decode; over an FP8
+ * cache P times the token's scale to fp16 instead (11 bits; fewer for a token below 2^-16 of the row's
+ * largest, to 2^-27 of it), and a query's content elements below 2^-9 of their row's largest are taken to
+ * 2^-17 of it.  A query row with infinities or NaN gets NaN.
  * Deterministic: the result depends only on the logical cache content. */
 size_t mla_decode_tree_workspace_size(const mla_dims_t *dims, int B, int total_nodes, int max_seq_len);
 mla_status_t mla_decode_tree(const mla_dims_t *dims, int B, const int32_t *cu_nodes, int total_nodes,

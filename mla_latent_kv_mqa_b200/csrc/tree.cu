@@ -252,6 +252,7 @@ tree_simt_kernel(const __grid_constant__ TreeArgs a, int seg_len, int n_split, T
                 if (lane + 32 * q < a.d_c) o[q] = fmaf(pj, kvr[lane + 32 * q], o[q]);
         }
     }
+    if (l != l) m = l;  // scores of NaN move no maximum, and the join drops what has none
     if (!JOIN) {
         if (h >= a.n_h) return;
 #pragma unroll

@@ -22,6 +22,16 @@
 // write P as the MMA's A operand, and at a tile's end write O; four warps clean the V rows that some row
 // of the tile does not see (one warp took 25000 clocks a tile for it).
 //
+// FP8.  K's codes are operands as they are, at twice the rate, against two e4m3 parts of each query, which
+// together are the bf16 query (split_query): no K passes through registers, and S takes as long as in bf16.
+// (Codes converted to bf16 tiles by four more warps: 593 us where this takes 490, and 96 registers a thread
+// for the softmax, which spilled.)  V would need P in parts too, and a part's range is too small for a long
+// context's weights: the cleaning warps turn V's codes into fp16 tiles, exactly, by two instructions for four
+// codes (bf16: eight, 2% slower in all), and P is fp16.  Its 11 bits reach from 2^15 down to 2^-14, so m is
+// chosen to bound P with the tokens' scales in it, and what is below 2^-27 of a row's largest weight times
+// scale loses bits (bf16 would keep 8 of them, where most weights have 11 here).  Content and RoPE scores
+// are apart, since only the first take the token's scale: one buffer of S, no second.
+//
 // Masks.  Steps before ctx need none.  In the others a row's thread selects by its node's bits.  P is 0
 // where a node does not see a token, and 0 times what such a row holds must be 0: the cleaning warps zero
 // the rows behind the sequence, and the infinities and NaN of drafted rows (whoever sees such a row has
@@ -54,27 +64,25 @@ constexpr int DC = 512, ROW = 576, PG = 64, NCB = ROW / 64;
 constexpr int TILE = 128, HALF = 64;              // rows of a tile, and of a CTA
 constexpr int STEP = 256, SPG = STEP / PG;        // tokens and pages of a step
 constexpr int CB = PG * 128;                      // 64 rows x 64 bf16 columns, 128-byte swizzle
-constexpr int STAGE = 2 * CB;                     // K: two pages' column block; V: a page's 128 columns
+constexpr int STAGE = 2 * CB;                     // K: two pages' 128 bytes a row; V: a page's 128 columns
+constexpr int F8_KST = DC / 128 + 1;              // FP8: K stages of a step, the codes' and the RoPE keys'
 constexpr int MAX_STAGES = 4;
 constexpr int P_SLOTS = 2;                        // pages of P held at once
 constexpr int Q_OFF = 0, P_OFF = NCB * CB, K_OFF = P_OFF + P_SLOTS * CB;
-constexpr int RAW = 8192, RAW_STAGES = 2;         // FP8: the codes of a stage, before their conversion
+constexpr int RAW = 8192, RAW_STAGES = 2;         // FP8: the codes of a V stage, before their conversion
 // Shared memory and tensor memory of the bf16 (F8 = false) and FP8 kernels.
 template <bool F8>
 struct Lay {
-    static constexpr int k_stages = F8 ? 3 : 4, v_stages = F8 ? 3 : 4;
-    static constexpr int v_off = K_OFF + k_stages * STAGE;
-    static constexpr int kraw_off = v_off + v_stages * STAGE, vraw_off = kraw_off + RAW_STAGES * RAW;
-    static constexpr int data = F8 ? vraw_off + RAW_STAGES * RAW : kraw_off;
+    static constexpr int k_stages = 4, v_stages = F8 ? 3 : 4;
+    static constexpr int v_off = K_OFF + k_stages * STAGE, vraw_off = v_off + v_stages * STAGE;
+    static constexpr int data = F8 ? vraw_off + RAW_STAGES * RAW : vraw_off;
     static constexpr int s_bufs = F8 ? 1 : 2;     // FP8: content and RoPE scores apart, one buffer of both
 };
 constexpr int DATA = Lay<false>::data;
 static_assert(Lay<true>::data == DATA, "one shared-memory size");
-template <bool F8>
-constexpr int THREADS = F8 ? 640 : 512;
-constexpr int MAX_WARPS = 20;
+constexpr int THREADS = 512, WARPS = THREADS / 32;
 constexpr int LOAD_K_WARP = 0, LOAD_V_WARP = 1, QK_WARP = 2, PV_WARP = 3, SM_WARP0 = 4, CLEAN_WARP0 = 12;
-constexpr int SM_WARPS = 8, SM_THREADS = 32 * SM_WARPS, CLEAN_THREADS = 128;  // FP8: two such groups, for K and for V
+constexpr int SM_WARPS = 8, SM_THREADS = 32 * SM_WARPS, CLEAN_THREADS = 128;
 constexpr uint32_t S_COL = 0, O_COL = 256, TMEM_COLS = 512;
 constexpr float RESCALE_LOG2 = 8.0f;
 constexpr int BAR_MAX = 1, BAR_CLEAN = 2;
@@ -83,8 +91,8 @@ struct __align__(16) Ctrl {
     uint64_t k_full[MAX_STAGES], v_full[MAX_STAGES];    // even CTA: both CTAs' halves are there (landed, cleaned, converted)
     uint64_t k_empty[MAX_STAGES], v_empty[MAX_STAGES];  // each CTA: the MMAs that read the stage are done
     uint64_t land[MAX_STAGES];  // each CTA: a V stage that the cleaning warps have to go over has landed
-    uint64_t kraw_full[RAW_STAGES], kraw_empty[RAW_STAGES], vraw_full[RAW_STAGES], vraw_empty[RAW_STAGES];  // FP8 codes
-    uint64_t q_full, q_empty;
+    uint64_t vraw_full[RAW_STAGES], vraw_empty[RAW_STAGES];  // FP8: each CTA's codes of V
+    uint64_t q_land, q_full, q_empty;  // FP8: each CTA's queries have landed; both CTAs' are operands; read by the MMAs
     uint64_t s_full[2], s_free[2];
     uint64_t p_full[SPG], p_free[SPG];  // a page of P: written / its MMAs done
     // By step parity: O read or rescaled as the step needs / the step's MMAs done.  A CTA may be a step ahead of
@@ -93,9 +101,10 @@ struct __align__(16) Ctrl {
     uint32_t tmem_base, abort;
     int w_b, w_tile, w_step, w_n, w_tg;
     long long w_units;  // of the batch
-    long long scan_u[MAX_WARPS];
-    int scan_t[MAX_WARPS];
+    long long scan_u[WARPS];
+    int scan_t[WARPS];
     alignas(16) float scale[SM_WARPS][2][PG];  // FP8: each softmax warp's page's scales, as they are and with 0 for infinities and NaN
+    float q_unit[2][HALF];  // FP8, by segment parity: what a row's scores are multiples of
     float top[2][SPG][HALF], sum[SPG][HALF];  // by step parity (a thread may be a step behind its partners), page, row
 };
 constexpr int SMEM = 1024 + DATA + (int)((sizeof(Ctrl) + 127) / 128 * 128);
@@ -198,7 +207,6 @@ __device__ __forceinline__ int pair_of_unit(long long u, long long U, int pairs)
 // The pair's run: every CTA scans the batch's tiles and units (two passes where the batch is larger than
 // the block); pair 0 also leaves the offsets for the join.  One sequence that is no tree refuses all: no
 // units, and no tiles for the join.
-template <int THREADS>
 __device__ __noinline__ void schedule(const TreeArgs &a, const TreePlan &pl, int pair, uint32_t rank, Ctrl *c) {
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     auto block_scan = [&](long long &u, int &t, long long &all_u, int &all_t) {  // inclusive
@@ -325,21 +333,74 @@ __device__ __forceinline__ bool named_red_or(bool v, int id, int n) {
     return r != 0;
 }
 
-// Four e4m3 codes (low byte first) to four bf16 values, exactly (NaN stays NaN), through fp16 and fp32: 46
-// clocks for 16 codes of each thread of a warp, loads and stores included, where moving the bits and an
-// exact product take 67.
-__device__ __forceinline__ void e4m3x4_to_bf16x4(uint32_t w, uint32_t &lo, uint32_t &hi) {
-    uint32_t a, b;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(a) : "h"((unsigned short)w));
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(b) : "h"((unsigned short)(w >> 16)));
-    const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&a));
-    const float2 y = __half22float2(*reinterpret_cast<const __half2 *>(&b));
-    lo = pack_bf16x2(x.x, x.y);
-    hi = pack_bf16x2(y.x, y.y);
+// Four e4m3 codes (low byte first) as fp16 values, exactly (NaN stays NaN).
+__device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t w, uint32_t &lo, uint32_t &hi) {
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(lo) : "h"((unsigned short)w));
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(hi) : "h"((unsigned short)(w >> 16)));
 }
-// A pair of bf16 values with 0 for infinities and NaN.
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+// At least log2 of a scale's size, by less than 1 (from -60 on).
+__device__ __forceinline__ int scale_exponent(float s) { return max((int)(__float_as_uint(s) >> 23 & 255u) - 126, -60); }
+// A pair of bf16 values (fp16: EXP = 0x7c00) with 0 for infinities and NaN.
+template <uint32_t EXP = 0x7f80u>
 __device__ __forceinline__ uint32_t finite_pair(uint32_t x) {
-    return x & ((x & 0x7f80u) == 0x7f80u ? 0xffff0000u : 0xffffffffu) & ((x & 0x7f800000u) == 0x7f800000u ? 0xffffu : 0xffffffffu);
+    return x & ((x & EXP) == EXP ? 0xffff0000u : 0xffffffffu) & ((x & (EXP << 16)) == (EXP << 16) ? 0xffffu : 0xffffffffu);
+}
+
+__device__ __forceinline__ void ld_shared_v4(uint32_t at, uint32_t *x) {
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(at));
+}
+
+// FP8: a landed query row (nine blocks of 64 bf16 columns) becomes, in place, 2^k times itself as e4m3 operands
+// against the codes: of the row's 128 columns from 128 i, the nearest codes in block 2 i and the codes of
+// what is left in block 2 i + 1; the RoPE columns stay bf16.  2^k puts the row's largest content element in
+// [128, 256).  A bf16 value has 8 significant bits and a code 4, so both parts together are the value itself,
+// down to 2^-9 of the row's largest; below, they are within 2^-17 of that largest.  Scores come out as
+// multiples of 2^-k, the row's `unit`.  (A content element that is not finite makes every score of its row NaN.)
+// k is 68 at most, so that the RoPE columns stay in range.  Eight lanes a row; a lane holds all its 64 columns before it writes.
+__device__ __forceinline__ void split_query(uint32_t q, int row, int c, float *unit) {
+    const uint32_t at = q + row * 128, key = row & 7, half = c >> 2, ch = 2 * (c & 3);
+    uint32_t x[4][8], top = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {  // columns 128 i + 16 c .. + 15
+        ld_shared_v4(at + (2 * i + half) * CB + ((ch ^ key) << 4), x[i]);
+        ld_shared_v4(at + (2 * i + half) * CB + (((ch + 1) ^ key) << 4), x[i] + 4);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) top = __vmaxu2(top, x[i][j] & 0x7fff7fffu);
+    }
+    top = max(top & 0xffffu, top >> 16);
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));  // the row's largest, as bf16 bits
+    const int e = min(max((int)(top >> 7), 66), 254);  // its exponent + 127
+    const float mul = __uint_as_float(top >= 0x7f80u ? 0x7fc00000u : (uint32_t)(134 + 127 - e) << 23);
+    if (c == 0) unit[row] = __uint_as_float((uint32_t)(e - 7) << 23);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const __half2 v = __floats2half2_rn(__uint_as_float(x[i][j] << 16) * mul, __uint_as_float(x[i][j] & 0xffff0000u) * mul);
+            unsigned short h, r;
+            uint32_t near;
+            asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(h) : "r"(*reinterpret_cast<const uint32_t *>(&v)));
+            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(near) : "h"(h));
+            const __half2 rest = __hsub2(v, *reinterpret_cast<const __half2 *>(&near));
+            asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(*reinterpret_cast<const uint32_t *>(&rest)));
+            hi[j >> 1] = j & 1 ? hi[j >> 1] | (uint32_t)h << 16 : h;
+            lo[j >> 1] = j & 1 ? lo[j >> 1] | (uint32_t)r << 16 : r;
+        }
+        st_shared_v4(at + 2 * i * CB + ((c ^ key) << 4), hi[0], hi[1], hi[2], hi[3]);
+        st_shared_v4(at + (2 * i + 1) * CB + ((c ^ key) << 4), lo[0], lo[1], lo[2], lo[3]);
+    }
+    const uint32_t rope = at + (NCB - 1) * CB + ((c ^ key) << 4);
+    uint32_t y[4];
+    ld_shared_v4(rope, y);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) y[j] = pack_bf16x2(__uint_as_float(y[j] << 16) * mul, __uint_as_float(y[j] & 0xffff0000u) * mul);
+    st_shared_v4(rope, y[0], y[1], y[2], y[3]);
 }
 
 // Which of the 32 tokens j .. j + 31 a node sees: all before ctx, its mask's bits from there, none behind L.
@@ -357,15 +418,15 @@ __device__ __forceinline__ uint32_t sees32(const uint32_t *mask, int words, int 
     return rem < 32 ? v & (0xffffffffu >> (32 - rem)) : v;
 }
 
-// tm_k, tm_v: column blocks of the bf16 cache; FP8: tm_k the RoPE keys, tm_v a page's codes as boxes of 128
-// columns, tm_c as boxes of 64 (unused in the bf16 kernel).
+// tm_k, tm_v: column blocks of the bf16 cache; FP8: tm_k the RoPE keys, tm_v and tm_c a page's codes as boxes of
+// 128 columns, as they are and in the operands' layout (unused in the bf16 kernel).
 template <bool F8>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS<F8>, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_c,
                const __grid_constant__ TreeArgs a, const __grid_constant__ TreePlan pl) {
     constexpr int K_STAGES = Lay<F8>::k_stages, V_STAGES = Lay<F8>::v_stages, V_OFF = Lay<F8>::v_off;
-    constexpr int S_BUFS = Lay<F8>::s_bufs;
+    constexpr int S_BUFS = Lay<F8>::s_bufs, KST = F8 ? F8_KST : NCB;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_s = smem_u32(smem_raw), data_s = (raw_s + 1023u) & ~1023u;
     Ctrl *ctrl = reinterpret_cast<Ctrl *>(smem_raw + (data_s - raw_s) + DATA);
@@ -379,16 +440,15 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         for (int i = 0; i < MAX_STAGES; ++i) {
             mbar_init(bar(ctrl->k_full[i]), 2);
             mbar_init(bar(ctrl->k_empty[i]), 1);
-            mbar_init(bar(ctrl->v_full[i]), 2);
+            mbar_init(bar(ctrl->v_full[i]), F8 ? 2 * CLEAN_THREADS / 32 : 2);
             mbar_init(bar(ctrl->v_empty[i]), 1);
             mbar_init(bar(ctrl->land[i]), 1);
         }
         for (int i = 0; i < RAW_STAGES; ++i) {
-            mbar_init(bar(ctrl->kraw_full[i]), 1);
-            mbar_init(bar(ctrl->kraw_empty[i]), 1);
             mbar_init(bar(ctrl->vraw_full[i]), 1);
-            mbar_init(bar(ctrl->vraw_empty[i]), 1);
+            mbar_init(bar(ctrl->vraw_empty[i]), CLEAN_THREADS / 32);
         }
+        mbar_init(bar(ctrl->q_land), 1);
         mbar_init(bar(ctrl->q_full), 2);
         mbar_init(bar(ctrl->q_empty), 1);
         for (int i = 0; i < 2; ++i) {
@@ -414,7 +474,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     tc_fence_after();
     pdl_trigger();
     pdl_wait();  // inputs are read from here on
-    schedule<THREADS<F8>>(a, pl, pair, rank, ctrl);
+    schedule(a, pl, pair, rank, ctrl);
     const uint32_t tmem = ctrl->tmem_base;
     auto fail = [&]() {
         *abort_flag = 1;
@@ -429,7 +489,8 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         Ring st{0, 0};
         uint32_t q_ph = 1;
         bool ok = true;
-        int ids[SPG], raw = 0;  // FP8: code stages sent so far
+        int ids[SPG];
+        uint32_t raw = 0;  // FP8: code stages sent so far
         auto pages = [&]() {
 #pragma unroll
             for (int p = 0; p < SPG; ++p) {
@@ -456,30 +517,29 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             if (it.first) {
                 if (!(ok = wait(bar(ctrl->q_empty), q_ph, abort_flag))) break;
                 q_ph ^= 1u;
-                mbar_arrive_expect_tx_remote(lead(ctrl->q_full), NCB * CB);
-                tma_load_3d_pair(data_s + Q_OFF, &tm_q, 0, it.s.t0 * a.n_h + it.tile * TILE + (int)rank * HALF, 0,
-                                 lead(ctrl->q_full));
+                const int q0 = it.s.t0 * a.n_h + it.tile * TILE + (int)rank * HALF;
+                if (F8) {
+                    mbar_arrive_expect_tx(bar(ctrl->q_land), NCB * CB);
+                    tma_load_3d(data_s + Q_OFF, &tm_q, 0, q0, 0, bar(ctrl->q_land));
+                } else {
+                    mbar_arrive_expect_tx_remote(lead(ctrl->q_full), NCB * CB);
+                    tma_load_3d_pair(data_s + Q_OFF, &tm_q, 0, q0, 0, lead(ctrl->q_full));
+                }
             }
             const int p0 = rank ? ids[2] : ids[0], p1 = rank ? ids[3] : ids[1];
             it.next(a);
             pages();  // of the next step: the table's latency passes under this one's loads
-            if (F8) {  // the codes go to the converting warps, eight blocks; the RoPE keys are operands as they are
-                for (int cb = 0; ok && cb < NCB - 1; ++cb) {
-                    if (!(ok = wait(bar(ctrl->kraw_empty[raw & 1]), ((raw >> 1) & 1) ^ 1, abort_flag))) break;
-                    const uint32_t dst = data_s + Lay<F8>::kraw_off + (raw & 1) * RAW, land = bar(ctrl->kraw_full[raw & 1]);
-                    mbar_arrive_expect_tx(land, ((p0 >= 0) + (p1 >= 0)) * (RAW / 2));
-                    if (p0 >= 0) tma_load_2d(dst, &tm_c, cb * 64, p0 * PG, land);
-                    if (p1 >= 0) tma_load_2d(dst + RAW / 2, &tm_c, cb * 64, p1 * PG, land);
-                    ++raw;
-                    st.adv(K_STAGES);
-                }
-            }
-            for (int cb = F8 ? NCB - 1 : 0; ok && cb < NCB; ++cb) {
+            for (int cb = 0; ok && cb < KST; ++cb) {
                 if (!(ok = wait(bar(ctrl->k_empty[st.i]), st.ph ^ 1u, abort_flag))) break;
                 const uint32_t dst = data_s + K_OFF + st.i * STAGE, full = lead(ctrl->k_full[st.i]);
                 mbar_arrive_expect_tx_remote(full, (p0 >= 0 ? CB : 0) + (p1 >= 0 ? CB : 0));
-                if (p0 >= 0) tma_load_3d_pair(dst, &tm_k, 0, p0 * PG, F8 ? 0 : cb, full);
-                if (p1 >= 0) tma_load_3d_pair(dst + CB, &tm_k, 0, p1 * PG, F8 ? 0 : cb, full);
+                if (F8 && cb < KST - 1) {
+                    if (p0 >= 0) tma_load_2d_pair(dst, &tm_c, cb * 128, p0 * PG, full);
+                    if (p1 >= 0) tma_load_2d_pair(dst + CB, &tm_c, cb * 128, p1 * PG, full);
+                } else {
+                    if (p0 >= 0) tma_load_3d_pair(dst, &tm_k, 0, p0 * PG, F8 ? 0 : cb, full);
+                    if (p1 >= 0) tma_load_3d_pair(dst + CB, &tm_k, 0, p1 * PG, F8 ? 0 : cb, full);
+                }
                 st.adv(K_STAGES);
             }
         }
@@ -495,10 +555,10 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 const bool clean = (pg0 + p + 1) * PG > ctx;
                 for (int nh = 0; ok && p < np && nh < 2; ++nh) {
                     if (F8) {
-                        if (!(ok = wait(bar(ctrl->vraw_empty[raw & 1]), ((raw >> 1) & 1) ^ 1, abort_flag))) break;
-                        const uint32_t land = bar(ctrl->vraw_full[raw & 1]);
+                        if (!(ok = wait(bar(ctrl->vraw_empty[raw % RAW_STAGES]), ((raw / RAW_STAGES) & 1) ^ 1, abort_flag))) break;
+                        const uint32_t land = bar(ctrl->vraw_full[raw % RAW_STAGES]);
                         mbar_arrive_expect_tx(land, RAW);
-                        tma_load_2d(data_s + Lay<F8>::vraw_off + (raw & 1) * RAW, &tm_v, nh * 256 + (int)rank * 128, id[p] * PG, land);
+                        tma_load_2d(data_s + Lay<F8>::vraw_off + (raw % RAW_STAGES) * RAW, &tm_v, nh * 256 + (int)rank * 128, id[p] * PG, land);
                         ++raw;
                         st.adv(V_STAGES);
                         continue;
@@ -528,7 +588,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         }
         if (!ok) fail();
     } else if (warp == QK_WARP && lane == 0 && rank == 0) {  // ================= S of both CTAs =================
-        constexpr uint32_t idesc = idesc_bf16(TILE, STEP, false, false);
+        constexpr uint32_t idesc = idesc_bf16(TILE, STEP, false, false), idesc_f8 = idesc_e4m3(TILE, STEP);
         Walk it;
         it.init(a, &ctrl->w_b);
         Ring st{0, 0};
@@ -544,15 +604,21 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             }
             if (!(ok = wait(bar(ctrl->s_free[sb]), ((u / S_BUFS) & 1) ^ 1, abort_flag))) break;
 #pragma unroll 1
-            for (int cb = 0; cb < NCB; ++cb) {
+            for (int cb = 0; cb < KST; ++cb) {
                 if (!(ok = wait(bar(ctrl->k_full[st.i]), st.ph, abort_flag))) break;
                 tc_fence_after();
-                const uint32_t kl = k_lo + st.i * (STAGE >> 4), ql = q_lo + cb * (CB >> 4);
-                const bool rope = F8 && cb == NCB - 1;  // FP8: the RoPE part of the scores apart, it takes no scale
-                const uint32_t d = tmem + S_COL + (F8 ? (rope ? 128 : 0) : sb * 128);
-                const bool acc = cb != 0 && !rope;
+                const uint32_t kl = k_lo + st.i * (STAGE >> 4);
+                if (F8 && cb < KST - 1) {  // 128 columns of codes against both parts of the queries
+                    const uint32_t ql = q_lo + 2 * cb * (CB >> 4);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) mma_ss_pair(d, ql + 2 * k, kl + 2 * k, HI, idesc, acc || k > 0);
+                    for (int k = 0; k < 8; ++k)
+                        mma_ss_pair_f8(tmem + S_COL, ql + (k >> 2) * (CB >> 4) + 2 * (k & 3), kl + 2 * (k & 3), HI, idesc_f8, cb > 0 || k > 0);
+                } else {  // FP8: the RoPE part of the scores apart, it takes no scale
+                    const uint32_t ql = q_lo + (F8 ? NCB - 1 : cb) * (CB >> 4);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        mma_ss_pair(tmem + S_COL + (F8 ? 128 : sb * 128), ql + 2 * k, kl + 2 * k, HI, idesc, (!F8 && cb > 0) || k > 0);
+                }
                 mma_commit_pair(bar(ctrl->k_empty[st.i]));
                 st.adv(K_STAGES);
             }
@@ -563,7 +629,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         }
         if (!ok) fail();
     } else if (warp == PV_WARP && lane == 0 && rank == 0) {  // ================= O of both CTAs =================
-        constexpr uint32_t idesc = idesc_bf16(TILE, 256, false, true);
+        constexpr uint32_t idesc = F8 ? idesc_f16(TILE, 256, false, true) : idesc_bf16(TILE, 256, false, true);
         Walk it;
         it.init(a, &ctrl->w_b);
         Ring st{0, 0};
@@ -597,60 +663,60 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             it.next(a);
         }
         if (!ok) fail();
-    } else if (F8 && warp >= CLEAN_WARP0) {  // ================= FP8: codes to bf16 tiles =================
-        // Four warps convert K's stages, four V's (cleaning drafted rows on the way).
-        const bool kw = warp < CLEAN_WARP0 + 4;
-        const int t = (warp & 3) * 32 + lane, id = kw ? BAR_CLEAN : BAR_CLEAN + 1;
-        const int stages = kw ? K_STAGES : V_STAGES;
-        uint64_t *full = kw ? ctrl->k_full : ctrl->v_full, *empty = kw ? ctrl->k_empty : ctrl->v_empty;
-        uint64_t *raw_full = kw ? ctrl->kraw_full : ctrl->vraw_full, *raw_empty = kw ? ctrl->kraw_empty : ctrl->vraw_empty;
-        const uint32_t raw0 = data_s + (kw ? Lay<F8>::kraw_off : Lay<F8>::vraw_off), st0 = data_s + (kw ? K_OFF : V_OFF);
+    } else if (F8 && warp >= CLEAN_WARP0) {  // ================= FP8: Q in two parts, V's codes to fp16 tiles =================
+        const int t = threadIdx.x - CLEAN_WARP0 * 32;
         Walk it;
         it.init(a, &ctrl->w_b);
         Ring st{0, 0};
-        int raw = 0;
+        uint32_t q_ph = 0;
+        uint32_t raw = 0;
         bool ok = true;
         while (ok && !it.done()) {
-            const int n = kw ? NCB - 1 : 2 * it.pages();
-            for (int i = 0; i < n; ++i, ++raw, st.adv(stages)) {
-                const bool good = wait(bar(raw_full[raw & 1]), (raw >> 1) & 1, abort_flag) &&
-                                  wait(bar(empty[st.i]), st.ph ^ 1u, abort_flag);
-                const uint32_t src = raw0 + (raw & 1) * RAW, dst = st0 + st.i * STAGE;
-                const int j0 = (it.step * SPG + (i >> 1)) * PG;             // V: the page's first token
-                const int drafted = it.s.ctx - j0, end = it.s.L - j0;       // V: the first drafted row, and the sequence's end
-                // A thread takes four chunks of 16 codes, columns 16 c of two rows of two blocks; its loads come before
-                // its stores, each of which would hold the next load back.
-                const int c = t & 3, row0 = t >> 2;
-                const uint32_t src_t = src + row0 * (kw ? 64 : 128) + c * 16;
-                const uint32_t dst0 = dst + row0 * 128 + (((2 * c) ^ (row0 & 7)) << 4), dst1 = dst + row0 * 128 + (((2 * c + 1) ^ (row0 & 7)) << 4);
-                const bool tail = !kw && drafted < PG;
+            if (it.first) {
+                const bool good = wait(bar(ctrl->q_land), q_ph, abort_flag);
+                for (int r0 = 0; r0 < HALF; r0 += CLEAN_THREADS / 8) split_query(data_s + Q_OFF, r0 + (t >> 3), t & 7, ctrl->q_unit[q_ph]);
+                q_ph ^= 1u;
+                fence_proxy_async_smem();
+                if (!(ok = !named_red_or(!good, BAR_CLEAN, CLEAN_THREADS))) break;
+                if (t == 0) mbar_arrive_pair(lead(ctrl->q_full));
+            }
+            for (int i = 0, n = 2 * it.pages(); i < n; ++i, ++raw, st.adv(V_STAGES)) {
+                const bool good = wait(bar(ctrl->vraw_full[raw % RAW_STAGES]), (raw / RAW_STAGES) & 1, abort_flag) &&
+                                  wait(bar(ctrl->v_empty[st.i]), st.ph ^ 1u, abort_flag);
+                const int j0 = (it.step * SPG + (i >> 1)) * PG;        // the page's first token
+                const int drafted = it.s.ctx - j0, end = it.s.L - j0;  // the first drafted row, and the sequence's end
+                // A thread takes four chunks of 16 codes, columns 16 c of two rows of two blocks, odd rows the blocks the
+                // other way round so that eight lanes read 128 different bytes modulo 128.  Its loads come before its
+                // stores, each of which would hold the next load back.
+                const int c = t & 3, row0 = t >> 2, odd = row0 & 1;
+                const uint32_t src = data_s + Lay<F8>::vraw_off + (raw % RAW_STAGES) * RAW + row0 * 128 + c * 16;
+                const uint32_t dst = data_s + V_OFF + st.i * STAGE + row0 * 128;
+                const uint32_t dst0 = dst + (((2 * c) ^ (row0 & 7)) << 4), dst1 = dst + (((2 * c + 1) ^ (row0 & 7)) << 4);
+                const bool tail = drafted < PG;
                 uint32_t w[4][4];
 #pragma unroll
-                for (int k = 0; k < 4; ++k)  // block (K: page) k / 2, rows row0 and row0 + 32
-                    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                                 : "=r"(w[k][0]), "=r"(w[k][1]), "=r"(w[k][2]), "=r"(w[k][3])
-                                 : "r"(src_t + (kw ? (k >> 1) * (RAW / 2) + (k & 1) * 2048 : (k >> 1) * 64 + (k & 1) * 4096)));
+                for (int k = 0; k < 4; ++k)  // block k / 2 (odd rows: the other), rows row0 and row0 + 32
+                    ld_shared_v4(src + ((k >> 1) ^ odd) * 64 + (k & 1) * 4096, w[k]);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     uint32_t o[8];
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) e4m3x4_to_bf16x4(w[k][q], o[2 * q], o[2 * q + 1]);
+                    for (int q = 0; q < 4; ++q) e4m3x4_to_f16x4(w[k][q], o[2 * q], o[2 * q + 1]);
                     if (tail) {
                         const int row = row0 + 32 * (k & 1);
 #pragma unroll
-                        for (int q = 0; q < 8; ++q) o[q] = row >= end ? 0u : row >= drafted ? finite_pair(o[q]) : o[q];
+                        for (int q = 0; q < 8; ++q) o[q] = row >= end ? 0u : row >= drafted ? finite_pair<0x7c00u>(o[q]) : o[q];
                     }
-                    st_shared_v4(dst0 + (k >> 1) * CB + (k & 1) * 4096, o[0], o[1], o[2], o[3]);
-                    st_shared_v4(dst1 + (k >> 1) * CB + (k & 1) * 4096, o[4], o[5], o[6], o[7]);
+                    st_shared_v4(dst0 + ((k >> 1) ^ odd) * CB + (k & 1) * 4096, o[0], o[1], o[2], o[3]);
+                    st_shared_v4(dst1 + ((k >> 1) ^ odd) * CB + (k & 1) * 4096, o[4], o[5], o[6], o[7]);
                 }
                 fence_proxy_async_smem();
-                if (!(ok = !named_red_or(!good, id, CLEAN_THREADS))) break;
-                if (t == 0) {
-                    mbar_arrive_pair(lead(full[st.i]));
-                    mbar_arrive(bar(raw_empty[raw & 1]));
+                if (!(ok = __all_sync(0xffffffffu, good))) break;
+                if (lane == 0) {  // each warp for itself: a barrier among the four cost 4% of the whole
+                    mbar_arrive_pair(lead(ctrl->v_full[st.i]));
+                    mbar_arrive(bar(ctrl->vraw_empty[raw % RAW_STAGES]));
                 }
             }
-            if (kw) st.adv(stages);  // the RoPE keys' stage, which the loader fills
             it.next(a);
         }
         if (!ok && lane == 0) fail();
@@ -673,9 +739,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     const int row = k * (CLEAN_THREADS / 16) + (t >> 4), j = j0 + row;
                     const uint32_t at = base + row * 128;
                     uint32_t x[4];
-                    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                                 : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
-                                 : "r"(at));
+                    ld_shared_v4(at, x);
                     bool hit = false;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
@@ -704,6 +768,8 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         int before = 0;  // steps so far that had the page pg ^ 2, which shares the slot of P
         bool ok = true, good = true;
         float sc0 = 0.f, sc1 = 0.f;
+        int sc_top = 0;
+        bool sc_near = true;
         float(*scales)[PG] = ctrl->scale[warp - SM_WARP0];
         auto load_scales = [&](const Walk &w) {
             sc0 = sc1 = 0.f;
@@ -716,6 +782,8 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             sc1 = src[32];
         };
         if (F8) load_scales(it);
+        float to_log2 = a.scale_log2;  // a score of S to log2 units
+        int seg = 0;
         for (int u = 0; ok && !it.done(); ++u) {
             const int row = it.tile * TILE + (int)rank * HALF + r;  // of the sequence's (node, head) pairs
             const bool mine = row < it.s.n * a.n_h;
@@ -726,26 +794,35 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             if (F8) {
                 scales[0][lane] = sc0;
                 scales[0][lane + 32] = sc1;
-                scales[1][lane] = fabsf(sc0) <= FLT_MAX ? sc0 : 0.f;
-                scales[1][lane + 32] = fabsf(sc1) <= FLT_MAX ? sc1 : 0.f;
+                sc0 = fabsf(sc0) <= FLT_MAX ? sc0 : 0.f;
+                sc1 = fabsf(sc1) <= FLT_MAX ? sc1 : 0.f;
+                scales[1][lane] = sc0;
+                scales[1][lane + 32] = sc1;
+                const int e0 = scale_exponent(sc0), e1 = scale_exponent(sc1);
+                sc_top = __reduce_max_sync(0xffffffffu, max(e0, e1));
+                sc_near = sc_top - __reduce_min_sync(0xffffffffu, min(e0, e1)) <= 4;
                 __syncwarp();
             }
+            if (F8 && it.first) to_log2 = a.scale_log2 * ctrl->q_unit[seg++ & 1][r];
             if (good) {
                 const uint32_t sa = tmem + lane_base + S_COL + buf * 128 + cg * PG;
                 if (F8) {  // content scores times the tokens' scales, and the RoPE scores
 #pragma unroll
-                    for (int c = 0; c < PG / 8; ++c) {
-                        uint32_t x[8], y[8];
-                        tmem_ld8(sa + c * 8, x);
-                        tmem_ld8(sa + 128 + c * 8, y);
+                    for (int c = 0; c < 2; ++c) tmem_ld32(sa + 128 + c * 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32 * c));
+#pragma unroll
+                    for (int c = 0; c < PG / 16; ++c) {
+                        uint32_t x[16];
+                        tmem_ld16(sa + c * 16, x);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int j = 0; j < 8; j += 4) {
-                            const float4 sc = *reinterpret_cast<const float4 *>(&scales[0][8 * c + j]);
-                            v[8 * c + j] = __float_as_uint(fmaf(__uint_as_float(x[j]), sc.x, __uint_as_float(y[j])));
-                            v[8 * c + j + 1] = __float_as_uint(fmaf(__uint_as_float(x[j + 1]), sc.y, __uint_as_float(y[j + 1])));
-                            v[8 * c + j + 2] = __float_as_uint(fmaf(__uint_as_float(x[j + 2]), sc.z, __uint_as_float(y[j + 2])));
-                            v[8 * c + j + 3] = __float_as_uint(fmaf(__uint_as_float(x[j + 3]), sc.w, __uint_as_float(y[j + 3])));
+                        for (int j = 0; j < 16; j += 4) {
+                            const float4 sc = *reinterpret_cast<const float4 *>(&scales[0][16 * c + j]);
+                            const float t[4] = {sc.x, sc.y, sc.z, sc.w};
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                uint32_t &y = v[16 * c + j + i];
+                                y = __float_as_uint(fmaf(__uint_as_float(x[j + i]), t[i], __uint_as_float(y)));
+                            }
                         }
                     }
                 } else {
@@ -773,10 +850,21 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                         if (!((see >> j) & 1u)) v[32 * w + j] = 0xff800000u;  // -inf
                 }
             }
+            // The largest score in log2 units.  FP8: P is exp2(score - m) times the token's scale, in fp16, so m bounds
+            // score + log2(scale) - 7.  P's largest is then between 2^2 and 2^7, and below 2^15 when m moves.  The scales
+            // of a page count as their largest where they are within 2^4 of one another, else each as it is.
             float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            float top;
+            if (!F8 || sc_near) {
 #pragma unroll
-            for (int j = 0; j < PG; ++j) x[j & 3] = fmaxf(x[j & 3], __uint_as_float(v[j]));
-            float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+                for (int j = 0; j < PG; ++j) x[j & 3] = fmaxf(x[j & 3], __uint_as_float(v[j]));
+                top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * to_log2 + (F8 ? (float)(sc_top - 7) : 0.f);
+            } else {
+#pragma unroll
+                for (int j = 0; j < PG; ++j)
+                    x[j & 3] = fmaxf(x[j & 3], fmaf(__uint_as_float(v[j]), to_log2, (float)(scale_exponent(scales[1][j]) - 7)));
+                top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+            }
             ctrl->top[sb][pg][r] = top;
             if (named_red_or(!good, BAR_MAX, SM_THREADS)) {
                 ok = false;
@@ -784,7 +872,6 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             }
 #pragma unroll
             for (int k = 0; k < SPG; ++k) top = fmaxf(top, ctrl->top[sb][k][r]);
-            top *= a.scale_log2;
             float fac = 1.f;
             if (it.first) {
                 m = top;
@@ -796,16 +883,21 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             const float base = m == -INFINITY ? 0.f : m;
             float s[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int j = 0; j < PG / 2; ++j) {  // P as bf16 pairs, into the front half of v
-                const float p0 = ex2(fmaf(__uint_as_float(v[2 * j]), a.scale_log2, -base));
-                const float p1 = ex2(fmaf(__uint_as_float(v[2 * j + 1]), a.scale_log2, -base));
-                s[j & 3] += p0 + p1;
+            for (int j = 0; j < PG / 4; ++j) {  // P as bf16 pairs, into the front half of v
+                float p[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) p[i] = ex2(fmaf(__uint_as_float(v[4 * j + i]), to_log2, -base));
+                s[0] += p[0] + p[1];
+                s[1] += p[2] + p[3];
                 if (F8) {  // the value product is over the codes: their scales go into P
-                    const float2 sc = *reinterpret_cast<const float2 *>(&scales[1][2 * j]);
-                    v[j] = pack_bf16x2(p0 * sc.x, p1 * sc.y);
-                } else {
-                    v[j] = pack_bf16x2(p0, p1);
+                    const float4 sc = *reinterpret_cast<const float4 *>(&scales[1][4 * j]);
+                    p[0] *= sc.x;
+                    p[1] *= sc.y;
+                    p[2] *= sc.z;
+                    p[3] *= sc.w;
                 }
+                v[2 * j] = F8 ? pack_f16x2(p[0], p[1]) : pack_bf16x2(p[0], p[1]);
+                v[2 * j + 1] = F8 ? pack_f16x2(p[2], p[3]) : pack_bf16x2(p[2], p[3]);
             }
             l = l * fac + ((s[0] + s[1]) + (s[2] + s[3]));
             // Every thread waits for every step's MMAs in turn, two steps behind (by then they are done): a wait by
@@ -869,7 +961,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 }
                 if (pg == 0) {
                     if (!whole) {
-                        pl.m[slot * TILE + (int)rank * HALF + r] = m;
+                        pl.m[slot * TILE + (int)rank * HALF + r] = total == total ? m : total;  // NaN scores move no maximum
                         pl.l[slot * TILE + (int)rank * HALF + r] = total;
                     } else if (mine && a.lse) {
                         a.lse[(size_t)it.s.t0 * a.n_h + row] =
@@ -918,9 +1010,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                         for (int i = 0; i < 4; ++i) {
                             const int rr = 8 * i + (lane >> 2), ch = lane & 3;
                             uint32_t x[4];
-                            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                                         : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
-                                         : "r"(stage + rr * 64 + ((ch ^ ((rr >> 1) & 3)) << 4)));
+                            ld_shared_v4(stage + rr * 64 + ((ch ^ ((rr >> 1) & 3)) << 4), x);
                             if (rr < rows_left)
                                 *reinterpret_cast<uint4 *>(dst + rr * width + (narrow ? c >> 1 : c) * 64 + ch * 16) =
                                     make_uint4(x[0], x[1], x[2], x[3]);
@@ -1055,7 +1145,7 @@ int tree_pairs() {
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM) != cudaSuccess) return 0;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(2 * (sms / 2));
-        cfg.blockDim = dim3(kern == tree_tc_kernel<true> ? THREADS<true> : THREADS<false>);
+        cfg.blockDim = dim3(THREADS);
         cfg.dynamicSmemBytes = SMEM;
         cudaLaunchAttribute attr;
         attr.id = cudaLaunchAttributeClusterDimension;
@@ -1118,7 +1208,7 @@ cudaError_t launch_tree_tc(const mla_dims_t &d, const TreeArgs &a, void *ws, cud
     CUtensorMap tm_q, tm_k, tm_v, tm_c;
     const bool maps = f8 ? tmap_bf16_colblocks(&tm_k, a.kr_pool, pool_rows, ROW - DC, (ROW - DC) * 2, PG, 1) &&
                                tmap_u8_rows(&tm_v, a.kv_pool, DC, pool_rows, DC, 128, PG) &&
-                               tmap_u8_rows(&tm_c, a.kv_pool, DC, pool_rows, DC, 64, PG)
+                               tmap_2d(&tm_c, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.kv_pool, DC, pool_rows, DC, 128, PG)
                          : tmap_bf16_colblocks(&tm_k, a.kv_pool, pool_rows, ROW, ROW * 2, PG, 1) &&
                                tmap_bf16_colblocks(&tm_v, a.kv_pool, pool_rows, ROW, ROW * 2, PG, 2);
     if (!maps || !tmap_bf16_colblocks(&tm_q, a.q_abs, q_rows, ROW, ROW * 2, HALF, NCB)) return cudaErrorInvalidValue;
@@ -1128,7 +1218,7 @@ cudaError_t launch_tree_tc(const mla_dims_t &d, const TreeArgs &a, void *ws, cud
     pdl.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * pairs);
-    cfg.blockDim = dim3(f8 ? THREADS<true> : THREADS<false>);
+    cfg.blockDim = dim3(THREADS);
     cfg.dynamicSmemBytes = SMEM;
     cfg.stream = st;
     cfg.attrs = &pdl;

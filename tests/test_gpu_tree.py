@@ -96,8 +96,16 @@ class Batch:
         rows = R.cache_rows(c.kv_pool, c.kr_pool, c.kv_scale, self.table[b], L, self.page)
         nodes = np.arange(self.n[b]) if nodes is None else np.asarray(nodes)
         see = np.concatenate([np.ones((len(nodes), self.ctx[b]), dtype=bool), self.see[b][nodes]], 1)
-        t = torch.from_numpy(self.cu[b] + nodes).cuda()
-        return t, R.attend(self.q[t], rows, torch.from_numpy(see).cuda(), self.d_c, self.scale)
+        t, see = torch.from_numpy(self.cu[b] + nodes).cuda(), torch.from_numpy(see).cuda()
+        self.extra = (0, 0)
+        if self.kv == "fp8" and self.tensor_core():
+            # every weight is 1 at most, so the row's largest weight times scale is the largest scale at most
+            at = self.owned[b][torch.arange(L, device="cuda") // self.page], torch.arange(L, device="cuda") % self.page
+            ds, da = R.fp8_terms(self.q[t], c.kv_pool[at], c.kv_scale[at], see, self.d_c, self.scale)
+            w = torch.where(torch.isfinite(c.kv_scale[at]), c.kv_scale[at], 0).abs()
+            largest = torch.stack([w[m].amax() if m.any() else w.new_zeros(()) for m in see]).double()
+            self.extra = (ds, da * largest[:, None, None])
+        return t, R.attend(self.q[t], rows, see, self.d_c, self.scale)
 
     def check(self, got, out="f32", sample=None):
         o, lse = got
@@ -108,11 +116,13 @@ class Batch:
             t, (ro, rl, size, reach) = self.reference(b, nodes)
             eo = (o[t].double() - ro).abs()
             bound = R.o_bound(ro, size, reach, self.row, out == "bf16", self.tensor_core())
+            if self.kv == "fp8" and self.tensor_core():
+                bound = bound + 2 * size * self.extra[0][..., None] + self.extra[1]
             assert (eo <= bound).all(), (b, float((eo / bound).max()))
             seen = torch.isfinite(rl)
             assert torch.equal(torch.isfinite(lse[t]), seen)
             el = (lse[t].double() - rl).abs()[seen]
-            lb = R.lse_bound(rl, reach, self.row)[seen]
+            lb = (R.lse_bound(rl, reach, self.row) + self.extra[0])[seen]
             assert (el <= lb).all(), (b, float((el / lb).max()))
             assert (o[t][~seen] == 0).all() and (lse[t][~seen] == float("-inf")).all()
         no_error()
@@ -458,4 +468,153 @@ def test_every_fp8_code(flags):
         assert torch.isfinite(o[~sees]).all()
         # an infinite scale makes the score +inf or -inf, by the sign of q . code: weight NaN, or 0 and no part of o
         assert not torch.isfinite(lse[sees]).any() if bad != bad else not torch.isfinite(lse[sees]).all()
+    no_error()
+
+
+# ---- FP8 on the tensor cores: query parts and fp16 weights -----------------------------------------
+
+def test_fp8_scales_far_apart():
+    """Tokens' scales over 2^40 within a page, some of them 0, under flat weights; the largest float in
+    the scale of drafted tokens reaches only the nodes that see them."""
+    b = Batch([500, 90], [9, 4], kv="fp8", heads=24, seed=41)
+    b.q[:, ::2, :512] = 0                                            # weights by the RoPE part alone
+    b.q[:, 1::2] *= 2.0 ** -12
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    for s in range(2):
+        j = torch.arange(int(b.ctx[s] + b.n[s]), device="cuda")
+        at = b.owned[s][j // 64], j % 64
+        b.cache.kv_scale[at] *= 2.0 ** torch.randint(-20, 21, (len(j),), generator=g, device="cuda").float()
+        b.cache.kv_scale[at[0][::7], at[1][::7]] = 0
+    o, lse = b.decode()
+    b.check((o, lse))
+    # in each segment the error is counted against the row's own largest weight times scale
+    for s in range(2):
+        L = int(b.ctx[s] + b.n[s])
+        at = b.owned[s][torch.arange(L, device="cuda") // 64], torch.arange(L, device="cuda") % 64
+        rows = R.cache_rows(b.cache.kv_pool, b.cache.kr_pool, b.cache.kv_scale, b.table[s], L, 64)
+        t, (ro, rl, size, reach) = b.reference(s)
+        see = np.concatenate([np.ones((b.n[s], b.ctx[s]), dtype=bool), b.see[s]], 1)
+        ds, da = R.fp8_terms(b.q[t], b.cache.kv_pool[at], b.cache.kv_scale[at], torch.from_numpy(see).cuda(), 512, b.scale)
+        for i in range(int(b.n[s])):
+            m = torch.from_numpy(see[i]).cuda()
+            p = torch.softmax(b.q[t[i]].double() @ rows[m].T * b.scale, -1)
+            largest = (p * b.cache.kv_scale[at][m].double()).amax(-1)
+            bound = R.o_bound(ro[i], size[i], reach[i], b.row, False, True) + 2 * size[i] * ds[i][:, None] + da[i] * largest[:, None]
+            assert ((o[t[i]].double() - ro[i]).abs() <= bound).all()
+    slot = int(b.ctx[0]) + 3
+    b.cache.kv_scale[b.owned[0][slot // 64], slot % 64] = torch.finfo(torch.float32).max
+    o2, lse2 = b.decode()
+    sees = torch.from_numpy(np.concatenate([b.see[0][:, 3], np.zeros(4, dtype=bool)])).cuda()
+    assert torch.equal(o2[~sees], o[~sees]) and torch.equal(lse2[~sees], lse[~sees])
+    no_error()
+
+
+def test_fp8_queries_with_one_large_element():
+    b = Batch([700, 3], [5, 8], kv="fp8", heads=40, seed=43)
+    b.q[:, :, 17] *= 1000
+    b.q[0, 3, :512] = 0
+    b.q[1, :, :512] *= 2.0 ** -40                                    # content far below the RoPE part, and far above
+    b.q[2, :, :512] *= 2.0 ** 10
+    b.q[3, :, 512:] = 0
+    b.check(b.decode())
+
+
+@pytest.mark.parametrize("kv,flags", [("bf16", 0), ("fp8", 0), ("bf16", 1), ("fp8", 1)])
+@pytest.mark.parametrize("ctx", [40, 2000])                          # in one run, and joined from several
+@pytest.mark.parametrize("column", [5, 530])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_a_query_that_is_not_finite_stays_in_its_row(kv, flags, ctx, column, value):
+    b = Batch([ctx], [4], kv=kv, heads=16, flags=flags, seed=47)
+    good, good_lse = b.decode()
+    b.q[2, 7, column] = value
+    o, lse = b.decode()
+    assert torch.isnan(o[2, 7]).all() and not torch.isfinite(lse[2, 7])
+    others = torch.ones(4, 16, dtype=torch.bool, device="cuda")
+    others[2, 7] = False
+    assert torch.equal(o[others], good[others]) and torch.equal(lse[others], good_lse[others])
+    no_error()
+
+
+# ---- larger work: several tiles and runs a pair, many sequences, many segments ----------------------
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+@pytest.mark.parametrize("ctx,n,heads", [([3000, 2100, 700, 2900], [40, 17, 33, 64], 128), ([4000] * 6, [5, 9, 2, 7, 1, 3], 128),
+                                         ([20000, 5], [3, 200], 16)])
+def test_many_units_a_pair(kv, ctx, n, heads):
+    b = Batch(ctx, n, heads=heads, kv=kv, seed=51)
+    first = b.decode("bf16")
+    b.check(first, "bf16", sample=3)
+    for _ in range(3):
+        again = b.decode("bf16")
+        assert torch.equal(again[0], first[0]) and torch.equal(again[1], first[1])
+
+
+@pytest.mark.parametrize("kv,flags", [("bf16", 0), ("fp8", 0), ("bf16", 1)])
+def test_more_sequences_than_a_block_has_threads(kv, flags):
+    """1100 sequences, some without nodes, one with a bad length."""
+    from mla_latent_kv_mqa_b200 import native as N
+    rng = np.random.default_rng(5)
+    n = rng.integers(0, 4, 1100)
+    n[[0, 511, 512, 1099]] = [1, 0, 2, 3]
+    b = Batch(rng.integers(0, 130, 1100), n, heads=3, kv=kv, flags=flags, seed=53)
+    o, lse = b.decode()
+    keep_B, b.B = b.B, 40                                            # the whole batch against the plain form takes minutes
+    b.check((o, lse))
+    b.B = keep_B
+    for s in (511, 512, 513, 700, 1098, 1099):
+        if b.n[s]:
+            t, (ro, rl, size, reach) = b.reference(s)
+            bound = R.o_bound(ro, size, reach, b.row, False, b.tensor_core())
+            if kv == "fp8":
+                bound = bound + 2 * size * b.extra[0][..., None] + b.extra[1]
+            assert ((o[t].double() - ro).abs() <= bound).all()
+    b.lens[600] = -1
+    n600 = slice(int(b.cu[600]), int(b.cu[601]))
+    o2, lse2 = b.decode()
+    if b.n[600]:
+        assert N.mla_get_last_device_error() == N.MLA_ERR_BAD_SEQ_LEN
+        o[n600], lse[n600] = 0, float("-inf")
+    assert torch.equal(o2, o) and torch.equal(lse2, lse)
+
+
+@pytest.mark.parametrize("kv,act,shape,L", [("f32", "f32", TOY, 4000), ("bf16", "bf16", (128, 256, 32), 3100)])
+def test_a_long_context_of_other_shapes(kv, act, shape, L):
+    """More segments than a cluster joins."""
+    b = Batch([L], [1], kv=kv, act=act, shape=shape, heads=2, seed=57)
+    b.check(b.decode())
+
+
+def test_two_streams_at_once_and_a_workspace_that_grows():
+    """Calls of one layer on two streams have a workspace each; a captured graph keeps the one it was captured with."""
+    a = Batch([900, 300], [6, 4], heads=32, seed=61)
+    c = Batch([3000, 2000, 1000], [30, 20, 10], heads=32, seed=62)
+    c.layer = a.layer
+    want_a, want_c = a.decode(), c.decode()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = []
+    for k in range(6):
+        with torch.cuda.stream(streams[k & 1]):
+            x = (a, c)[k & 1]
+            got.append((x, x.layer.decode_tree(x.cache, x.q, x.table, x.lens, x.trees, x.max_len)))
+    torch.cuda.synchronize()
+    for x, (o, lse) in got:
+        want = want_a if x is a else want_c
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+    s = torch.cuda.Stream()
+    o, lse = torch.zeros_like(want_a[0]), torch.zeros_like(want_a[1])
+    with torch.cuda.stream(s):
+        a.layer.decode_tree(a.cache, a.q, a.table, a.lens, a.trees, a.max_len, o_lat=o, lse=lse)
+        s.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            a.layer.decode_tree(a.cache, a.q, a.table, a.lens, a.trees, a.max_len, o_lat=o, lse=lse)
+        c.layer.decode_tree(c.cache, c.q, c.table, c.lens, c.trees, c.max_len)   # a larger workspace on the same stream
+        junk = [torch.full((1 << 22,), float("nan"), device="cuda") for _ in range(8)]
+        o.zero_()
+        g.replay()
+    s.synchronize()
+    del junk
+    assert torch.equal(o, want_a[0]) and torch.equal(lse, want_a[1])
     no_error()

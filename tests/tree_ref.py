@@ -66,10 +66,27 @@ def o_bound(o, size, reach, row, out_bf16, tensor_core, segments=True):
     """|error| of o_lat, element by element.  fp32 products and sums in a score: row + 1 roundings (twice
     that where the tensor core truncates) of terms whose sum of sizes is `reach`, which moves every
     weight by that much, and 2^-21 for each of exp2's approximations; on the tensor core a weight is
-    rounded to bf16 once and a segment's sum once more; the output once."""
+    rounded to bf16 once and a segment's sum once more; the output once.  (FP8 there: fp8_terms too.)"""
     ds = (row + 1) * EPS_F32 * 2 * reach
     rel = 2 * ds[..., None] + 2.0 ** -20 + 64 * EPS_F32 + (EPS_BF16 * (2 if segments else 1) if tensor_core else 0)
     return size * rel + (EPS_BF16 if out_bf16 else EPS_F32) * o.abs() + 1e-30
+
+
+def fp8_terms(q, kv, scale_t, see, d_c, scale):
+    """What the tensor-core kernel's formats add over an FP8 cache: (error of a score, absolute error of
+    o).  q [n, H, row]; kv, scale_t: codes [L, d_c] and scales [L]; see [n, L].  A query's content element
+    is off by 2^-10 where its row's largest is at least 2^7.  A weight times its scale is off by 2^-25 at
+    most where fp16 has no 11 bits for it, and the row's largest is 2^2 at least."""
+    codes = kv.view(torch.float8_e4m3fn).double()[:, :d_c].abs()
+    s = torch.where(torch.isfinite(scale_t), scale_t, 0).double().abs()
+    dq = q[..., :d_c].double().abs().amax(-1) * 2.0 ** -17 * scale
+    n, H, _ = q.shape
+    ds, da = torch.zeros(n, H, dtype=torch.float64, device=q.device), torch.zeros(n, H, d_c, dtype=torch.float64, device=q.device)
+    for i in range(n):
+        if see[i].any():
+            ds[i] = dq[i] * (codes[see[i]].sum(-1) * s[see[i]]).max()
+            da[i] = 2.0 ** -27 * codes[see[i]].sum(0)
+    return ds, da
 
 
 def lse_bound(lse, reach, row):
