@@ -117,23 +117,25 @@ struct TreePlan {
     long long *units;
     int *tiles;
     int4 *tile;
-    float *o, *m, *l;  // [2 pairs][128 / 8][512][8 rows], [2 pairs][128 rows]
+    float *o, *m, *l;  // [2 pairs][128 / 8][512 / 4][8 rows][4 columns], [2 pairs][128 rows]
     int pairs;
 };
 
 struct Seq {
     int t0, n, L, ctx, tiles, steps;
 };
-__device__ __forceinline__ Seq seq_of(const TreeArgs &a, int b) {
+__device__ __forceinline__ Seq seq_of(const TreeArgs &a, int t0, int n, int L) {
     Seq s;
-    s.t0 = a.cu[b];
-    s.n = a.cu[b + 1] - s.t0;
-    s.L = a.seq_lens[b];
+    s.t0 = t0;
+    s.n = n;
+    s.L = L;
     s.ctx = s.L - s.n;
     s.tiles = (int)(((long long)s.n * a.n_h + TILE - 1) / TILE);
     s.steps = s.ctx < 0 || s.L > a.max_seq_len || s.L > a.max_blocks * PG ? 0 : (s.L + STEP - 1) / STEP;
     return s;
 }
+
+__device__ __forceinline__ Seq seq_of(const TreeArgs &a, int b) { return seq_of(a, a.cu[b], a.cu[b + 1] - a.cu[b], a.seq_lens[b]); }
 
 // Walks a pair's units; every role walks the same ones.
 struct Walk {
@@ -196,9 +198,12 @@ struct Ring {
     }
 };
 
-__device__ __forceinline__ long long unit_start(long long c, long long U, int pairs) { return c * U / pairs; }
+// A pair's first unit.  (Batches of fewer than 2^24 units, all but the largest, without a 64-bit division.)
+__device__ __forceinline__ long long unit_start(long long c, long long U, int pairs) {
+    return U < (1 << 24) ? (uint32_t)c * (uint32_t)U / (uint32_t)pairs : c * U / pairs;
+}
 __device__ __forceinline__ int pair_of_unit(long long u, long long U, int pairs) {
-    int c = (int)(u * pairs / U);
+    int c = U < (1 << 24) ? (int)((uint32_t)u * (uint32_t)pairs / (uint32_t)U) : (int)(u * pairs / U);
     while (c + 1 < pairs && unit_start(c + 1, U, pairs) <= u) ++c;
     while (c > 0 && unit_start(c, U, pairs) > u) --c;
     return c;
@@ -248,11 +253,12 @@ __device__ __noinline__ void schedule(const TreeArgs &a, const TreePlan &pl, int
         t = 0;
         TreeSpan sp;
         if (b >= a.B) return;
+        const int L = a.seq_lens[b];  // beside the offsets
         if (!tree_span(a.cu, b, a.B, a.T, a.max_nodes, &sp)) {
             bad = true;
             return;
         }
-        q = seq_of(a, b);
+        q = seq_of(a, sp.t0, sp.n, L);
         bad_len |= q.n > 0 && q.steps == 0;
         t = q.tiles;
         u = (long long)t * q.steps;
@@ -968,15 +974,16 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                             total == 0.f ? -INFINITY : (base + log2f(total)) * 0.69314718055994531f;
                     }
                 }
-                if (!whole) {  // partial rows: [slot][row / 8][column][row % 8]; a warp's store is a column of 32 rows
-                    float *dst = pl.o + (((size_t)slot * (TILE / 8) + ((int)rank * HALF + r) / 8) * DC + cg * 256 + half * 128) * 8 + (r & 7);
+                if (!whole) {  // partial rows: a warp's store is four columns of 32 rows, four times 128 bytes
+                    float *dst = pl.o + (((size_t)slot * (TILE / 8) + ((int)rank * HALF + r) / 8) * DC + cg * 256 + half * 128) * 8 + (r & 7) * 4;
 #pragma unroll 1
                     for (int c = 0; c < 4; ++c) {
                         uint32_t o[32];
                         tmem_ld32(tmem + lane_base + O_COL + cg * 128 + c * 32, o);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) __stcg(dst + (c * 32 + i) * 8, __uint_as_float(o[i]));
+                        for (int i = 0; i < 32; i += 4)
+                            __stcg(reinterpret_cast<uint4 *>(dst + (c * 32 + i) * 8), make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]));
                     }
                 } else {
                     // O's rows pass through 2 KB of P (its MMAs are done) a warp, 64 bytes of each of the 32 rows at a
@@ -1042,30 +1049,29 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
 }
 
 // Joins the tiles that lie in several pairs' runs: o = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s.  A block
-// takes eight rows, 16 contiguous KB of a slot's partials; a thread four of the rows in four columns.  The
-// block finds the slots and weights of its rows side by side first, so that the partials are read without
-// waiting for one another, and turns the sums in shared memory to write whole rows.  Rows of a sequence without steps (a bad length) are 0 and -inf.
-constexpr int JOIN_ROWS = 8, JOIN_THREADS = 256, JOIN_SLOTS = 128, JOIN_PAD = DC + 4;
+// takes eight rows, 16 contiguous KB of a slot's partials; a thread a row in 16 columns.  The block finds the
+// slots and weights of its rows side by side first, so that the partials are read without waiting for one
+// another.  Rows of a sequence without steps (a bad length) are 0 and -inf.
+constexpr int JOIN_ROWS = 8, JOIN_THREADS = 256, JOIN_SLOTS = 128;
 __global__ void __launch_bounds__(JOIN_THREADS)
 tree_tc_join_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ TreePlan pl) {
-    __shared__ __align__(16) float weight[JOIN_SLOTS][JOIN_ROWS];
-    __shared__ __align__(16) float sums[JOIN_ROWS][JOIN_PAD];
+    __shared__ float weight[JOIN_SLOTS][JOIN_ROWS];
     __shared__ int slots[JOIN_SLOTS];
     pdl_trigger();
     pdl_wait();
     const int g = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    if (g >= *pl.tiles) return;
-    const int4 t = pl.tile[g];
+    const int4 t = __ldcg(&pl.tile[g]);  // beside the other two; of no use behind the last tile
     const long long U = *pl.units;
+    if (g >= *pl.tiles) return;
     const int r0 = blockIdx.y * JOIN_ROWS, left = t.y, c0 = t.z, n = abs(t.w);
     if (r0 >= left || n == 1) return;
-    for (int i = tid; i < n; i += JOIN_THREADS) {
-        const int c = c0 + i;  // a pair without units left nothing; the first pair may have begun with another tile
-        slots[i] = unit_start(c, U, pl.pairs) == unit_start(c + 1, U, pl.pairs) ? -1 : 2 * c + (i == 0 && t.w < 0);
-    }
+    // A pair without units left nothing: it counts with weight 0 and any slot of the tile's.  The first pair may
+    // have begun with another tile.
+    const int first = 2 * c0 + (t.w < 0);
+    for (int i = tid; i < n; i += JOIN_THREADS)
+        slots[i] = i == 0 ? first : unit_start(c0 + i, U, pl.pairs) == unit_start(c0 + i + 1, U, pl.pairs) ? -1 : 2 * (c0 + i);
     __syncthreads();
     // a warp per row: its maximum, weights and sum
-    const size_t grow = (size_t)t.x + r0 + warp;
     float M = -INFINITY, l = 0.f;
     for (int i = lane; i < n; i += 32) {
         const float m = slots[i] < 0 ? -INFINITY : pl.m[slots[i] * TILE + r0 + warp];
@@ -1089,44 +1095,36 @@ tree_tc_join_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ 
     if (l != 0.f) {
         for (int i = lane; i < n; i += 32) weight[i][warp] /= l;
     }
-    if (a.lse && lane == 0 && r0 + warp < left) a.lse[grow] = l == 0.f ? -INFINITY : (base + log2f(l)) * 0.69314718055994531f;
+    if (a.lse && lane == 0 && r0 + warp < left)
+        a.lse[(size_t)t.x + r0 + warp] = l == 0.f ? -INFINITY : (base + log2f(l)) * 0.69314718055994531f;
     __syncthreads();
-    const int quad = (tid & 1) * 4, col = tid >> 1;  // rows quad .. quad + 3, columns col + 128 k
+    const int row = tid & 7, quad = tid >> 3;  // columns 4 quad .. + 3, + 128 k
+    const float *src = pl.o + ((size_t)(r0 / 8) * DC + quad * 4) * 8 + row * 4;
     float4 acc[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
+#pragma unroll 4
     for (int i = 0; i < n; ++i) {
-        if (slots[i] < 0) continue;
-        const float4 w = *reinterpret_cast<const float4 *>(&weight[i][quad]);
-        const float4 *src = reinterpret_cast<const float4 *>(
-            pl.o + (((size_t)slots[i] * (TILE / 8) + r0 / 8) * DC + col) * 8 + quad);
+        const float w = weight[i][row];
+        const float *part = src + (size_t)(slots[i] < 0 ? first : slots[i]) * TILE * DC;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            const float4 x = __ldcg(src + k * 128 * 2);
-            acc[k].x = w.x == 0.f ? acc[k].x : fmaf(w.x, x.x, acc[k].x);
-            acc[k].y = w.y == 0.f ? acc[k].y : fmaf(w.y, x.y, acc[k].y);
-            acc[k].z = w.z == 0.f ? acc[k].z : fmaf(w.z, x.z, acc[k].z);
-            acc[k].w = w.w == 0.f ? acc[k].w : fmaf(w.w, x.w, acc[k].w);
+            const float4 x = __ldcg(reinterpret_cast<const float4 *>(part + k * 128 * 8));
+            acc[k].x = w == 0.f ? acc[k].x : fmaf(w, x.x, acc[k].x);
+            acc[k].y = w == 0.f ? acc[k].y : fmaf(w, x.y, acc[k].y);
+            acc[k].z = w == 0.f ? acc[k].z : fmaf(w, x.z, acc[k].z);
+            acc[k].w = w == 0.f ? acc[k].w : fmaf(w, x.w, acc[k].w);
         }
     }
+    if (r0 + row >= left) return;
+    const size_t at = ((size_t)t.x + r0 + row) * DC + quad * 4;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-        sums[quad][col + 128 * k] = acc[k].x;
-        sums[quad + 1][col + 128 * k] = acc[k].y;
-        sums[quad + 2][col + 128 * k] = acc[k].z;
-        sums[quad + 3][col + 128 * k] = acc[k].w;
-    }
-    __syncthreads();
-    if (r0 + warp >= left) return;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {  // a warp per row
-        const float4 x = *reinterpret_cast<const float4 *>(&sums[warp][4 * lane + 128 * k]);
         if (a.out_bf16)
-            reinterpret_cast<uint2 *>(reinterpret_cast<__nv_bfloat16 *>(a.o) + grow * DC)[lane + 32 * k] =
-                make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
+            *reinterpret_cast<uint2 *>(reinterpret_cast<__nv_bfloat16 *>(a.o) + at + 128 * k) =
+                make_uint2(pack_bf16x2(acc[k].x, acc[k].y), pack_bf16x2(acc[k].z, acc[k].w));
         else
-            reinterpret_cast<float4 *>(reinterpret_cast<float *>(a.o) + grow * DC)[lane + 32 * k] = x;
+            *reinterpret_cast<float4 *>(reinterpret_cast<float *>(a.o) + at + 128 * k) = acc[k];
     }
 }
 
