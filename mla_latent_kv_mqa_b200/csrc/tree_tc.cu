@@ -24,13 +24,15 @@
 //
 // FP8.  K's codes are operands as they are, at twice the rate, against two e4m3 parts of each query, which
 // together are the bf16 query (split_query): no K passes through registers, and S takes as long as in bf16.
-// (Codes converted to bf16 tiles by four more warps: 593 us where this takes 490, and 96 registers a thread
-// for the softmax, which spilled.)  V would need P in parts too, and a part's range is too small for a long
-// context's weights: the cleaning warps turn V's codes into fp16 tiles, exactly, by two instructions for four
-// codes (bf16: eight, 2% slower in all), and P is fp16.  Its 11 bits reach from 2^15 down to 2^-14, so m is
-// chosen to bound P with the tokens' scales in it, and what is below 2^-27 of a row's largest weight times
-// scale loses bits (bf16 would keep 8 of them, where most weights have 11 here).  Content and RoPE scores
-// are apart, since only the first take the token's scale: one buffer of S, no second.
+// (K's codes converted to bf16 tiles by four more warps took 593 us where this takes 420, with 96 registers a
+// thread for the softmax, which spilled.)  V would need P in parts too, and a part's range is too small for a
+// long context's weights: the cleaning warps turn V's codes into fp16 tiles, exactly, by two instructions for
+// four codes (bf16 takes eight), and P is fp16.  Its 11 bits reach from 2^15 down to 2^-14, so m is chosen to
+// bound P with the tokens' scales in it; what is below 2^-16 of a row's largest weight times scale loses
+// bits, and below 2^-27 is lost.  Content and RoPE scores are apart, since only the first take the token's
+// scale: one buffer of S, no second.  What is left to the softmax and the conversion sets the pace (tensor
+// pipe 42% busy, clocks not limited): every instruction there shows, so the page's scales come two steps
+// after their page's id, without a wait, and what only a sequence's last pages need is out of the common path.
 //
 // Masks.  Steps before ctx need none.  In the others a row's thread selects by its node's bits.  P is 0
 // where a node does not see a token, and 0 times what such a row holds must be 0: the cleaning warps zero
@@ -67,13 +69,12 @@ constexpr int CB = PG * 128;                      // 64 rows x 64 bf16 columns, 
 constexpr int STAGE = 2 * CB;                     // K: two pages' 128 bytes a row; V: a page's 128 columns
 constexpr int F8_KST = DC / 128 + 1;              // FP8: K stages of a step, the codes' and the RoPE keys'
 constexpr int MAX_STAGES = 4;
-constexpr int P_SLOTS = 2;                        // pages of P held at once
-constexpr int Q_OFF = 0, P_OFF = NCB * CB, K_OFF = P_OFF + P_SLOTS * CB;
+constexpr int Q_OFF = 0, P_OFF = NCB * CB, K_OFF = P_OFF + SPG * CB;
 constexpr int RAW = 8192, RAW_STAGES = 2;         // FP8: the codes of a V stage, before their conversion
 // Shared memory and tensor memory of the bf16 (F8 = false) and FP8 kernels.
 template <bool F8>
 struct Lay {
-    static constexpr int k_stages = 4, v_stages = F8 ? 3 : 4;
+    static constexpr int k_stages = F8 ? 3 : 4, v_stages = 3;
     static constexpr int v_off = K_OFF + k_stages * STAGE, vraw_off = v_off + v_stages * STAGE;
     static constexpr int data = F8 ? vraw_off + RAW_STAGES * RAW : vraw_off;
     static constexpr int s_bufs = F8 ? 1 : 2;     // FP8: content and RoPE scores apart, one buffer of both
@@ -350,14 +351,29 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 }
 // At least log2 of a scale's size, by less than 1 (from -60 on).
 __device__ __forceinline__ int scale_exponent(float s) { return max((int)(__float_as_uint(s) >> 23 & 255u) - 126, -60); }
-// A pair of bf16 values (fp16: EXP = 0x7c00) with 0 for infinities and NaN.
-template <uint32_t EXP = 0x7f80u>
+// A pair of bf16 values with 0 for infinities and NaN.
 __device__ __forceinline__ uint32_t finite_pair(uint32_t x) {
-    return x & ((x & EXP) == EXP ? 0xffff0000u : 0xffffffffu) & ((x & (EXP << 16)) == (EXP << 16) ? 0xffffu : 0xffffffffu);
+    return x & ((x & 0x7f80u) == 0x7f80u ? 0xffff0000u : 0xffffffffu) & ((x & 0x7f800000u) == 0x7f800000u ? 0xffffu : 0xffffffffu);
 }
 
 __device__ __forceinline__ void ld_shared_v4(uint32_t at, uint32_t *x) {
     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(at));
+}
+
+// A thread's four chunks of codes where they landed, rows row0 (even k) and row0 + 32: 0 behind the sequence, and
+// for NaN in drafted rows.  Ahead of the conversion: selects in its loop cost every page 10%, in its registers 2%.
+__device__ __noinline__ void clean_codes(uint32_t src, int odd, int row0, int drafted, int end) {
+#pragma unroll 1
+    for (int k = 0; k < 4; ++k) {
+        const int row = row0 + 32 * (k & 1);
+        const uint32_t at = src + ((k >> 1) ^ odd) * 64 + (k & 1) * 4096;
+        if (row < drafted) continue;
+        uint32_t w[4];
+        ld_shared_v4(at, w);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) w[q] = row >= end ? 0u : w[q] & ~__vcmpeq4(w[q] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+        st_shared_v4(at, w[0], w[1], w[2], w[3]);
+    }
 }
 
 // FP8: a landed query row (nine blocks of 64 bf16 columns) becomes, in place, 2^k times itself as e4m3 operands
@@ -649,7 +665,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             for (int p = 0; ok && p < np; ++p) {
                 if (!(ok = wait(bar(ctrl->p_full[p]), (p_ph >> p) & 1u, abort_flag))) break;
                 p_ph ^= 1u << p;
-                const uint32_t pl_ = p_lo + (p & 1) * (CB >> 4);
+                const uint32_t pl_ = p_lo + p * (CB >> 4);
                 const bool acc = !it.first || p > 0;
 #pragma unroll 1
                 for (int nh = 0; nh < 2; ++nh) {
@@ -698,7 +714,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 const uint32_t src = data_s + Lay<F8>::vraw_off + (raw % RAW_STAGES) * RAW + row0 * 128 + c * 16;
                 const uint32_t dst = data_s + V_OFF + st.i * STAGE + row0 * 128;
                 const uint32_t dst0 = dst + (((2 * c) ^ (row0 & 7)) << 4), dst1 = dst + (((2 * c + 1) ^ (row0 & 7)) << 4);
-                const bool tail = drafted < PG;
+                if (drafted < PG) clean_codes(src, odd, row0, drafted, end);
                 uint32_t w[4][4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k)  // block k / 2 (odd rows: the other), rows row0 and row0 + 32
@@ -708,11 +724,6 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     uint32_t o[8];
 #pragma unroll
                     for (int q = 0; q < 4; ++q) e4m3x4_to_f16x4(w[k][q], o[2 * q], o[2 * q + 1]);
-                    if (tail) {
-                        const int row = row0 + 32 * (k & 1);
-#pragma unroll
-                        for (int q = 0; q < 8; ++q) o[q] = row >= end ? 0u : row >= drafted ? finite_pair<0x7c00u>(o[q]) : o[q];
-                    }
                     st_shared_v4(dst0 + ((k >> 1) ^ odd) * CB + (k & 1) * 4096, o[0], o[1], o[2], o[3]);
                     st_shared_v4(dst1 + ((k >> 1) ^ odd) * CB + (k & 1) * 4096, o[4], o[5], o[6], o[7]);
                 }
@@ -766,38 +777,40 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         // thread: row r of the CTA against page pg of the step (64 columns of S), and 128 of O's columns
         const int r = (warp & 1) * 32 + lane, half = (warp >> 1) & 1, cg = (warp - SM_WARP0) >> 2, pg = 2 * half + cg;
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t p_row = data_s + P_OFF + (uint32_t)(pg & 1) * CB + r * 128;
+        const uint32_t p_row = data_s + P_OFF + (uint32_t)pg * CB + r * 128;
         const uint32_t stage = data_s + P_OFF + (warp - SM_WARP0) * 2048;  // this warp's share of P, between tiles
         Walk it;
         it.init(a, &ctrl->w_b);
         float m = -INFINITY, l = 0.f;
-        int before = 0;  // steps so far that had the page pg ^ 2, which shares the slot of P
+        int before = 0;  // steps so far that had the page pg
         bool ok = true, good = true;
         float sc0 = 0.f, sc1 = 0.f;
         int sc_top = 0;
         bool sc_near = true;
         float(*scales)[PG] = ctrl->scale[warp - SM_WARP0];
-        auto load_scales = [&](const Walk &w) {
+        int next_block = -1;  // the page's in the tile's next step
+        auto block_of = [&](int step) {
+            const int g = step * SPG + pg;
+            return g * PG < it.s.L ? a.bt[(size_t)it.b * a.max_blocks + g] : -1;
+        };
+        auto load_scales = [&](int blk) {
             sc0 = sc1 = 0.f;
-            const int g = w.step * SPG + pg;
-            if (w.done() || g * PG >= w.s.L) return;
-            const int blk = a.bt[(size_t)w.b * a.max_blocks + g];
-            if (blk < 0 || blk >= a.num_blocks) return;  // the loader reports it
+            if (blk < 0 || blk >= a.num_blocks) return;  // the loader reports a bad one
             const float *src = a.kv_scale + (size_t)blk * PG + lane;
             sc0 = src[0];
             sc1 = src[32];
         };
-        if (F8) load_scales(it);
         float to_log2 = a.scale_log2;  // a score of S to log2 units
         int seg = 0;
         for (int u = 0; ok && !it.done(); ++u) {
             const int row = it.tile * TILE + (int)rank * HALF + r;  // of the sequence's (node, head) pairs
             const bool mine = row < it.s.n * a.n_h;
             const int sb = u & 1, buf = u % S_BUFS;
-            good = __all_sync(0xffffffffu, good && wait(bar(ctrl->s_full[buf]), (u / S_BUFS) & 1, abort_flag));
-            tc_fence_after();
-            uint32_t v[PG];
-            if (F8) {
+            if (F8) {  // the page's scales, before S is there
+                if (it.first) {
+                    load_scales(block_of(it.step));
+                    next_block = block_of(it.step + 1);
+                }
                 scales[0][lane] = sc0;
                 scales[0][lane + 32] = sc1;
                 sc0 = fabsf(sc0) <= FLT_MAX ? sc0 : 0.f;
@@ -805,10 +818,13 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 scales[1][lane] = sc0;
                 scales[1][lane + 32] = sc1;
                 const int e0 = scale_exponent(sc0), e1 = scale_exponent(sc1);
-                sc_top = __reduce_max_sync(0xffffffffu, max(e0, e1));
-                sc_near = sc_top - __reduce_min_sync(0xffffffffu, min(e0, e1)) <= 4;
+                sc_top = __shfl_sync(0xffffffffu, e0, 0) + 2;
+                sc_near = __all_sync(0xffffffffu, e0 <= sc_top && e0 >= sc_top - 4 && e1 <= sc_top && e1 >= sc_top - 4);
                 __syncwarp();
             }
+            good = __all_sync(0xffffffffu, good && wait(bar(ctrl->s_full[buf]), (u / S_BUFS) & 1, abort_flag));
+            tc_fence_after();
+            uint32_t v[PG];
             if (F8 && it.first) to_log2 = a.scale_log2 * ctrl->q_unit[seg++ & 1][r];
             if (good) {
                 const uint32_t sa = tmem + lane_base + S_COL + buf * 128 + cg * PG;
@@ -840,10 +856,9 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 __syncwarp();
                 if (lane == 0) mbar_arrive_pair(lead(ctrl->s_free[buf]));
             }
-            if (F8) {  // the next step's scales: the table's and their latency pass under this step
-                Walk ahead = it;
-                ahead.next(a);
-                load_scales(ahead);
+            if (F8 && !it.last()) {  // on their way under this step, and the table's entry two steps ahead, so that nothing waits
+                load_scales(next_block);
+                next_block = block_of(it.step + 2);
             }
             const int j0 = it.step * STEP + pg * PG;
             if (j0 + PG > it.s.ctx) {
@@ -858,7 +873,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             }
             // The largest score in log2 units.  FP8: P is exp2(score - m) times the token's scale, in fp16, so m bounds
             // score + log2(scale) - 7.  P's largest is then between 2^2 and 2^7, and below 2^15 when m moves.  The scales
-            // of a page count as their largest where they are within 2^4 of one another, else each as it is.
+            // of a page count as four times its first where all are within 2^2 of that, else each as it is.
             float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
             float top;
             if (!F8 || sc_near) {
@@ -929,10 +944,8 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             if (lane == 0) mbar_arrive_pair(lead(ctrl->o_ok[sb]));
             const int np = it.pages();
             if (pg < np) {  // P is 0 behind the last page, and nothing multiplies it
-                // The slot's last user: page pg + 2 of the step before (a tile's first step finds all MMAs done),
-                // or page pg - 2 of this one.
-                if (pg >= 2 || !it.first)
-                    good = good && wait(bar(ctrl->p_free[pg ^ 2]), (before - (pg < 2)) & 1, abort_flag);
+                // its MMAs of the step before (a tile's first step finds all of them done)
+                if (!it.first) good = good && wait(bar(ctrl->p_free[pg]), (before - 1) & 1, abort_flag);
 #pragma unroll
                 for (int c = 0; c < PG / 8; ++c)  // eight tokens: one 16-byte chunk of P's row
                     st_shared_v4(p_row + ((c ^ (r & 7)) << 4), v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
@@ -940,7 +953,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 __syncwarp();
                 if (lane == 0) mbar_arrive_pair(lead(ctrl->p_full[pg]));
             }
-            before += (pg ^ 2) < np;
+            before += pg < np;
 
             if (it.last()) {
                 ctrl->sum[pg][r] = l;

@@ -42,7 +42,7 @@ def run(seed, units, planted=None, bufs=2):
     votes = [{"n": 0, "gen": 0} for _ in range(CTAS)]
     S = [None, None]                       # unit whose scores a buffer holds
     read_s = {}                            # unit -> warps that have read it
-    P = {}                                 # (cta, slot, half) -> (unit, page): two slots hold four pages in turn
+    P = {}                                 # (cta, page, half) -> unit
     q_empty, q_full = [Bar(1) for _ in range(CTAS)], Bar(CTAS)
     unit = {}                              # (cta, segment parity) -> segment whose scores' unit it is
     read_q = {}                            # (cta, segment) -> warps that have read it
@@ -88,7 +88,7 @@ def run(seed, units, planted=None, bufs=2):
                 while not p_full[p].passed(ph[p]):
                     yield
                 ph[p] ^= 1
-                assert all(P.get((c, p & 1, h)) == (u, p) for c in range(CTAS) for h in range(2)), "P not written"
+                assert all(P.get((c, p, h)) == u for c in range(CTAS) for h in range(2)), "P not written"
                 tensor["pv"] += [("O", u, p), ("c", p_free[p])]
                 yield
             tensor["pv"] += [("end", u), ("c", pv_done[u & 1])]
@@ -128,13 +128,12 @@ def run(seed, units, planted=None, bufs=2):
             o_ok[u & 1].arrive()
             yield
             if pg < pages:
-                wait = (pg >= 2 or not first) and planted != 'no wait for P'
-                while wait and not p_free[pg ^ 2][cta].passed(before - (pg < 2)):
+                while not first and planted != 'no wait for P' and not p_free[pg][cta].passed(before - 1):
                     yield
-                P[cta, pg & 1, h] = u, pg
+                P[cta, pg, h] = u
                 p_full[pg].arrive()
                 yield
-            before += (pg ^ 2) < pages
+            before += pg < pages
             if last:
                 while not pv_done[sb][cta].passed(u >> 1):
                     yield
@@ -151,7 +150,7 @@ def run(seed, units, planted=None, bufs=2):
                     S[op[1] % bufs] = op[1]
                 elif op[0] == "O":
                     started.add(op[1])
-                    assert all(P.get((c, op[2] & 1, h)) == op[1:] for c in range(CTAS) for h in range(2)), "P overwritten before it was read"
+                    assert all(P.get((c, op[2], h)) == op[1] for c in range(CTAS) for h in range(2)), "P overwritten before it was read"
                 elif op[0] == "end":
                     done.add(op[1])
                 else:
