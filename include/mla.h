@@ -371,7 +371,8 @@ mla_status_t mla_lse_merge_finish(int rows, int n_h, int d_c, const float *acc, 
  * One step: mla_tree_prepare once; per layer mla_tree_append, mla_absorb_q (pos from
  * mla_tree_prepare), mla_decode_tree, mla_out_proj; after verification mla_cache_keep.
  * A sequence with more nodes than the arguments allow, or whose rows are not rows of the batch, sets
- * MLA_ERR_BAD_TREE on the device and is skipped.  At most MLA_MAX_TREE_NODES nodes a sequence.
+ * MLA_ERR_BAD_TREE on the device; its outputs mean nothing then, and nor do the batch's (each call takes the
+ * other sequences or leaves them out).  At most MLA_MAX_TREE_NODES nodes a sequence.
  * ---------------------------------------------------------------------------------------- */
 #define MLA_MAX_TREE_NODES 1024
 

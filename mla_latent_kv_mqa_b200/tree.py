@@ -18,6 +18,7 @@ from __future__ import annotations
 import torch
 
 from . import native as N
+from .layer import index_tensors, same_caches
 
 
 class DraftTrees:
@@ -30,17 +31,25 @@ class DraftTrees:
     def __init__(self, cu_nodes: torch.Tensor, parent: torch.Tensor, max_nodes: int, mask: torch.Tensor | None = None):
         if not 1 <= max_nodes <= N.MLA_MAX_TREE_NODES:
             raise ValueError(f"max_nodes must be in [1, {N.MLA_MAX_TREE_NODES}]")
+        for x in (cu_nodes, parent):
+            if x.dtype != torch.int32 or x.dim() != 1 or not x.is_contiguous():
+                raise ValueError("cu_nodes and parent must be contiguous int32 vectors")
+        if cu_nodes.numel() < 1:
+            raise ValueError("cu_nodes must have an entry per sequence and one more")
         self.cu_nodes, self.parent, self.max_nodes = cu_nodes, parent, int(max_nodes)
         self.B, self.total_nodes = cu_nodes.numel() - 1, parent.numel()
         self.mask_words = (self.max_nodes + 31) // 32 if mask is None else mask.shape[1]
         if mask is not None and (mask.shape[0] != self.total_nodes or 32 * self.mask_words < self.max_nodes or
-                                 not mask.is_contiguous()):
-            raise ValueError("mask must be contiguous [total_nodes, >= ceil(max_nodes / 32)]")
+                                 mask.dtype != torch.int32 or not mask.is_contiguous()):
+            raise ValueError("mask must be contiguous int32 [total_nodes, >= ceil(max_nodes / 32)]")
         dev = cu_nodes.device
         self.mask = torch.empty((self.total_nodes, self.mask_words), dtype=torch.int32, device=dev) if mask is None else mask
         self.pos, self.slot, self.seq_idx = (torch.empty(self.total_nodes, dtype=torch.int32, device=dev) for _ in range(3))
 
     def prepare(self, seq_lens, stream=None):
+        if seq_lens.shape[0] != self.B:
+            raise ValueError("prepare: seq_lens has an entry per tree")
+        index_tensors(self.cu_nodes, seq_lens)
         N.mla_tree_prepare(self.B, self.cu_nodes, self.total_nodes, self.parent, seq_lens, self.mask_words, self.mask,
                            self.pos, self.slot, self.seq_idx, stream)
 
@@ -48,9 +57,12 @@ class DraftTrees:
         """The rows of the accepted nodes ``keep`` [B, max_keep] (each row's first num_keep[b],
         ascending) to behind the committed tokens, in every cache; returns the new lengths."""
         B, max_blocks = block_table.shape
+        if B != self.B or seq_lens.shape[0] != B or keep.shape[0] != B or num_keep.shape[0] != B:
+            raise ValueError("keep: block_table, seq_lens, keep and num_keep have a row per tree")
+        index_tensors(block_table, seq_lens, keep, num_keep, new_lens)
         if new_lens is None:
             new_lens = torch.empty_like(seq_lens)
-        pools = N.make_pools([c.pool() for c in caches])
-        N.mla_cache_keep(caches[0].dims, pools, B, self.cu_nodes, self.total_nodes, block_table, max_blocks,
+        dims, pools = same_caches(caches, caches[0].num_blocks), N.make_pools([c.pool() for c in caches])
+        N.mla_cache_keep(dims, pools, B, self.cu_nodes, self.total_nodes, block_table, max_blocks,
                          caches[0].num_blocks, seq_lens, keep, num_keep, keep.shape[1], new_lens, stream)
         return new_lens

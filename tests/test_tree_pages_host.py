@@ -48,9 +48,11 @@ def test_tree_calls_refuse_bad_arguments(N):
         assert dec(**{k: None}) == bad, k
     assert dec(ws=16) == bad and dec(kr=16) == bad
     assert dec(out=N.MLA_DTYPE_FP8_E4M3) == N.MLA_ERR_UNSUPPORTED
-    assert dec(nbytes=1024) == N.MLA_ERR_WORKSPACE_TOO_SMALL
+    assert dec(nbytes=255) == N.MLA_ERR_WORKSPACE_TOO_SMALL
     assert dec(B=0, q=None) == N.MLA_OK and dec(T=0, q=None) == N.MLA_OK
     s = _v3(N, flags=N.MLA_FLAG_SIMT_DECODE)
+    few = N.make_dims(2, 64, 128, 32)                                       # one block a segment: more than a cluster joins
+    assert N.mla_decode_tree_workspace_size(few, 1, 1, 1 << 18) > 1 << 14
     assert 0 < N.mla_decode_tree_workspace_size(s, 2, 6, 256)
     assert N.mla_decode_tree_workspace_size(s, 2, -1, 256) == 0 and N.mla_decode_tree_workspace_size(s, 2, 6, 0) == 0
 
@@ -131,3 +133,47 @@ def test_plain_pages_count_every_holder():
             p.compact()
         held = np.bincount(p.table[p.table >= 0], minlength=20)
         assert np.array_equal(held, p.refs)
+
+
+def test_the_python_calls_refuse_what_the_kernels_would_misread(N):
+    """Shapes, types and places of tensors, checked before any address is handed on."""
+    import torch
+    from mla_latent_kv_mqa_b200 import layer as L, pages as P, tree as T
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32)
+    dims = L.dims_for(2, 8, 16, 4, act="f32", kv="f32", page=4)
+    trees = T.DraftTrees(i32(0, 2), i32(-1, 0), 2)
+    for cu, parent in ((torch.tensor([0, 2]), i32(-1, 0)), (i32(0, 2), torch.tensor([-1, 0])), (i32(0, 9, 2, 9)[::2], i32(-1, 0)),
+                       (i32(), i32())):
+        with pytest.raises(ValueError):
+            T.DraftTrees(cu, parent, 2)
+    for mask in (torch.zeros(2, 1), torch.zeros(3, 1, dtype=torch.int32), torch.zeros(2, 0, dtype=torch.int32)):
+        with pytest.raises(ValueError):
+            T.DraftTrees(i32(0, 2), i32(-1, 0), 2, mask=mask)
+    cache = L.PagedLatentCache(dims, 3, device="cpu")
+    other = L.PagedLatentCache(dims, 4, device="cpu")
+    lay = L.MLADecodeLayer.__new__(L.MLADecodeLayer)
+    lay.dims = dims
+    table, lens = torch.zeros(1, 2, dtype=torch.int32), i32(5)
+    q = torch.zeros(2, 2, 20)
+    for bad in (dict(q_abs=torch.zeros(3, 2, 20)), dict(q_abs=torch.zeros(2, 20, 2).transpose(1, 2)), dict(seq_lens=i32(5, 5)),
+                dict(block_table=torch.zeros(2, 2, dtype=torch.int32)), {}):     # the last: host tensors
+        with pytest.raises(ValueError):
+            lay.decode_tree(**{**dict(cache=cache, q_abs=q, block_table=table, seq_lens=lens, trees=trees, max_seq_len=8), **bad})
+    with pytest.raises(ValueError):
+        lay.tree_append(cache, torch.zeros(3, 16), torch.zeros(3, 4), trees, table)
+    with pytest.raises(ValueError):
+        trees.prepare(i32(5, 5))
+    with pytest.raises(ValueError):
+        trees.keep([cache], table, lens, torch.zeros(2, 1, dtype=torch.int32), i32(1))
+    with pytest.raises(ValueError):
+        L.same_caches([cache, other], 3)
+    with pytest.raises(ValueError):
+        L.same_caches([cache, L.PagedLatentCache(L.dims_for(2, 8, 16, 4, act="f32", kv="bf16", page=4), 3, device="cpu")], 3)
+    seqs = P.PagedSequences(4, 2, 3, 3, device="cpu")
+    for call in (lambda: seqs.fork(i32(0), i32(1)), lambda: seqs.fork(i32(0), i32(0, 1)), lambda: seqs.grow(torch.tensor([4])),
+                 lambda: seqs.trim(i32(0, 0), i32(1)), lambda: seqs.compact(), lambda: seqs.copy_pages([other], None),
+                 lambda: seqs.copy_pages([L.PagedLatentCache(L.dims_for(2, 8, 16, 4, act="f32", kv="f32", page=8), 3, device="cpu")], None)):
+        with pytest.raises(ValueError):
+            call()
+    with pytest.raises(AttributeError):
+        seqs.seq_lens = i32(0, 0)
