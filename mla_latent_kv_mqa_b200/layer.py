@@ -89,25 +89,18 @@ class PagedLatentCache:
         return n
 
 
-def on_current_device(*tensors) -> None:
-    """The kernels run on the current device: a tensor elsewhere (None aside) is refused, not read from there."""
-    for x in tensors:
-        if x is not None and (x.get_device() < 0 or x.get_device() != torch._C._cuda_getDevice()):
-            raise ValueError(f"a tensor is on {x.device}, not on the current CUDA device")
-
-
-def index_tensors(*tensors) -> None:
-    """Contiguous int32 on the current device (None aside), as the C calls read them."""
-    for x in tensors:
-        if x is not None and (x.dtype != torch.int32 or not x.is_contiguous()):
-            raise ValueError("lengths, tables and indices are contiguous int32 tensors")
-    on_current_device(*tensors)
+# The kernels run on the current device and read rows and indices as they lie: a tensor elsewhere, of another type or
+# with strides of its own is refused, not misread.  (Written out where it is called: a helper per tensor costs a
+# microsecond a call.)
+_INT32 = torch.int32
+_on_device = getattr(torch._C, "_cuda_getDevice", None)
+_MISREAD = ("tensors are contiguous and on the current CUDA device; lengths, tables and indices are int32")
 
 
 def same_caches(caches, num_blocks) -> N.mla_dims_t:
     """The dims of caches behind one block table, which are of one shape and have its blocks."""
     dims = caches[0].dims
-    for c in caches:
+    for c in caches if len(caches) > 1 or caches[0].num_blocks != num_blocks else ():
         if c.num_blocks != num_blocks or (c.dims is not dims and bytes(c.dims) != bytes(dims)):
             raise ValueError("caches behind one block table are of one shape and have its number of blocks")
     return dims
@@ -242,13 +235,14 @@ class MLADecodeLayer:
     def tree_append(self, cache: PagedLatentCache, c_kv, k_r, trees, block_table, stream=None):
         """The drafted nodes' rows into their slots (trees.prepare first)."""
         B, max_blocks = block_table.shape
-        if c_kv.shape[0] != trees.total_nodes or k_r.shape[0] != trees.total_nodes or B != trees.B:
+        T, here = trees.total_nodes, c_kv.get_device()
+        if c_kv.size(0) != T or k_r.size(0) != T or B != trees.B:
             raise ValueError("tree_append: c_kv and k_r have a row per node, block_table one per tree")
-        if not c_kv.is_contiguous() or not k_r.is_contiguous():
-            raise ValueError("tree_append: c_kv and k_r are contiguous")
-        on_current_device(c_kv, k_r)
-        index_tensors(block_table)
-        N.mla_tree_append(self.dims, c_kv.shape[0], c_kv, k_r, trees.seq_idx, trees.slot, trees.pos, block_table, B,
+        if (here < 0 or here != _on_device() or k_r.get_device() != here or block_table.get_device() != here or
+                trees.slot.get_device() != here or cache.kv_pool.get_device() != here or block_table.dtype is not _INT32 or
+                not (c_kv.is_contiguous() and k_r.is_contiguous() and block_table.is_contiguous())):
+            raise ValueError(_MISREAD)
+        N.mla_tree_append(self.dims, T, c_kv, k_r, trees.seq_idx, trees.slot, trees.pos, block_table, B,
                           max_blocks, cache.num_blocks, cache.kv_pool, cache.kr_pool, cache.kv_scale, stream)
 
     def decode_tree(self, cache: PagedLatentCache, q_abs, block_table, seq_lens, trees, max_seq_len,
@@ -260,10 +254,14 @@ class MLADecodeLayer:
         B, max_blocks = block_table.shape
         T = trees.total_nodes
         dt = DTYPE[out_dtype]
-        if q_abs.shape[0] != T or B != trees.B or seq_lens.shape[0] != B or not q_abs.is_contiguous():
-            raise ValueError("decode_tree: q_abs has a row per node, contiguous; block_table and seq_lens one per tree")
-        on_current_device(q_abs)
-        index_tensors(block_table, seq_lens)
+        if q_abs.size(0) != T or B != trees.B or seq_lens.numel() != B:
+            raise ValueError("decode_tree: q_abs has a row per node, block_table and seq_lens one per tree")
+        here = q_abs.get_device()
+        if (here < 0 or here != _on_device() or block_table.get_device() != here or seq_lens.get_device() != here or
+                trees.cu_nodes.get_device() != here or cache.kv_pool.get_device() != here or
+                block_table.dtype is not _INT32 or seq_lens.dtype is not _INT32 or
+                not (q_abs.is_contiguous() and block_table.is_contiguous() and seq_lens.is_contiguous())):
+            raise ValueError(_MISREAD)
         if o_lat is None:
             o_lat = q_abs.new_empty((T, d.n_h, d.d_c), dtype=TORCH_ACT[dt])
         elif o_lat.dtype != TORCH_ACT[dt] or tuple(o_lat.shape) != (T, d.n_h, d.d_c) or not o_lat.is_contiguous():

@@ -16,7 +16,7 @@ from __future__ import annotations
 import torch
 
 from . import native as N
-from .layer import Workspace, index_tensors, on_current_device, same_caches
+from .layer import _INT32, _MISREAD, Workspace, _on_device, same_caches
 
 
 class PageMoves:
@@ -54,6 +54,7 @@ class PagedSequences:
         self._table = N.make_page_table(page_size, num_seqs, max_blocks, num_blocks, self._block_table, self._refs,
                                         self._seq_lens)
         self._ws = Workspace(self._block_table.device)
+        self._device = self._refs.get_device()
 
     # Written in place (copy_), not replaced: the calls hold their addresses.
     @property
@@ -68,6 +69,14 @@ class PagedSequences:
     def seq_lens(self) -> torch.Tensor:
         return self._seq_lens
 
+    def _look_over(self, *indices):
+        here = self._device
+        if here < 0 or here != _on_device():
+            raise ValueError(_MISREAD)
+        for x in indices:
+            if x is not None and (x.dtype is not _INT32 or x.get_device() != here or not x.is_contiguous()):
+                raise ValueError(_MISREAD)
+
     def _workspace(self, n: int, stream):
         return self._ws.get(n, stream, lambda: N.mla_pages_workspace_size(self._table, n))
 
@@ -75,7 +84,7 @@ class PagedSequences:
         """Sequence child[i] becomes a copy of parent[i]; all parents are read before any child changes."""
         if parent.numel() != child.numel():
             raise ValueError("fork: a parent for every child")
-        index_tensors(self._refs, parent, child)
+        self._look_over(parent, child)
         n = parent.numel()
         ws = self._workspace(n, stream)
         N.mla_pages_fork(self._table, n, parent, child, ws, ws.numel(), stream)
@@ -86,7 +95,7 @@ class PagedSequences:
         n = new_lens.numel()
         if seqs is not None and seqs.numel() != n:
             raise ValueError("grow: a length for every sequence")
-        index_tensors(self._refs, new_lens, seqs)
+        self._look_over(new_lens, seqs)
         ws = self._workspace(n, stream)
         moves = PageMoves(n, self._block_table.device)
         N.mla_pages_grow(self._table, n, seqs, new_lens, moves.pairs_ptr, moves.number_ptr, ws, ws.numel(), stream)
@@ -96,12 +105,12 @@ class PagedSequences:
         """Sequences are cut to ``new_lens`` tokens (0: the sequence ends); their pages lose a holder."""
         if seqs is not None and seqs.numel() != new_lens.numel():
             raise ValueError("trim: a length for every sequence")
-        index_tensors(self._refs, new_lens, seqs)
+        self._look_over(new_lens, seqs)
         N.mla_pages_trim(self._table, new_lens.numel(), seqs, new_lens, stream)
 
     def compact(self, stream=None):
         """The pages in use take the lowest ids; returns the page copies to make (PageMoves), for copy_pages."""
-        on_current_device(self._refs)
+        self._look_over()
         ws = self._workspace(0, stream)
         moves = PageMoves(self.num_blocks // 2, self._block_table.device)
         N.mla_pages_compact(self._table, moves.pairs_ptr, moves.number_ptr, ws, ws.numel(), stream)
@@ -114,12 +123,14 @@ class PagedSequences:
         dims = same_caches(caches, self.num_blocks)
         if dims.page_size != self._table.page_size:
             raise ValueError("copy_pages: the caches' pages are not the table's")
-        on_current_device(caches[0].kv_pool)
+        self._look_over()
+        if any(c.kv_pool.get_device() != self._device for c in caches):
+            raise ValueError(_MISREAD)
         pools = N.make_pools([c.pool() for c in caches])
         if isinstance(moves, PageMoves):
             pairs, number, most = moves.pairs_ptr, moves.number_ptr, moves.most
         else:
             pairs, number = moves
-            index_tensors(pairs, number)
+            self._look_over(pairs, number)
             most = pairs.shape[0]
         N.mla_cache_copy_pages(dims, pools, self.num_blocks, pairs, number, most, stream)

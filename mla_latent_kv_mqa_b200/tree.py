@@ -18,7 +18,7 @@ from __future__ import annotations
 import torch
 
 from . import native as N
-from .layer import index_tensors, same_caches
+from .layer import _INT32, _MISREAD, _on_device, same_caches
 
 
 class DraftTrees:
@@ -47,9 +47,12 @@ class DraftTrees:
         self.pos, self.slot, self.seq_idx = (torch.empty(self.total_nodes, dtype=torch.int32, device=dev) for _ in range(3))
 
     def prepare(self, seq_lens, stream=None):
-        if seq_lens.shape[0] != self.B:
+        if seq_lens.numel() != self.B:
             raise ValueError("prepare: seq_lens has an entry per tree")
-        index_tensors(self.cu_nodes, seq_lens)
+        here = seq_lens.get_device()
+        if (here < 0 or here != _on_device() or self.cu_nodes.get_device() != here or seq_lens.dtype is not _INT32 or
+                not seq_lens.is_contiguous()):
+            raise ValueError(_MISREAD)
         N.mla_tree_prepare(self.B, self.cu_nodes, self.total_nodes, self.parent, seq_lens, self.mask_words, self.mask,
                            self.pos, self.slot, self.seq_idx, stream)
 
@@ -57,11 +60,19 @@ class DraftTrees:
         """The rows of the accepted nodes ``keep`` [B, max_keep] (each row's first num_keep[b],
         ascending) to behind the committed tokens, in every cache; returns the new lengths."""
         B, max_blocks = block_table.shape
-        if B != self.B or seq_lens.shape[0] != B or keep.shape[0] != B or num_keep.shape[0] != B:
+        if B != self.B or seq_lens.numel() != B or keep.size(0) != B or num_keep.numel() != B:
             raise ValueError("keep: block_table, seq_lens, keep and num_keep have a row per tree")
-        index_tensors(block_table, seq_lens, keep, num_keep, new_lens)
+        here = seq_lens.get_device()
+        if (here < 0 or here != _on_device() or self.cu_nodes.get_device() != here or block_table.get_device() != here or
+                keep.get_device() != here or num_keep.get_device() != here or caches[0].kv_pool.get_device() != here or
+                block_table.dtype is not _INT32 or seq_lens.dtype is not _INT32 or keep.dtype is not _INT32 or
+                num_keep.dtype is not _INT32 or
+                not (block_table.is_contiguous() and seq_lens.is_contiguous() and keep.is_contiguous() and num_keep.is_contiguous())):
+            raise ValueError(_MISREAD)
         if new_lens is None:
             new_lens = torch.empty_like(seq_lens)
+        elif new_lens.dtype is not _INT32 or new_lens.numel() != B or new_lens.get_device() != here or not new_lens.is_contiguous():
+            raise ValueError(_MISREAD)
         dims, pools = same_caches(caches, caches[0].num_blocks), N.make_pools([c.pool() for c in caches])
         N.mla_cache_keep(dims, pools, B, self.cu_nodes, self.total_nodes, block_table, max_blocks,
                          caches[0].num_blocks, seq_lens, keep, num_keep, keep.shape[1], new_lens, stream)
