@@ -387,7 +387,7 @@ mla_status_t mla_lse_merge_finish(int rows, int n_h, int d_c, const float *acc, 
  *              cu_nodes[B], and those of a sequence with seq_lens[b] < n_b (MLA_ERR_BAD_SEQ_LEN), get
  *              seq_idx -1, which mla_tree_append skips; the former get mask, pos and slot 0.
  * A parent outside [-1, k) sets MLA_ERR_BAD_TREE; the node is taken as a child of the last committed
- * token.  B = 0 with total_nodes = 0 is a no-op. */
+ * token.  The rows of a sequence that is no tree of the batch get seq_idx -1, pos and slot 0.  B = 0 with total_nodes = 0 is a no-op. */
 mla_status_t mla_tree_prepare(int B, const int32_t *cu_nodes, int total_nodes, const int32_t *parent,
                               const int32_t *seq_lens, int mask_words, uint32_t *mask, int32_t *pos,
                               int32_t *slot, int32_t *seq_idx, mla_stream_t stream);
@@ -427,6 +427,7 @@ mla_status_t mla_tree_append(const mla_dims_t *dims, int T, const void *c_kv, co
  * cache P times the token's scale to fp16 instead (11 bits; fewer for a token below 2^-16 of the row's
  * largest, to 2^-27 of it), and a query's content elements below 2^-9 of their row's largest are taken to
  * 2^-17 of it.  A query row with infinities or NaN gets NaN.
+ * MLA_FLAG_FP8_MMA and MLA_FLAG_TEST_GIVE_UP do not concern this call.
  * Deterministic: the result depends only on the logical cache content. */
 size_t mla_decode_tree_workspace_size(const mla_dims_t *dims, int B, int total_nodes, int max_seq_len);
 mla_status_t mla_decode_tree(const mla_dims_t *dims, int B, const int32_t *cu_nodes, int total_nodes,

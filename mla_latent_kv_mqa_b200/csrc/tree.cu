@@ -43,6 +43,11 @@ tree_prepare_kernel(int B, const int32_t *cu, int T, const int32_t *parent,
     TreeSpan sp;
     if (!tree_span(cu, b, B, T, 32 * words, &sp)) {
         if (threadIdx.x == 0) record_error(err, kErrBadTree);
+        // what an earlier step left in these rows must not send mla_tree_append anywhere
+        for (int t = (b == 0 ? 0 : max(cu[b], 0)) + threadIdx.x; t < min(cu[b + 1], T); t += kPrepThreads) {
+            pos[t] = slot[t] = 0;
+            seq_idx[t] = -1;
+        }
         return;
     }
     const int ctx = seq_lens[b] - sp.n;

@@ -618,3 +618,17 @@ def test_two_streams_at_once_and_a_workspace_that_grows():
     del junk
     assert torch.equal(o, want_a[0]) and torch.equal(lse, want_a[1])
     no_error()
+
+
+@pytest.mark.parametrize("cu,rows", [([0, 40, 43], range(0, 40)), ([3, 5, 43], range(0, 5)), ([0, 2, 60], range(2, 43))])
+def test_prepare_leaves_no_place_in_the_rows_of_what_is_no_tree(cu, rows):
+    """More nodes than the mask has bits, rows before the first, rows behind the last: the rows' sequence is none,
+    whatever an earlier step left there, so that an append goes nowhere."""
+    from mla_latent_kv_mqa_b200 import native as N, tree as T
+    trees = T.DraftTrees(dev(cu), dev(np.full(43, -1)), 32)
+    for x in (trees.seq_idx, trees.slot, trees.pos):
+        x.fill_(1)
+    trees.prepare(dev([100, 100]))
+    torch.cuda.synchronize()
+    assert N.mla_get_last_device_error() == N.MLA_ERR_BAD_TREE
+    assert (trees.seq_idx.cpu().numpy()[list(rows)] == -1).all()
