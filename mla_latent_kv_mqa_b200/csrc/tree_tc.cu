@@ -31,7 +31,7 @@
 // bound P with the tokens' scales in it; what is below 2^-16 of a row's largest weight times scale loses
 // bits, and below 2^-27 is lost.  Content and RoPE scores are apart, since only the first take the token's
 // scale: one buffer of S, no second.  What is left to the softmax and the conversion sets the pace (tensor
-// pipe 42% busy, clocks not limited): every instruction there shows, so the page's scales come two steps
+// pipe 50% busy, clocks not limited): every instruction there shows, so the page's scales come two steps
 // after their page's id, without a wait, and what only a sequence's last pages need is out of the common path.
 //
 // Masks.  Steps before ctx need none.  In the others a row's thread selects by its node's bits.  P is 0
