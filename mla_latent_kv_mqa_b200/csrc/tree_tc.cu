@@ -43,11 +43,11 @@
 // equal runs; a tile that lies in several runs leaves partial (O, m, l), at most two a pair, which a
 // second kernel joins.
 //
-// Measured (one B200, warm): 24 sequences of 1024-8190 tokens, 3-24 nodes, 128 heads 440 us = 1060 TFLOP/s;
-// 16 of 6000-8192, 64 nodes 1.81 ms = 1120; 4 of 131072, 4 nodes 555 us = 1050; FP8, 32 of 4097-8192, 2-12 nodes
-// 418 us = 960.  (GPUs that power holds lower: 13% more.)  A step takes ~6700 clocks over bf16, of which the
-// MMAs run 4352 and shared memory is busy ~5500 (each operand byte is written once and read once by each of
-// its MMAs, with 64 rows a CTA against it).
+// Measured (one B200, warm): 24 sequences of 1024-8190 tokens, 3-24 nodes, 128 heads 431 us = 1080 TFLOP/s;
+// 16 of 6000-8192, 64 nodes 1.8 ms = 1130; 4 of 131072, 4 nodes 538 us = 1090; FP8, 32 of 4097-8192, 2-12 nodes
+// 420 us = 950.  (GPUs that power holds lower: 13% more.)  A step takes ~6600 clocks over bf16, of which the
+// MMAs run 4352.  L2 hands the SMs 5.1 GB a call, 11.5 TB/s where loads alone reach 12.4 (557 KB a step and pair:
+// 128 rows a pair use a byte, and O leaves no tensor memory for more rows), and shared memory is busy ~5500 clocks.
 //
 // Every wait is bounded (2 s).  On give-up both CTAs' abort flags are set, MLA_ERR_DEVICE_TIMEOUT is
 // recorded, and both CTAs stay until copies and MMAs in flight have had time to land.
@@ -362,6 +362,39 @@ __device__ __forceinline__ uint32_t finite_pair(uint32_t x) {
     return x & ((x & 0x7f80u) == 0x7f80u ? 0xffff0000u : 0xffffffffu) & ((x & 0x7f800000u) == 0x7f800000u ? 0xffffu : 0xffffffffu);
 }
 
+// Two fp32 values an instruction, and a maximum of three: fewer instructions are also less power, which holds the clock
+// over bf16 (ragged batch 443 -> 431 us).
+__device__ __forceinline__ uint64_t pair_of(uint32_t lo, uint32_t hi) {
+    uint64_t x;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "r"(lo), "r"(hi));
+    return x;
+}
+__device__ __forceinline__ uint64_t pair_of(float lo, float hi) { return pair_of(__float_as_uint(lo), __float_as_uint(hi)); }
+__device__ __forceinline__ float2 floats_of(uint64_t x) {
+    uint32_t lo, hi;
+    asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(x));
+    return make_float2(__uint_as_float(lo), __uint_as_float(hi));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
 __device__ __forceinline__ void ld_shared_v4(uint32_t at, uint32_t *x) {
     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(at));
 }
@@ -845,11 +878,13 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
 #pragma unroll
                         for (int j = 0; j < 16; j += 4) {
                             const float4 sc = *reinterpret_cast<const float4 *>(&scales[0][16 * c + j]);
-                            const float t[4] = {sc.x, sc.y, sc.z, sc.w};
+                            const uint64_t t[2] = {pair_of(sc.x, sc.y), pair_of(sc.z, sc.w)};
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                uint32_t &y = v[16 * c + j + i];
-                                y = __float_as_uint(fmaf(__uint_as_float(x[j + i]), t[i], __uint_as_float(y)));
+                            for (int i = 0; i < 2; ++i) {
+                                uint32_t *y = v + 16 * c + j + 2 * i;
+                                const float2 d = floats_of(fma2(pair_of(x[j + 2 * i], x[j + 2 * i + 1]), t[i], pair_of(y[0], y[1])));
+                                y[0] = __float_as_uint(d.x);
+                                y[1] = __float_as_uint(d.y);
                             }
                         }
                     }
@@ -884,8 +919,8 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             float top;
             if (!F8 || sc_near) {
 #pragma unroll
-                for (int j = 0; j < PG; ++j) x[j & 3] = fmaxf(x[j & 3], __uint_as_float(v[j]));
-                top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * to_log2 + (F8 ? (float)(sc_top - 7) : 0.f);
+                for (int j = 0; j < PG; j += 2) x[j >> 1 & 3] = max3(x[j >> 1 & 3], __uint_as_float(v[j]), __uint_as_float(v[j + 1]));
+                top = max3(fmaxf(x[0], x[1]), x[2], x[3]) * to_log2 + (F8 ? (float)(sc_top - 7) : 0.f);
             } else {
 #pragma unroll
                 for (int j = 0; j < PG; ++j)
@@ -908,25 +943,26 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 m = fmaxf(m, top);
             }
             const float base = m == -INFINITY ? 0.f : m;
-            float s[4] = {0.f, 0.f, 0.f, 0.f};
+            uint64_t s0 = 0, s1 = 0;
+            const uint64_t mul = pair_of(to_log2, to_log2), sub = pair_of(-base, -base);
 #pragma unroll
-            for (int j = 0; j < PG / 4; ++j) {  // P as bf16 pairs, into the front half of v
-                float p[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) p[i] = ex2(fmaf(__uint_as_float(v[4 * j + i]), to_log2, -base));
-                s[0] += p[0] + p[1];
-                s[1] += p[2] + p[3];
+            for (int j = 0; j < PG / 4; ++j) {  // P as 16-bit pairs, into the front half of v
+                const float2 a0 = floats_of(fma2(pair_of(v[4 * j], v[4 * j + 1]), mul, sub));
+                const float2 a1 = floats_of(fma2(pair_of(v[4 * j + 2], v[4 * j + 3]), mul, sub));
+                uint64_t p0 = pair_of(ex2(a0.x), ex2(a0.y)), p1 = pair_of(ex2(a1.x), ex2(a1.y));
+                s0 = add2(s0, p0);
+                s1 = add2(s1, p1);
                 if (F8) {  // the value product is over the codes: their scales go into P
                     const float4 sc = *reinterpret_cast<const float4 *>(&scales[1][4 * j]);
-                    p[0] *= sc.x;
-                    p[1] *= sc.y;
-                    p[2] *= sc.z;
-                    p[3] *= sc.w;
+                    p0 = mul2(p0, pair_of(sc.x, sc.y));
+                    p1 = mul2(p1, pair_of(sc.z, sc.w));
                 }
-                v[2 * j] = F8 ? pack_f16x2(p[0], p[1]) : pack_bf16x2(p[0], p[1]);
-                v[2 * j + 1] = F8 ? pack_f16x2(p[2], p[3]) : pack_bf16x2(p[2], p[3]);
+                const float2 f0 = floats_of(p0), f1 = floats_of(p1);
+                v[2 * j] = F8 ? pack_f16x2(f0.x, f0.y) : pack_bf16x2(f0.x, f0.y);
+                v[2 * j + 1] = F8 ? pack_f16x2(f1.x, f1.y) : pack_bf16x2(f1.x, f1.y);
             }
-            l = l * fac + ((s[0] + s[1]) + (s[2] + s[3]));
+            const float2 sum2 = floats_of(add2(s0, s1));
+            l = l * fac + (sum2.x + sum2.y);
             // Every thread waits for every step's MMAs in turn, two steps behind (by then they are done): a wait by
             // parity tells two phases apart, not three.  The next vote hears of a failure.
             if (u >= 2) good = wait(bar(ctrl->pv_done[sb]), ((u >> 1) & 1) ^ 1, abort_flag);
