@@ -118,6 +118,8 @@ class Workspace:
         """A buffer of at least ``size()`` bytes, which depends on ``key`` alone."""
         need = self._sizes.get(key)
         if need is None:
+            if len(self._sizes) > 1024:  # lengths that change every step
+                self._sizes.clear()
             need = self._sizes[key] = max(256, size())
         handle = N._stream(stream)
         buf = self._by_stream.get(handle)
