@@ -380,9 +380,9 @@ mla_status_t mla_tree_append(const mla_dims_t *dims, int T, const void *c_kv, co
                                         (cudaStream_t)stream));
 }
 
-// The sizes of mla_decode_tree that the kernels index with: node rows times heads in int.
+// The sizes of mla_decode_tree that the kernels index with: node rows times heads, and tokens rounded up to a step, in int.
 static bool tree_sizes_ok(const mla_dims_t *dims, int B, int total_nodes, int max_seq_len) {
-    return B >= 0 && B <= (1 << 20) && total_nodes >= 0 && max_seq_len >= 1 &&
+    return B >= 0 && B <= (1 << 20) && total_nodes >= 0 && max_seq_len >= 1 && max_seq_len <= INT_MAX - 1024 &&
            (int64_t)total_nodes * dims->n_h <= INT_MAX - 1024 && dims->n_h <= 65535;
 }
 

@@ -204,7 +204,7 @@ tree_simt_kernel(const __grid_constant__ TreeArgs a, int seg_len, int n_split, T
     const int L = a.seq_lens[b], ctx = L - sp.n;
     const bool bad = ctx < 0 || L > a.max_seq_len || L > a.max_blocks * a.page;
     if (bad && first) record_error(a.err, kErrBadSeqLen);
-    const int j_begin = split * seg_len, j_end = bad ? 0 : min(L, j_begin + seg_len);
+    const int j_begin = split * seg_len, j_end = bad ? 0 : j_begin + min(L - j_begin, seg_len);
     const size_t pr = ((size_t)split * a.T + t) * a.n_h + h;  // this warp's partial row
     const uint32_t *mask = a.mask + (size_t)t * a.mask_words;
 

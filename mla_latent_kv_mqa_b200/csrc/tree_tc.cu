@@ -41,10 +41,10 @@
 //
 // Split along the tokens.  All (tile, step) units of the batch are dealt to the pairs in contiguous
 // equal runs; a tile that lies in several runs leaves partial (O, m, l), at most two a pair, which a
-// second kernel joins.
+// second kernel joins.  Where few tiles are spread over many pairs, a tile's steps are turned (tile_turn).
 //
 // Measured (one B200, warm): 24 sequences of 1024-8190 tokens, 3-24 nodes, 128 heads 431 us = 1080 TFLOP/s;
-// 16 of 6000-8192, 64 nodes 1.8 ms = 1130; 4 of 131072, 4 nodes 538 us = 1090; FP8, 32 of 4097-8192, 2-12 nodes
+// 16 of 6000-8192, 64 nodes 1.8 ms = 1130; 4 of 131072, 4 nodes 481 us = 1210; FP8, 32 of 4097-8192, 2-12 nodes
 // 420 us = 950.  (GPUs that power holds lower: 13% more.)  A step takes ~6600 clocks over bf16, of which the
 // MMAs run 4352.  L2 hands the SMs 5.1 GB a call, 11.5 TB/s where loads alone reach 12.4 (557 KB a step and pair:
 // 128 rows a pair use a byte, and O leaves no tensor memory for more rows), and shared memory is busy ~5500 clocks.
@@ -92,6 +92,7 @@ constexpr int LOAD_K_WARP = 0, LOAD_V_WARP = 1, QK_WARP = 2, PV_WARP = 3, SM_WAR
 constexpr int SM_WARPS = 8, SM_THREADS = 32 * SM_WARPS, CLEAN_THREADS = 128;
 constexpr uint32_t S_COL = 0, O_COL = 256, TMEM_COLS = 512;
 constexpr float RESCALE_LOG2 = 8.0f;
+constexpr int TURN_STEPS = 64;                    // steps of the sequences whose tiles may be turned (launch_tree_tc)
 constexpr int BAR_MAX = 1, BAR_CLEAN = 2;
 
 struct __align__(16) Ctrl {
@@ -107,7 +108,7 @@ struct __align__(16) Ctrl {
     uint64_t o_ok[2], pv_done[2];
     uint32_t tmem_base, abort;
     int w_b, w_tile, w_step, w_n, w_tg;
-    long long w_units;  // of the batch
+    long long w_units, w_end;  // of the batch; where the pair's run ends
     long long scan_u[WARPS];
     int scan_t[WARPS];
     alignas(16) float scale[SM_WARPS][2][PG];  // FP8: each softmax warp's page's scales, as they are and with 0 for infinities and NaN
@@ -144,26 +145,54 @@ __device__ __forceinline__ Seq seq_of(const TreeArgs &a, int t0, int n, int L) {
 
 __device__ __forceinline__ Seq seq_of(const TreeArgs &a, int b) { return seq_of(a, a.cu[b], a.cu[b + 1] - a.cu[b], a.seq_lens[b]); }
 
+// A pair's first unit.  (Batches of fewer than 2^24 units, all but the largest, without a 64-bit division.)
+__device__ __forceinline__ long long unit_start(long long c, long long U, int pairs) {
+    return U < (1 << 24) ? (uint32_t)c * (uint32_t)U / (uint32_t)pairs : c * U / pairs;
+}
+__device__ __forceinline__ int pair_of_unit(long long u, long long U, int pairs) {
+    int c = U < (1 << 24) ? (int)((uint32_t)u * (uint32_t)pairs / (uint32_t)U) : (int)(u * pairs / U);
+    while (c + 1 < pairs && unit_start(c + 1, U, pairs) <= u) ++c;
+    while (c > 0 && unit_start(c, U, pairs) > u) --c;
+    return c;
+}
+
+// Where a tile's steps begin among its sequence's (they go around from there).  Pairs start together and keep pace, so
+// where a tile takes several runs, its first whole run begins at the sequence's first step: all tiles of the sequence
+// then go over the same places of a long cache at the same time, and L2 hands on what one of them fetched.
+// u0: the tile's first unit.
+__device__ __noinline__ int tile_turn(long long u0, int steps, long long U, int pairs) {
+    if ((long long)steps * pairs <= U + pairs) return 0;  // no longer than a run
+    const int c = pair_of_unit(u0, U, pairs);
+    return unit_start(c, U, pairs) == u0 ? 0 : steps - (int)(unit_start(c + 1, U, pairs) - u0);
+}
+
 // Walks a pair's units; every role walks the same ones.
+template <bool TURN>
 struct Walk {
     Seq s;
     int b, tile, step, left, tg;  // tg: the tile's number in the batch
     bool first;  // of its segment (a run of one tile's steps)
     bool head;   // the segment is the pair's first
     int seg0;    // the segment's first step
-    __device__ void init(const TreeArgs &a, const int *w) {
-        b = w[0];
-        tile = w[1];
-        step = seg0 = w[2];
-        left = w[3];
-        tg = w[4];
+    int turn;    // TURN: the place of the tile's first step
+    __device__ void init(const TreeArgs &a, const TreePlan &pl, const Ctrl *c) {
+        b = c->w_b;
+        tile = c->w_tile;
+        step = seg0 = c->w_step;
+        left = c->w_n;
+        tg = c->w_tg;
         first = head = true;
-        if (left > 0) s = seq_of(a, b);
+        if (left > 0) {
+            s = seq_of(a, b);
+            if (TURN) turn = tile_turn(c->w_end - left - step, s.steps, c->w_units, pl.pairs);
+        }
     }
+    // The place of the tile's step k among its sequence's.
+    __device__ __forceinline__ int at(int k) const { return !TURN ? k : k + turn >= s.steps ? k + turn - s.steps : k + turn; }
     __device__ bool done() const { return left <= 0; }
-    __device__ int pages() const { return min(SPG, (s.L + PG - 1) / PG - step * SPG); }  // of this step
+    __device__ int pages() const { return min(SPG, (s.L + PG - 1) / PG - at(step) * SPG); }  // of this step
     __device__ bool last() const { return left == 1 || step == s.steps - 1; }
-    __device__ __forceinline__ void next(const TreeArgs &a) {
+    __device__ __forceinline__ void next(const TreeArgs &a, const TreePlan &pl, const Ctrl *c) {
         first = last();
         if (first) head = false;
         --left;
@@ -178,6 +207,7 @@ struct Walk {
                 if (b < a.B) s = seq_of(a, b);
                 else left = 0;
             }
+            if (TURN && left > 0) turn = tile_turn(c->w_end - left, s.steps, c->w_units, pl.pairs);
         }
         if (first) seg0 = step;
     }
@@ -204,17 +234,6 @@ struct Ring {
         }
     }
 };
-
-// A pair's first unit.  (Batches of fewer than 2^24 units, all but the largest, without a 64-bit division.)
-__device__ __forceinline__ long long unit_start(long long c, long long U, int pairs) {
-    return U < (1 << 24) ? (uint32_t)c * (uint32_t)U / (uint32_t)pairs : c * U / pairs;
-}
-__device__ __forceinline__ int pair_of_unit(long long u, long long U, int pairs) {
-    int c = U < (1 << 24) ? (int)((uint32_t)u * (uint32_t)pairs / (uint32_t)U) : (int)(u * pairs / U);
-    while (c + 1 < pairs && unit_start(c + 1, U, pairs) <= u) ++c;
-    while (c > 0 && unit_start(c, U, pairs) > u) --c;
-    return c;
-}
 
 // The pair's run: every CTA scans the batch's tiles and units (two passes where the batch is larger than
 // the block); pair 0 also leaves the offsets for the join.  One sequence that is no tree refuses all: no
@@ -281,6 +300,7 @@ __device__ __noinline__ void schedule(const TreeArgs &a, const TreePlan &pl, int
             c->w_n = (int)(s1 - s0);
             c->w_tg = t1 - q.tiles + c->w_tile;
             c->w_units = U;
+            c->w_end = s1;
         }
         if (report) {
             if (!refuse && q.steps == 0)  // nobody's: the join writes 0 and -inf
@@ -481,7 +501,7 @@ __device__ __forceinline__ uint32_t sees32(const uint32_t *mask, int words, int 
 
 // tm_k, tm_v: column blocks of the bf16 cache; FP8: tm_k the RoPE keys, tm_v and tm_c a page's codes as boxes of
 // 128 columns, as they are and in the operands' layout (unused in the bf16 kernel).
-template <bool F8>
+template <bool F8, bool TURN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_c,
@@ -545,8 +565,8 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
 
     if ((warp == LOAD_K_WARP || warp == LOAD_V_WARP) && lane == 0) {  // ================= loads =================
         const bool kw = warp == LOAD_K_WARP;
-        Walk it;
-        it.init(a, &ctrl->w_b);
+        Walk<TURN> it;
+        it.init(a, pl, ctrl);
         Ring st{0, 0};
         uint32_t q_ph = 1;
         bool ok = true;
@@ -555,7 +575,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         auto pages = [&]() {
 #pragma unroll
             for (int p = 0; p < SPG; ++p) {
-                const int pg = it.step * SPG + p;
+                const int pg = it.at(it.step) * SPG + p;
                 ids[p] = -1;
                 if (!it.done() && pg * PG < it.s.L) {
                     int blk = a.bt[(size_t)it.b * a.max_blocks + pg];
@@ -588,7 +608,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 }
             }
             const int p0 = rank ? ids[2] : ids[0], p1 = rank ? ids[3] : ids[1];
-            it.next(a);
+            it.next(a, pl, ctrl);
             pages();  // of the next step: the table's latency passes under this one's loads
             for (int cb = 0; ok && cb < KST; ++cb) {
                 if (!(ok = wait(bar(ctrl->k_empty[st.i]), st.ph ^ 1u, abort_flag))) break;
@@ -608,8 +628,8 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             int id[SPG];
 #pragma unroll
             for (int p = 0; p < SPG; ++p) id[p] = ids[p];
-            const int pg0 = it.step * SPG, ctx = it.s.ctx, np = it.pages();
-            it.next(a);
+            const int pg0 = it.at(it.step) * SPG, ctx = it.s.ctx, np = it.pages();
+            it.next(a, pl, ctrl);
             pages();
 #pragma unroll
             for (int p = 0; p < SPG; ++p) {
@@ -650,8 +670,8 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         if (!ok) fail();
     } else if (warp == QK_WARP && lane == 0 && rank == 0) {  // ================= S of both CTAs =================
         constexpr uint32_t idesc = idesc_bf16(TILE, STEP, false, false), idesc_f8 = idesc_e4m3(TILE, STEP);
-        Walk it;
-        it.init(a, &ctrl->w_b);
+        Walk<TURN> it;
+        it.init(a, pl, ctrl);
         Ring st{0, 0};
         uint32_t q_ph = 0;
         constexpr uint32_t HI = sdesc_sw128_hi(1024);
@@ -686,13 +706,13 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             if (!ok) break;
             mma_commit_pair(bar(ctrl->s_full[sb]));
             if (it.last()) mma_commit_pair(bar(ctrl->q_empty));
-            it.next(a);
+            it.next(a, pl, ctrl);
         }
         if (!ok) fail();
     } else if (warp == PV_WARP && lane == 0 && rank == 0) {  // ================= O of both CTAs =================
         constexpr uint32_t idesc = F8 ? idesc_f16(TILE, 256, false, true) : idesc_bf16(TILE, 256, false, true);
-        Walk it;
-        it.init(a, &ctrl->w_b);
+        Walk<TURN> it;
+        it.init(a, pl, ctrl);
         Ring st{0, 0};
         constexpr uint32_t HI = sdesc_sw128_hi(1024);
         const uint32_t p_lo = sdesc_sw128_lo(data_s + P_OFF, 16), v_lo = sdesc_sw128_lo(data_s + V_OFF, CB);
@@ -721,13 +741,13 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             }
             if (!ok) break;
             mma_commit_pair(bar(ctrl->pv_done[u & 1]));
-            it.next(a);
+            it.next(a, pl, ctrl);
         }
         if (!ok) fail();
     } else if (F8 && warp >= CLEAN_WARP0) {  // ================= FP8: Q in two parts, V's codes to fp16 tiles =================
         const int t = threadIdx.x - CLEAN_WARP0 * 32;
-        Walk it;
-        it.init(a, &ctrl->w_b);
+        Walk<TURN> it;
+        it.init(a, pl, ctrl);
         Ring st{0, 0};
         uint32_t q_ph = 0;
         uint32_t raw = 0;
@@ -744,7 +764,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             for (int i = 0, n = 2 * it.pages(); i < n; ++i, ++raw, st.adv(V_STAGES)) {
                 const bool good = wait(bar(ctrl->vraw_full[raw % RAW_STAGES]), (raw / RAW_STAGES) & 1, abort_flag) &&
                                   wait(bar(ctrl->v_empty[st.i]), st.ph ^ 1u, abort_flag);
-                const int j0 = (it.step * SPG + (i >> 1)) * PG;        // the page's first token
+                const int j0 = (it.at(it.step) * SPG + (i >> 1)) * PG;        // the page's first token
                 const int drafted = it.s.ctx - j0, end = it.s.L - j0;  // the first drafted row, and the sequence's end
                 // A thread takes four chunks of 16 codes, columns 16 c of two rows of two blocks, odd rows the blocks the
                 // other way round so that eight lanes read 128 different bytes modulo 128.  Its loads come before its
@@ -773,19 +793,19 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     mbar_arrive(bar(ctrl->vraw_empty[raw % RAW_STAGES]));
                 }
             }
-            it.next(a);
+            it.next(a, pl, ctrl);
         }
         if (!ok && lane == 0) fail();
     } else if (warp >= CLEAN_WARP0) {  // ================= V rows not seen by all =================
         const int t = threadIdx.x - CLEAN_WARP0 * 32;
-        Walk it;
-        it.init(a, &ctrl->w_b);
+        Walk<TURN> it;
+        it.init(a, pl, ctrl);
         Ring st{0, 0};
         uint32_t land_ph = 0;  // a bit per stage: only the stages that are cleaned use their barrier
         bool ok = true;
         while (ok && !it.done()) {
             for (int v = 0; ok && v < 2 * it.pages(); ++v, st.adv(V_STAGES)) {
-                const int j0 = (it.step * SPG + (v >> 1)) * PG;
+                const int j0 = (it.at(it.step) * SPG + (v >> 1)) * PG;
                 if (j0 + PG <= it.s.ctx) continue;
                 const bool good = wait(bar(ctrl->land[st.i]), (land_ph >> st.i) & 1u, abort_flag);
                 land_ph ^= 1u << st.i;
@@ -809,7 +829,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 if (!(ok = !named_red_or(!good, BAR_CLEAN, CLEAN_THREADS))) break;
                 if (t == 0) mbar_arrive_pair(lead(ctrl->v_full[st.i]));
             }
-            it.next(a);
+            it.next(a, pl, ctrl);
         }
         if (!ok && lane == 0) fail();
     } else if (warp >= SM_WARP0 && warp < SM_WARP0 + SM_WARPS) {  // ================= softmax, P, O =================
@@ -818,8 +838,8 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t p_row = data_s + P_OFF + (uint32_t)pg * CB + r * 128;
         const uint32_t stage = data_s + P_OFF + (warp - SM_WARP0) * 2048;  // this warp's share of P, between tiles
-        Walk it;
-        it.init(a, &ctrl->w_b);
+        Walk<TURN> it;
+        it.init(a, pl, ctrl);
         float m = -INFINITY, l = 0.f;
         int before = 0;  // steps so far that had the page pg
         bool ok = true, good = true;
@@ -829,7 +849,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         float(*scales)[PG] = ctrl->scale[warp - SM_WARP0];
         int next_block = -1;  // the page's in the tile's next step
         auto block_of = [&](int step) {
-            const int g = step * SPG + pg;
+            const int g = it.at(step) * SPG + pg;
             return g * PG < it.s.L ? a.bt[(size_t)it.b * a.max_blocks + g] : -1;
         };
         auto load_scales = [&](int blk) {
@@ -901,7 +921,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 load_scales(next_block);
                 next_block = block_of(it.step + 2);
             }
-            const int j0 = it.step * STEP + pg * PG;
+            const int j0 = it.at(it.step) * STEP + pg * PG;
             if (j0 + PG > it.s.ctx) {
                 const uint32_t *mask = a.mask + (size_t)(it.s.t0 + (mine ? row / a.n_h : 0)) * a.mask_words;
 #pragma unroll
@@ -1081,7 +1101,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     }
                 }
             }
-            it.next(a);
+            it.next(a, pl, ctrl);
         }
         if (!(ok && good)) fail();
     }
@@ -1183,7 +1203,7 @@ tree_tc_join_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ 
     }
 }
 
-// Pairs that run at once on the current device (0: it cannot be queried), looked up once.  Both kernels
+// Pairs that run at once on the current device (0: it cannot be queried), looked up once.  All variants
 // have the same launch shape and shared memory.
 int tree_pairs() {
     static int known[64];
@@ -1194,7 +1214,7 @@ int tree_pairs() {
     if (known[dev]) return known[dev];
     int sms = 148, most = 0;
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    for (auto kern : {tree_tc_kernel<false>, tree_tc_kernel<true>}) {
+    for (auto kern : {tree_tc_kernel<false, false>, tree_tc_kernel<true, false>, tree_tc_kernel<false, true>, tree_tc_kernel<true, true>}) {
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM) != cudaSuccess) return 0;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(2 * (sms / 2));
@@ -1276,8 +1296,12 @@ cudaError_t launch_tree_tc(const mla_dims_t &d, const TreeArgs &a, void *ws, cud
     cfg.stream = st;
     cfg.attrs = &pdl;
     cfg.numAttrs = 1;
-    cudaError_t e = f8 ? cudaLaunchKernelEx(&cfg, tree_tc_kernel<true>, tm_q, tm_k, tm_v, tm_c, a, pl)
-                       : cudaLaunchKernelEx(&cfg, tree_tc_kernel<false>, tm_q, tm_k, tm_v, tm_c, a, pl);
+    // Few tiles of long sequences, each over several pairs (4 x 131072 tokens, four tiles each): turned 481 us, as they
+    // come 540.  Many tiles have nothing to share, and the turns' instructions cost them 3% (24 ragged sequences 440 -> 455 us).
+    const bool turn = 2 * tree_tiles(a.B, (int64_t)q_rows) <= pairs && a.max_seq_len >= TURN_STEPS * STEP;
+    auto kern = f8 ? turn ? tree_tc_kernel<true, true> : tree_tc_kernel<true, false>
+                   : turn ? tree_tc_kernel<false, true> : tree_tc_kernel<false, false>;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, kern, tm_q, tm_k, tm_v, tm_c, a, pl);
     if (e != cudaSuccess) return e;
     cfg.gridDim = dim3((unsigned)tree_tiles(a.B, (int64_t)q_rows), TILE / JOIN_ROWS);
     cfg.blockDim = dim3(JOIN_THREADS);

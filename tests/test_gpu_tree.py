@@ -540,7 +540,8 @@ def test_a_query_that_is_not_finite_stays_in_its_row(kv, flags, ctx, column, val
 
 @pytest.mark.parametrize("kv", ["bf16", "fp8"])
 @pytest.mark.parametrize("ctx,n,heads", [([3000, 2100, 700, 2900], [40, 17, 33, 64], 128), ([4000] * 6, [5, 9, 2, 7, 1, 3], 128),
-                                         ([20000, 5], [3, 200], 16)])
+                                         ([20000, 5], [3, 200], 16), ([33000, 17001, 16500], [4, 1, 6], 128),
+                                           ([65535], [2], 64)])
 def test_many_units_a_pair(kv, ctx, n, heads):
     b = Batch(ctx, n, heads=heads, kv=kv, seed=51)
     first = b.decode("bf16")

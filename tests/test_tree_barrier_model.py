@@ -186,7 +186,8 @@ def batch(seed, n=14):
         if first:
             left = rng.randint(1, 4)
         left -= 1
-        units.append((first, left == 0, rng.randint(1, 4) if left == 0 else 4, rng.random() < 0.3))
+        # a tile's steps go around, so the one with fewer pages may be any of them
+        units.append((first, left == 0, rng.randint(1, 4) if rng.random() < 0.3 else 4, rng.random() < 0.3))
     units[-1] = (units[-1][0], True) + units[-1][2:]
     return units
 

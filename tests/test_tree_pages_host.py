@@ -55,6 +55,7 @@ def test_tree_calls_refuse_bad_arguments(N):
     assert N.mla_decode_tree_workspace_size(few, 1, 1, 1 << 18) > 1 << 14
     assert 0 < N.mla_decode_tree_workspace_size(s, 2, 6, 256)
     assert N.mla_decode_tree_workspace_size(s, 2, -1, 256) == 0 and N.mla_decode_tree_workspace_size(s, 2, 6, 0) == 0
+    assert N.mla_decode_tree_workspace_size(s, 2, 6, 2 ** 31 - 1) == 0 and dec(blocks=(1 << 25) - 1, max_len=2 ** 31 - 64) == bad
 
     pools = N.make_pools([(16, None, None)] * 2)
 

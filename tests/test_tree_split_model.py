@@ -114,3 +114,21 @@ def test_mask_words():
         j = 32 * int(rng.integers(0, 12))
         want = sum(1 << i for i in range(32) if j + i < ctx + n and (j + i < ctx or (bits >> (j + i - ctx)) & 1))
         assert sees32(bits, j, ctx, ctx + n) == want
+
+
+@pytest.mark.parametrize("n,lens,heads", [([4] * 4, [131072] * 4, 128), ([4, 1, 6], [33004, 17002, 16506], 128), ([3], [20003], 16), ([9], [70000], 128)])
+def test_turned_tiles(n, lens, heads):
+    """A tile's steps go around from its turn; the first whole run of every long tile starts at the sequence's first step."""
+    pairs = 74
+    tiles, steps = shapes(n, lens, heads)
+    U = sum(t * s for t, s in zip(tiles, steps))
+    u0 = 0
+    for t, s in zip(tiles, steps):
+        for _ in range(t):
+            c, turn = pair_of_unit(u0, U, pairs), 0
+            if s * pairs > U + pairs and unit_start(c, U, pairs) != u0:
+                turn = s - (unit_start(c + 1, U, pairs) - u0)
+                assert 0 < turn < s
+                assert (unit_start(c + 1, U, pairs) - u0 + turn) % s == 0
+            assert sorted(k + turn if k + turn < s else k + turn - s for k in range(s)) == list(range(s))
+            u0 += s
