@@ -530,7 +530,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             mbar_init(bar(ctrl->vraw_empty[i]), CLEAN_THREADS / 32);
         }
         mbar_init(bar(ctrl->q_land), 1);
-        mbar_init(bar(ctrl->q_full), 2);
+        mbar_init(bar(ctrl->q_full), F8 ? 2 * CLEAN_THREADS / 32 : 2);
         mbar_init(bar(ctrl->q_empty), 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar(ctrl->s_full[i]), 1);
@@ -753,13 +753,14 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         uint32_t raw = 0;
         bool ok = true;
         while (ok && !it.done()) {
-            if (it.first) {
+            if (it.first) {  // each warp the rows that it splits, and for itself: a warp that gave up waits for no other
                 const bool good = wait(bar(ctrl->q_land), q_ph, abort_flag);
                 for (int r0 = 0; r0 < HALF; r0 += CLEAN_THREADS / 8) split_query(data_s + Q_OFF, r0 + (t >> 3), t & 7, ctrl->q_unit[q_ph]);
                 q_ph ^= 1u;
                 fence_proxy_async_smem();
-                if (!(ok = !named_red_or(!good, BAR_CLEAN, CLEAN_THREADS))) break;
-                if (t == 0) mbar_arrive_pair(lead(ctrl->q_full));
+                if (!(ok = __all_sync(0xffffffffu, good))) break;
+                __syncwarp();  // a vote orders no memory
+                if (lane == 0) mbar_arrive_pair(lead(ctrl->q_full));
             }
             for (int i = 0, n = 2 * it.pages(); i < n; ++i, ++raw, st.adv(V_STAGES)) {
                 const bool good = wait(bar(ctrl->vraw_full[raw % RAW_STAGES]), (raw / RAW_STAGES) & 1, abort_flag) &&
@@ -788,6 +789,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 }
                 fence_proxy_async_smem();
                 if (!(ok = __all_sync(0xffffffffu, good))) break;
+                __syncwarp();
                 if (lane == 0) {  // each warp for itself: a barrier among the four cost 4% of the whole
                     mbar_arrive_pair(lead(ctrl->v_full[st.i]));
                     mbar_arrive(bar(ctrl->vraw_empty[raw % RAW_STAGES]));
