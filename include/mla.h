@@ -98,7 +98,7 @@ typedef enum {
  * The value product P . V keeps bf16 V (dequantised on chip).  QuantMLA review, Motivation
  * & Problem Statement (an FP8 content cache next to a high-precision RoPE-key cache). */
 #define MLA_FLAG_FP8_MMA 8u
-#define MLA_FLAG_TEST_GIVE_UP 4u /* test of the failure path of the tensor-core decode: in
+#define MLA_FLAG_TEST_GIVE_UP 4u /* test of the failure path of the tensor-core decodes: in
                                     every cluster with two or more pages, after the copies of
                                     the first page have started, one bounded wait (20 us) on a
                                     barrier that nothing completes gives up.  The cluster then
@@ -427,7 +427,8 @@ mla_status_t mla_tree_append(const mla_dims_t *dims, int T, const void *c_kv, co
  * cache P times the token's scale to fp16 instead (11 bits; fewer for a token below 2^-16 of the row's
  * largest, to 2^-27 of it), and a query's content elements below 2^-9 of their row's largest are taken to
  * 2^-17 of it.  A query row with infinities or NaN gets NaN.
- * MLA_FLAG_FP8_MMA and MLA_FLAG_TEST_GIVE_UP do not concern this call.
+ * MLA_FLAG_FP8_MMA does not concern this call.  MLA_FLAG_TEST_GIVE_UP does what it does in the tensor-core
+ * decode, in every pair of SMs with two or more steps of 256 tokens.
  * Deterministic: the result depends only on the logical cache content. */
 size_t mla_decode_tree_workspace_size(const mla_dims_t *dims, int B, int total_nodes, int max_seq_len);
 mla_status_t mla_decode_tree(const mla_dims_t *dims, int B, const int32_t *cu_nodes, int total_nodes,

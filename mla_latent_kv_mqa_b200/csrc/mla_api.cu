@@ -442,6 +442,7 @@ mla_status_t mla_decode_tree(const mla_dims_t *dims, int B, const int32_t *cu_no
     a.out_bf16 = out_dtype == MLA_DTYPE_BF16;
     a.lse = lse;
     a.err = device_error_word();
+    a.test_give_up = (dims->flags & MLA_FLAG_TEST_GIVE_UP) != 0;
     if (tree_tc_supported(*dims)) {
         // TMA reads of the cache and q_abs, vector stores of o_lat; page rows as int TMA coordinates
         if (!aligned(q_abs, 16) || !aligned(kv_pool, 16) || (kr_pool && !aligned(kr_pool, 16)) ||

@@ -24,6 +24,7 @@ struct TreeArgs {
     int out_bf16;
     float *lse;
     unsigned *err;
+    int test_give_up;  // MLA_FLAG_TEST_GIVE_UP
 };
 
 // Partial results of one token segment: o [segment][T * n_h][d_c], m and l [segment][T * n_h].

@@ -50,7 +50,8 @@
 // 128 rows a pair use a byte, and O leaves no tensor memory for more rows), and shared memory is busy ~5500 clocks.
 //
 // Every wait is bounded (2 s).  On give-up both CTAs' abort flags are set, MLA_ERR_DEVICE_TIMEOUT is
-// recorded, and both CTAs stay until copies and MMAs in flight have had time to land.
+// recorded, and both CTAs stay until copies and MMAs in flight have had time to land.  What the join acts on
+// (schedule) is written before the first wait; of a pair that gave up it joins whatever the partials hold.
 #include <cuda_fp16.h>
 #include <cudaTypedefs.h>
 #include <float.h>
@@ -106,8 +107,9 @@ struct __align__(16) Ctrl {
     // By step parity: O read or rescaled as the step needs / the step's MMAs done.  A CTA may be a step ahead of
     // its peer, so one barrier would take its arrivals for two steps as both CTAs' for one.
     uint64_t o_ok[2], pv_done[2];
+    uint64_t never_done;  // nothing completes it (MLA_FLAG_TEST_GIVE_UP)
     uint32_t tmem_base, abort;
-    int w_b, w_tile, w_step, w_n, w_tg;
+    int w_b, w_tile, w_step, w_n;
     long long w_units, w_end;  // of the batch; where the pair's run ends
     long long scan_u[WARPS];
     int scan_t[WARPS];
@@ -170,7 +172,7 @@ __device__ __noinline__ int tile_turn(long long u0, int steps, long long U, int 
 template <bool TURN>
 struct Walk {
     Seq s;
-    int b, tile, step, left, tg;  // tg: the tile's number in the batch
+    int b, tile, step, left;
     bool first;  // of its segment (a run of one tile's steps)
     bool head;   // the segment is the pair's first
     int seg0;    // the segment's first step
@@ -180,7 +182,6 @@ struct Walk {
         tile = c->w_tile;
         step = seg0 = c->w_step;
         left = c->w_n;
-        tg = c->w_tg;
         first = head = true;
         if (left > 0) {
             s = seq_of(a, b);
@@ -198,12 +199,9 @@ struct Walk {
         --left;
         if (++step == s.steps) {
             step = 0;
-            ++tg;
             if (++tile == s.tiles) {
                 tile = 0;
-                const int2 to = next_seq(a, b);
-                b = to.x;
-                tg += to.y;
+                b = next_seq(a, b);
                 if (b < a.B) s = seq_of(a, b);
                 else left = 0;
             }
@@ -211,16 +209,14 @@ struct Walk {
         }
         if (first) seg0 = step;
     }
-    // The next sequence with units (B: none) and the tiles in between.  Out of line: the roles call it once a
-    // sequence and share the instruction cache.
-    static __device__ __noinline__ int2 next_seq(const TreeArgs &a, int b) {
-        int skipped = 0;
+    // The next sequence with units (B: none).  Out of line: the roles call it once a sequence and share the
+    // instruction cache.
+    static __device__ __noinline__ int next_seq(const TreeArgs &a, int b) {
         while (++b < a.B) {
             const Seq n = seq_of(a, b);
             if (n.steps > 0 && n.tiles > 0) break;
-            skipped += n.tiles;
         }
-        return make_int2(b, skipped);
+        return b;
     }
 };
 
@@ -298,9 +294,17 @@ __device__ __noinline__ void schedule(const TreeArgs &a, const TreePlan &pl, int
             c->w_tile = (int)((s0 - u0) / q.steps);
             c->w_step = (int)((s0 - u0) % q.steps);
             c->w_n = (int)(s1 - s0);
-            c->w_tg = t1 - q.tiles + c->w_tile;
             c->w_units = U;
             c->w_end = s1;
+        }
+        // The records of the tiles that begin in the run: every tile has one before any wait, so that the join finds
+        // none of an earlier call's after a give-up.
+        if (!refuse && rank == 0 && mine > 0 && u0 < s1 && s0 < u1) {
+            for (long long k = s0 > u0 ? (s0 - u0 + q.steps - 1) / q.steps : 0; k < q.tiles && u0 + k * q.steps < s1; ++k) {
+                const long long v = u0 + k * q.steps, last = v + q.steps - 1;
+                const int n = last < s1 ? 1 : pair_of_unit(last, U, pl.pairs) - pair + 1;
+                pl.tile[t1 - q.tiles + k] = make_int4(q.t0 * a.n_h + (int)k * TILE, q.n * a.n_h - (int)k * TILE, pair, v == s0 ? n : -n);
+            }
         }
         if (report) {
             if (!refuse && q.steps == 0)  // nobody's: the join writes 0 and -inf
@@ -532,6 +536,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         mbar_init(bar(ctrl->q_land), 1);
         mbar_init(bar(ctrl->q_full), F8 ? 2 * CLEAN_THREADS / 32 : 2);
         mbar_init(bar(ctrl->q_empty), 1);
+        mbar_init(bar(ctrl->never_done), 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar(ctrl->s_full[i]), 1);
             mbar_init(bar(ctrl->s_free[i]), 2 * SM_WARPS);
@@ -594,7 +599,11 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             if (F8) prefetch_tensormap(&tm_c);
             pages();
         }
+        bool begun = false;
         while (ok && kw && !it.done()) {  // Q per segment; K: the CTA's two pages, a column block a stage
+            // the failure path's test: the first step's copies are under way, a short wait runs out
+            if (a.test_give_up && begun && !(ok = wait(bar(ctrl->never_done), 0u, abort_flag, 20000ull))) break;
+            begun = true;
             if (it.first) {
                 if (!(ok = wait(bar(ctrl->q_empty), q_ph, abort_flag))) break;
                 q_ph ^= 1u;
@@ -1032,16 +1041,6 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 const int slot = 2 * pair + (it.head ? 0 : 1);
                 const float inv = total == 0.f ? 0.f : 1.f / total;
                 const int row0 = row - lane;  // this warp's first row of the sequence
-                if (it.seg0 == 0 && rank == 0 && warp == SM_WARP0 && lane == 0) {  // the tile's first segment tells the join
-                    const int rest = it.s.steps - 1 - it.step;  // steps behind this segment: the pairs that hold them
-                    int n = 1;
-                    if (rest > 0) {
-                        const long long U = ctrl->w_units, u1 = unit_start(pair + 1, U, pl.pairs) + rest - 1;
-                        n = pair_of_unit(u1, U, pl.pairs) - pair + 1;
-                    }
-                    pl.tile[it.tg] = make_int4(it.s.t0 * a.n_h + it.tile * TILE, it.s.n * a.n_h - it.tile * TILE, pair,
-                                               it.head ? n : -n);
-                }
                 if (pg == 0) {
                     if (!whole) {
                         pl.m[slot * TILE + (int)rank * HALF + r] = total == total ? m : total;  // NaN scores move no maximum

@@ -6,6 +6,8 @@ import random
 
 import pytest
 
+from tests.test_tree_split_model import CASES, pair_of_unit, shapes, unit_start
+
 WARPS, RAW = 4, 2
 
 
@@ -78,3 +80,39 @@ def test_every_warp_leaves_after_a_give_up():
 
 def test_a_vote_among_them_would_wait_without_bound():
     assert any(not run(seed, votes=True) for seed in range(400))
+
+
+# ---- the join's records ------------------------------------------------------------------------------
+
+def records(tiles, steps, pair, pairs):
+    """(tile of the batch, first pair, its pairs, head) that a pair writes before it waits for anything."""
+    U = sum(t * s for t, s in zip(tiles, steps))
+    s0, s1 = unit_start(pair, U, pairs), unit_start(pair + 1, U, pairs)
+    out, u0, t0 = [], 0, 0
+    for t, s in zip(tiles, steps):
+        u1 = u0 + t * s
+        if u1 > u0 and u0 < s1 and s0 < u1:
+            k = (s0 - u0 + s - 1) // s if s0 > u0 else 0
+            while k < t and u0 + k * s < s1:
+                v = u0 + k * s
+                last = v + s - 1
+                out.append((t0 + k, pair, 1 if last < s1 else pair_of_unit(last, U, pairs) - pair + 1, v == s0))
+                k += 1
+        u0, t0 = u1, t0 + t
+    return out
+
+
+@pytest.mark.parametrize("pairs", [1, 2, 74])
+@pytest.mark.parametrize("n,lens,heads", CASES + [([9], [70000], 128), ([4] * 4, [131072] * 4, 128)])
+def test_every_tile_has_one_record(n, lens, heads, pairs):
+    tiles, steps = shapes(n, lens, heads)
+    U = sum(t * s for t, s in zip(tiles, steps))
+    got = [r for c in range(pairs) for r in records(tiles, steps, c, pairs)]
+    want, u0, t0 = [], 0, 0
+    for t, s in zip(tiles, steps):
+        for k in range(t if s else 0):
+            c0, c1 = pair_of_unit(u0, U, pairs), pair_of_unit(u0 + s - 1, U, pairs)
+            want.append((t0 + k, c0, c1 - c0 + 1, unit_start(c0, U, pairs) == u0))
+            u0 += s
+        t0 += t
+    assert got == want
