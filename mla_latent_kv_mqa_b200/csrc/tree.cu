@@ -50,7 +50,7 @@ tree_prepare_kernel(int B, const int32_t *cu, int T, const int32_t *parent,
         }
         return;
     }
-    const int ctx = seq_lens[b] - sp.n;
+    const int ctx = committed(seq_lens[b], sp.n);
     if (ctx < 0 && threadIdx.x == 0) record_error(err, kErrBadSeqLen);
     bool bad = false;
     for (int k = threadIdx.x; k < sp.n; k += kPrepThreads) {
@@ -125,7 +125,7 @@ cache_keep_kernel(const __grid_constant__ KeepArgs a, const __grid_constant__ Po
     TreeSpan sp;
     const bool tree_ok = tree_span(a.cu, b, a.B, a.T, INT_MAX, &sp);
     const int L = a.seq_lens[b], nk = a.num_keep[b];
-    const int ctx = L - sp.n;
+    const int ctx = committed(L, sp.n);
     bool bad = !tree_ok || nk < 0 || nk > a.max_keep || nk > sp.n;
     const bool bad_len = tree_ok && (ctx < 0 || L > a.max_blocks * a.page);
     bool bad_block = false;
@@ -201,7 +201,7 @@ tree_simt_kernel(const __grid_constant__ TreeArgs a, int seg_len, int n_split, T
         if (b == kTreeBad && first) record_error(a.err, kErrBadTree);
         return;  // a row behind the last sequence, or of no sequence: left as it is
     }
-    const int L = a.seq_lens[b], ctx = L - sp.n;
+    const int L = a.seq_lens[b], ctx = committed(L, sp.n);
     const bool bad = ctx < 0 || L > a.max_seq_len || L > a.max_blocks * a.page;
     if (bad && first) record_error(a.err, kErrBadSeqLen);
     const int j_begin = split * seg_len, j_end = bad ? 0 : j_begin + min(L - j_begin, seg_len);

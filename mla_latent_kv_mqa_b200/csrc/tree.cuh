@@ -45,6 +45,10 @@ __device__ __forceinline__ bool tree_span(const int32_t *cu, int b, int B, int T
     return ok;
 }
 
+// Committed tokens of a sequence of L tokens and n nodes, -1 where L is less than n (any int: no difference that
+// passes the type's range comes out as a length).
+__device__ __forceinline__ int committed(int L, int n) { return L < n ? -1 : L - n; }
+
 // The sequence that drafted row t: kTreeNone behind the last sequence, kTreeBad where cu is not a
 // non-decreasing list of rows or the sequence has more than max_nodes.
 constexpr int kTreeNone = -1, kTreeBad = -2;

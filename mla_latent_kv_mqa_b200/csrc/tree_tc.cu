@@ -139,7 +139,7 @@ __device__ __forceinline__ Seq seq_of(const TreeArgs &a, int t0, int n, int L) {
     s.t0 = t0;
     s.n = n;
     s.L = L;
-    s.ctx = s.L - s.n;
+    s.ctx = committed(L, n);
     s.tiles = (int)(((long long)s.n * a.n_h + TILE - 1) / TILE);
     s.steps = s.ctx < 0 || s.L > a.max_seq_len || s.L > a.max_blocks * PG ? 0 : (s.L + STEP - 1) / STEP;
     return s;
