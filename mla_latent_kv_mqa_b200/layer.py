@@ -65,8 +65,8 @@ class PagedLatentCache:
         elif kr_pool is not None or kv_scale is not None:
             raise ValueError("kr_pool and kv_scale belong to an FP8 cache")
         for x, shape, dtype in want:
-            if x is None or tuple(x.shape) != shape or x.dtype != dtype or not x.is_contiguous():
-                raise ValueError(f"cache buffer must be contiguous {dtype} {shape}")
+            if x is None or tuple(x.shape) != shape or x.dtype != dtype or not x.is_contiguous() or x.device != kv_pool.device:
+                raise ValueError(f"cache buffer must be contiguous {dtype} {shape}, all on one device")
         self = cls.__new__(cls)
         self.dims, self.num_blocks = dims, int(n)
         self.kv_pool, self.kr_pool, self.kv_scale = kv_pool, kr_pool, kv_scale
@@ -95,6 +95,12 @@ class PagedLatentCache:
 _INT32 = torch.int32
 _on_device = getattr(torch._C, "_cuda_getDevice", None)
 _MISREAD = ("tensors are contiguous and on the current CUDA device; lengths, tables and indices are int32")
+
+
+def fits(dims: N.mla_dims_t, of: N.mla_dims_t) -> bool:
+    """A cache of ``of`` has the rows that a layer of ``dims`` reads and writes."""
+    return of is dims or (of.kv_dtype == dims.kv_dtype and of.d_c == dims.d_c and of.d_r == dims.d_r and
+                          of.page_size == dims.page_size)
 
 
 def same_caches(caches, num_blocks) -> N.mla_dims_t:
@@ -238,13 +244,17 @@ class MLADecodeLayer:
         """The drafted nodes' rows into their slots (trees.prepare first)."""
         B, max_blocks = block_table.shape
         T, here = trees.total_nodes, c_kv.get_device()
-        if c_kv.size(0) != T or k_r.size(0) != T or B != trees.B:
-            raise ValueError("tree_append: c_kv and k_r have a row per node, block_table one per tree")
+        d = self.dims
+        act = TORCH_ACT[d.act_dtype]
+        if c_kv.shape != (T, d.d_c) or k_r.shape != (T, d.d_r) or c_kv.dtype is not act or k_r.dtype is not act or B != trees.B:
+            raise ValueError("tree_append: c_kv [nodes, d_c] and k_r [nodes, d_r] of the layer's type, block_table a row per tree")
+        if not fits(d, cache.dims):
+            raise ValueError("tree_append: the cache's rows are not the layer's")
         if (here < 0 or here != _on_device() or k_r.get_device() != here or block_table.get_device() != here or
                 trees.slot.get_device() != here or cache.kv_pool.get_device() != here or block_table.dtype is not _INT32 or
                 not (c_kv.is_contiguous() and k_r.is_contiguous() and block_table.is_contiguous())):
             raise ValueError(_MISREAD)
-        N.mla_tree_append(self.dims, T, c_kv, k_r, trees.seq_idx, trees.slot, trees.pos, block_table, B,
+        N.mla_tree_append(d, T, c_kv, k_r, trees.seq_idx, trees.slot, trees.pos, block_table, B,
                           max_blocks, cache.num_blocks, cache.kv_pool, cache.kr_pool, cache.kv_scale, stream)
 
     def decode_tree(self, cache: PagedLatentCache, q_abs, block_table, seq_lens, trees, max_seq_len,
@@ -256,8 +266,11 @@ class MLADecodeLayer:
         B, max_blocks = block_table.shape
         T = trees.total_nodes
         dt = DTYPE[out_dtype]
-        if q_abs.size(0) != T or B != trees.B or seq_lens.numel() != B:
-            raise ValueError("decode_tree: q_abs has a row per node, block_table and seq_lens one per tree")
+        if (q_abs.shape != (T, d.n_h, d.d_c + d.d_r) or q_abs.dtype is not TORCH_ACT[d.act_dtype] or B != trees.B or
+                seq_lens.numel() != B):
+            raise ValueError("decode_tree: q_abs is [nodes, n_h, d_c + d_r] of the layer's type, block_table and seq_lens have a row per tree")
+        if not fits(d, cache.dims):
+            raise ValueError("decode_tree: the cache's rows are not the layer's")
         here = q_abs.get_device()
         if (here < 0 or here != _on_device() or block_table.get_device() != here or seq_lens.get_device() != here or
                 trees.cu_nodes.get_device() != here or cache.kv_pool.get_device() != here or
@@ -266,15 +279,18 @@ class MLADecodeLayer:
             raise ValueError(_MISREAD)
         if o_lat is None:
             o_lat = q_abs.new_empty((T, d.n_h, d.d_c), dtype=TORCH_ACT[dt])
-        elif o_lat.dtype != TORCH_ACT[dt] or tuple(o_lat.shape) != (T, d.n_h, d.d_c) or not o_lat.is_contiguous():
-            raise ValueError("decode_tree: o_lat is contiguous [nodes, n_h, d_c] of out_dtype")
+        elif (o_lat.dtype != TORCH_ACT[dt] or o_lat.shape != (T, d.n_h, d.d_c) or not o_lat.is_contiguous() or
+              o_lat.get_device() != here):
+            raise ValueError("decode_tree: o_lat is contiguous [nodes, n_h, d_c] of out_dtype, where q_abs is")
         if lse is None:
             lse = q_abs.new_empty((T, d.n_h), dtype=torch.float32)
-        elif lse.dtype != torch.float32 or tuple(lse.shape) != (T, d.n_h) or not lse.is_contiguous():
-            raise ValueError("decode_tree: lse is contiguous [nodes, n_h] fp32")
+        elif lse.dtype != torch.float32 or lse.shape != (T, d.n_h) or not lse.is_contiguous() or lse.get_device() != here:
+            raise ValueError("decode_tree: lse is contiguous [nodes, n_h] fp32, where q_abs is")
         if workspace is None:
             workspace = self._tree_ws.get((B, T, max_seq_len), stream,
                                           lambda: N.mla_decode_tree_workspace_size(d, B, T, max_seq_len))
+        elif workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.get_device() != here:
+            raise ValueError("decode_tree: workspace is contiguous uint8, where q_abs is")
         N.mla_decode_tree(d, B, trees.cu_nodes, T, trees.max_nodes, q_abs, cache.kv_pool, cache.kr_pool,
                           cache.kv_scale, block_table, max_blocks, cache.num_blocks, seq_lens, max_seq_len,
                           trees.mask, trees.mask_words, workspace, workspace.numel(), o_lat, dt, lse, stream)

@@ -132,5 +132,7 @@ class PagedSequences:
         else:
             pairs, number = moves
             self._look_over(pairs, number)
+            if pairs.dim() != 2 or pairs.shape[1] != 2 or (number is not None and number.numel() < 1):
+                raise ValueError("copy_pages: moves are pairs [n, 2] and their number [1], or None for all")
             most = pairs.shape[0]
         N.mla_cache_copy_pages(dims, pools, self.num_blocks, pairs, number, most, stream)

@@ -34,17 +34,46 @@ class DraftTrees:
         for x in (cu_nodes, parent):
             if x.dtype != torch.int32 or x.dim() != 1 or not x.is_contiguous():
                 raise ValueError("cu_nodes and parent must be contiguous int32 vectors")
+        if parent.device != cu_nodes.device or (mask is not None and mask.device != cu_nodes.device):
+            raise ValueError("cu_nodes, parent and mask must be on one device")
+        if mask is not None and mask.dim() != 2:
+            raise ValueError("mask must be [total_nodes, words]")
         if cu_nodes.numel() < 1:
             raise ValueError("cu_nodes must have an entry per sequence and one more")
-        self.cu_nodes, self.parent, self.max_nodes = cu_nodes, parent, int(max_nodes)
+        self._cu_nodes, self._parent, self.max_nodes = cu_nodes, parent, int(max_nodes)
         self.B, self.total_nodes = cu_nodes.numel() - 1, parent.numel()
         self.mask_words = (self.max_nodes + 31) // 32 if mask is None else mask.shape[1]
         if mask is not None and (mask.shape[0] != self.total_nodes or 32 * self.mask_words < self.max_nodes or
                                  mask.dtype != torch.int32 or not mask.is_contiguous()):
             raise ValueError("mask must be contiguous int32 [total_nodes, >= ceil(max_nodes / 32)]")
         dev = cu_nodes.device
-        self.mask = torch.empty((self.total_nodes, self.mask_words), dtype=torch.int32, device=dev) if mask is None else mask
-        self.pos, self.slot, self.seq_idx = (torch.empty(self.total_nodes, dtype=torch.int32, device=dev) for _ in range(3))
+        self._mask = torch.empty((self.total_nodes, self.mask_words), dtype=torch.int32, device=dev) if mask is None else mask
+        self._pos, self._slot, self._seq_idx = (torch.empty(self.total_nodes, dtype=torch.int32, device=dev) for _ in range(3))
+
+    # Looked over once, above: written in place (copy_), not replaced.
+    @property
+    def cu_nodes(self) -> torch.Tensor:
+        return self._cu_nodes
+
+    @property
+    def parent(self) -> torch.Tensor:
+        return self._parent
+
+    @property
+    def mask(self) -> torch.Tensor:
+        return self._mask
+
+    @property
+    def pos(self) -> torch.Tensor:
+        return self._pos
+
+    @property
+    def slot(self) -> torch.Tensor:
+        return self._slot
+
+    @property
+    def seq_idx(self) -> torch.Tensor:
+        return self._seq_idx
 
     def prepare(self, seq_lens, stream=None):
         if seq_lens.numel() != self.B:
@@ -60,11 +89,13 @@ class DraftTrees:
         """The rows of the accepted nodes ``keep`` [B, max_keep] (each row's first num_keep[b],
         ascending) to behind the committed tokens, in every cache; returns the new lengths."""
         B, max_blocks = block_table.shape
-        if B != self.B or seq_lens.numel() != B or keep.size(0) != B or num_keep.numel() != B:
-            raise ValueError("keep: block_table, seq_lens, keep and num_keep have a row per tree")
+        if B != self.B or seq_lens.numel() != B or keep.dim() != 2 or keep.size(0) != B or num_keep.numel() != B:
+            raise ValueError("keep: block_table, seq_lens, keep [trees, max_keep] and num_keep have a row per tree")
+        if not caches:
+            raise ValueError("keep: no caches")
         here = seq_lens.get_device()
         if (here < 0 or here != _on_device() or self.cu_nodes.get_device() != here or block_table.get_device() != here or
-                keep.get_device() != here or num_keep.get_device() != here or caches[0].kv_pool.get_device() != here or
+                keep.get_device() != here or num_keep.get_device() != here or any(c.kv_pool.get_device() != here for c in caches) or
                 block_table.dtype is not _INT32 or seq_lens.dtype is not _INT32 or keep.dtype is not _INT32 or
                 num_keep.dtype is not _INT32 or
                 not (block_table.is_contiguous() and seq_lens.is_contiguous() and keep.is_contiguous() and num_keep.is_contiguous())):

@@ -51,3 +51,26 @@ def test_prepare_and_keep_refuse_such_a_length(L):
     assert N.mla_get_last_device_error() == N.MLA_ERR_BAD_SEQ_LEN
     assert new.tolist() == [102, L, 91]
     assert torch.equal(b.cache.kv_pool.view(torch.int16), before.view(torch.int16))
+
+
+# ---- refusals that need a device ---------------------------------------------------------------------
+
+def test_host_tensors_among_device_ones_are_refused():
+    from mla_latent_kv_mqa_b200 import layer as L, pages as P
+    b = Batch([100, 30], [6, 4], heads=4)
+    with pytest.raises(ValueError):
+        b.decode(o_lat=torch.zeros(10, 4, 512))
+    with pytest.raises(ValueError):
+        b.decode(lse=torch.zeros(10, 4))
+    for ws in (torch.zeros(1 << 26, dtype=torch.uint8), torch.zeros(1 << 24, device="cuda")):
+        with pytest.raises(ValueError):
+            b.decode(workspace=ws)
+    keep, num = dev([[0], [0]]), dev([1, 1])
+    other = L.PagedLatentCache(b.dims, b.cache.num_blocks, device="cpu")
+    with pytest.raises(ValueError):
+        b.trees.keep([b.cache, other], b.table, b.lens, keep, num)
+    seqs = P.PagedSequences(64, 2, 4, b.cache.num_blocks)
+    for moves in ((dev([0, 1]), dev([1])), (dev([[0, 1, 2]]), dev([1])), (dev([[0, 1]]), dev([])), (torch.zeros(1, 2, dtype=torch.int32), None)):
+        with pytest.raises(ValueError):
+            seqs.copy_pages([b.cache], moves)
+    b.check(b.decode())

@@ -1,0 +1,89 @@
+"""What the Python calls for drafted trees and pages refuse before any address reaches a kernel: types, widths, places
+and caches that are not the layer's.  Host tensors do: these checks come before the one for the device."""
+import pytest
+import torch
+
+from mla_latent_kv_mqa_b200 import build as B
+
+
+@pytest.fixture(scope="module")
+def M():
+    B.build()
+    from types import SimpleNamespace
+
+    from mla_latent_kv_mqa_b200 import layer, pages, tree
+    return SimpleNamespace(L=layer, P=pages, T=tree)
+
+
+def i32(*x, device="cpu"):
+    return torch.tensor(x, dtype=torch.int32, device=device)
+
+
+def setup(M, act="f32", kv="f32"):
+    dims = M.L.dims_for(2, 8, 16, 4, act=act, kv=kv, page=4)
+    lay = M.L.MLADecodeLayer.__new__(M.L.MLADecodeLayer)
+    lay.dims = dims
+    return dims, lay, M.L.PagedLatentCache(dims, 3, device="cpu"), M.T.DraftTrees(i32(0, 2), i32(-1, 0), 2)
+
+
+def test_decode_tree_queries_and_caches(M):
+    dims, lay, cache, trees = setup(M)
+    table, lens = torch.zeros(1, 2, dtype=torch.int32), i32(5)
+    other = {k: M.L.PagedLatentCache(M.L.dims_for(2, 8, c, r, act="f32", kv=kv, page=p), 3, device="cpu")
+             for k, (c, r, kv, p) in dict(kind=(16, 4, "bf16", 4), width=(32, 4, "f32", 4), rope=(16, 8, "f32", 4), page=(16, 4, "f32", 8)).items()}
+
+    def call(match, **kw):
+        with pytest.raises(ValueError, match=match):
+            lay.decode_tree(**{**dict(cache=cache, q_abs=torch.zeros(2, 2, 20), block_table=table, seq_lens=lens, trees=trees,
+                                      max_seq_len=8), **kw})
+    for q in (torch.zeros(2, 1, 20), torch.zeros(2, 2, 16), torch.zeros(2, 40), torch.zeros(2, 2, 20, dtype=torch.bfloat16),
+              torch.zeros(2, 2, 20, dtype=torch.float64)):
+        call("q_abs is", q_abs=q)
+    for c in other.values():
+        call("cache's rows", cache=c)
+    call("contiguous and on the current", )                              # host tensors
+
+
+def test_tree_append_rows(M):
+    dims, lay, cache, trees = setup(M)
+    table = torch.zeros(1, 2, dtype=torch.int32)
+    for c, k in ((torch.zeros(2, 8), torch.zeros(2, 4)), (torch.zeros(2, 16), torch.zeros(2, 2)), (torch.zeros(32), torch.zeros(2, 4)),
+                 (torch.zeros(2, 16, dtype=torch.bfloat16), torch.zeros(2, 4)), (torch.zeros(2, 16), torch.zeros(2, 4, dtype=torch.bfloat16))):
+        with pytest.raises(ValueError, match="c_kv"):
+            lay.tree_append(cache, c, k, trees, table)
+    wrong = M.L.PagedLatentCache(M.L.dims_for(2, 8, 16, 4, act="f32", kv="bf16", page=4), 3, device="cpu")
+    with pytest.raises(ValueError, match="cache's rows"):
+        lay.tree_append(wrong, torch.zeros(2, 16), torch.zeros(2, 4), trees, table)
+
+
+def test_trees_are_on_one_device_and_stay_as_looked_over(M):
+    cu, parent, mask = i32(0, 2), i32(-1, 0), torch.zeros(2, 1, dtype=torch.int32)
+    for args in ((cu, parent.to("meta"), 2), (cu.to("meta"), parent, 2), (cu, parent, 2, mask.to("meta"))):
+        with pytest.raises(ValueError, match="one device"):
+            M.T.DraftTrees(*args)
+    with pytest.raises(ValueError):
+        M.T.DraftTrees(cu, parent, 2, mask.view(-1))
+    trees = M.T.DraftTrees(cu, parent, 2, mask)
+    assert trees.mask is mask
+    for name in ("cu_nodes", "parent", "mask", "pos", "slot", "seq_idx"):
+        with pytest.raises(AttributeError):
+            setattr(trees, name, torch.zeros(1))
+
+
+def test_keep_lists_and_caches(M):
+    dims, lay, cache, trees = setup(M)
+    table, lens = torch.zeros(1, 2, dtype=torch.int32), i32(5)
+    for keep in (i32(0), torch.zeros(1, 1, 1, dtype=torch.int32)):
+        with pytest.raises(ValueError, match="max_keep"):
+            trees.keep([cache], table, lens, keep, i32(1))
+    with pytest.raises(ValueError, match="no caches"):
+        trees.keep([], table, lens, torch.zeros(1, 1, dtype=torch.int32), i32(1))
+
+
+def test_cache_buffers_are_on_one_device(M):
+    dims = M.L.dims_for(2, 8, 16, 4, kv="fp8", page=4)
+    kv, kr, s = torch.zeros(3, 4, 16, dtype=torch.uint8), torch.zeros(3, 4, 4, dtype=torch.bfloat16), torch.zeros(3, 4)
+    M.L.PagedLatentCache.over(dims, kv, kr, s)
+    for a, b in ((kr.to("meta"), s), (kr, s.to("meta"))):
+        with pytest.raises(ValueError, match="one device"):
+            M.L.PagedLatentCache.over(dims, kv, a, b)
