@@ -97,6 +97,26 @@ _on_device = getattr(torch._C, "_cuda_getDevice", None)
 _MISREAD = ("tensors are contiguous and on the current CUDA device; lengths, tables and indices are int32")
 
 
+def _stream_object(handle: int):
+    return torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
+
+
+def new_on(stream, make):
+    """make()'s tensors, for a call on ``stream``.  On another stream than the current one they are taken from that
+    stream's memory (what held it before has run there) and given back once both streams are past them."""
+    if stream is None:
+        return make()
+    here, handle = N._stream(None), N._stream(stream)
+    if here == handle:
+        return make()
+    current = torch.cuda.current_stream()
+    with torch.cuda.stream(_stream_object(handle)):
+        made = make()
+    for x in made:
+        x.record_stream(current)
+    return made
+
+
 def fits(dims: N.mla_dims_t, of: N.mla_dims_t) -> bool:
     """A cache of ``of`` has the rows that a layer of ``dims`` reads and writes."""
     return of is dims or (of.kv_dtype == dims.kv_dtype and of.d_c == dims.d_c and of.d_r == dims.d_r and
@@ -133,7 +153,8 @@ class Workspace:
             if buf is not None:
                 self._kept.append(buf)
                 need = max(need, 2 * buf.numel())
-            buf = self._by_stream[handle] = torch.empty(need, dtype=torch.uint8, device=self.device)
+            buf, = new_on(stream, lambda: (torch.empty(need, dtype=torch.uint8, device=self.device),))
+            self._by_stream[handle] = buf
         return buf
 
 
@@ -278,12 +299,12 @@ class MLADecodeLayer:
                 not (q_abs.is_contiguous() and block_table.is_contiguous() and seq_lens.is_contiguous())):
             raise ValueError(_MISREAD)
         if o_lat is None:
-            o_lat = q_abs.new_empty((T, d.n_h, d.d_c), dtype=TORCH_ACT[dt])
+            o_lat, = new_on(stream, lambda: (q_abs.new_empty((T, d.n_h, d.d_c), dtype=TORCH_ACT[dt]),))
         elif (o_lat.dtype != TORCH_ACT[dt] or o_lat.shape != (T, d.n_h, d.d_c) or not o_lat.is_contiguous() or
               o_lat.get_device() != here):
             raise ValueError("decode_tree: o_lat is contiguous [nodes, n_h, d_c] of out_dtype, where q_abs is")
         if lse is None:
-            lse = q_abs.new_empty((T, d.n_h), dtype=torch.float32)
+            lse, = new_on(stream, lambda: (q_abs.new_empty((T, d.n_h), dtype=torch.float32),))
         elif lse.dtype != torch.float32 or lse.shape != (T, d.n_h) or not lse.is_contiguous() or lse.get_device() != here:
             raise ValueError("decode_tree: lse is contiguous [nodes, n_h] fp32, where q_abs is")
         if workspace is None:

@@ -9,23 +9,25 @@ hold each (include/mla.h, "Pages of the cache").
     seqs.copy_pages(caches, seqs.compact())      # pages in use to the front of the pool
 
 ``block_table``, ``refs`` and ``seq_lens`` are the tensors the other calls take.  One table serves the
-caches of all layers.
+caches of all layers.  Calls take the current stream, or ``stream``: what a caller hands to a call on another
+stream than the current one, it keeps until that stream is past it.
 """
 from __future__ import annotations
 
 import torch
 
 from . import native as N
-from .layer import _INT32, _MISREAD, Workspace, _on_device, same_caches
+from .layer import _INT32, _MISREAD, Workspace, _on_device, _stream_object, new_on, same_caches
 
 
 class PageMoves:
     """Page copies to make, on the device: ``pairs`` [most, 2] of (from, to) and their ``number`` [1].  One buffer
-    holds both; unpacks as (pairs, number)."""
+    holds both, of the stream that writes them; unpacks as (pairs, number)."""
 
-    def __init__(self, most: int, device):
+    def __init__(self, most: int, device, stream=None):
         self.most = most
-        self._buf = torch.empty((most + 1, 2), dtype=torch.int32, device=device)
+        self._buf, = new_on(stream, lambda: (torch.empty((most + 1, 2), dtype=torch.int32, device=device),))
+        self._stream = N._stream(stream) if self._buf.is_cuda else None
         self.pairs_ptr = self._buf.data_ptr()
         self.number_ptr = self.pairs_ptr + 8 * most
 
@@ -36,6 +38,12 @@ class PageMoves:
     @property
     def number(self) -> torch.Tensor:
         return self._buf[self.most, :1]
+
+    def used_on(self, stream):
+        """A call on ``stream`` reads the moves: their memory is not given back before it has."""
+        handle = N._stream(stream)
+        if handle != self._stream:
+            self._buf.record_stream(_stream_object(handle))
 
     def __iter__(self):
         return iter((self.pairs, self.number))
@@ -97,7 +105,7 @@ class PagedSequences:
             raise ValueError("grow: a length for every sequence")
         self._look_over(new_lens, seqs)
         ws = self._workspace(n, stream)
-        moves = PageMoves(n, self._block_table.device)
+        moves = PageMoves(n, self._block_table.device, stream)
         N.mla_pages_grow(self._table, n, seqs, new_lens, moves.pairs_ptr, moves.number_ptr, ws, ws.numel(), stream)
         return moves
 
@@ -112,7 +120,7 @@ class PagedSequences:
         """The pages in use take the lowest ids; returns the page copies to make (PageMoves), for copy_pages."""
         self._look_over()
         ws = self._workspace(0, stream)
-        moves = PageMoves(self.num_blocks // 2, self._block_table.device)
+        moves = PageMoves(self.num_blocks // 2, self._block_table.device, stream)
         N.mla_pages_compact(self._table, moves.pairs_ptr, moves.number_ptr, ws, ws.numel(), stream)
         return moves
 
@@ -129,6 +137,7 @@ class PagedSequences:
         pools = N.make_pools([c.pool() for c in caches])
         if isinstance(moves, PageMoves):
             pairs, number, most = moves.pairs_ptr, moves.number_ptr, moves.most
+            moves.used_on(stream)
         else:
             pairs, number = moves
             self._look_over(pairs, number)

@@ -18,7 +18,7 @@ from __future__ import annotations
 import torch
 
 from . import native as N
-from .layer import _INT32, _MISREAD, _on_device, same_caches
+from .layer import _INT32, _MISREAD, _on_device, new_on, same_caches
 
 
 class DraftTrees:
@@ -101,7 +101,7 @@ class DraftTrees:
                 not (block_table.is_contiguous() and seq_lens.is_contiguous() and keep.is_contiguous() and num_keep.is_contiguous())):
             raise ValueError(_MISREAD)
         if new_lens is None:
-            new_lens = torch.empty_like(seq_lens)
+            new_lens, = new_on(stream, lambda: (torch.empty_like(seq_lens),))
         elif new_lens.dtype is not _INT32 or new_lens.numel() != B or new_lens.get_device() != here or not new_lens.is_contiguous():
             raise ValueError(_MISREAD)
         dims, pools = same_caches(caches, caches[0].num_blocks), N.make_pools([c.pool() for c in caches])

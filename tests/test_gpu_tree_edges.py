@@ -74,3 +74,97 @@ def test_host_tensors_among_device_ones_are_refused():
         with pytest.raises(ValueError):
             seqs.copy_pages([b.cache], moves)
     b.check(b.decode())
+
+
+# ---- calls on a stream that is not the current one ----------------------------------------------------
+
+def _sleep(stream, ms=30):
+    with torch.cuda.stream(stream):
+        torch.cuda._sleep(int(ms * 1.9e6))
+
+
+def _moved_pool(seqs, cache, blocks):
+    """Three sequences over a pool of `blocks` pages, the first ended: pages to move."""
+    seqs.grow(dev([64 * 5, 64 * 6, 64 * 4]))
+    seqs.trim(dev([0, 64 * 6, 64 * 4]))
+    cache.kv_pool.copy_(torch.arange(blocks, device="cuda")[:, None, None].expand_as(cache.kv_pool).to(cache.kv_pool.dtype))
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("second", [False, True])
+def test_moves_that_are_dropped_while_another_stream_reads_them(second):
+    """seqs.copy_pages(caches, seqs.compact(stream=s), stream=s): nobody holds the moves when s comes to them."""
+    from mla_latent_kv_mqa_b200 import layer as L, pages as P
+    cache = L.PagedLatentCache(L.dims_for(2, 128, 512, 64), 40)
+    seqs = P.PagedSequences(64, 3, 8, 40)
+    s, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(3):
+        seqs.trim(dev([0, 0, 0]))
+        _moved_pool(seqs, cache, 40)
+        _sleep(s)
+        moves = seqs.compact(stream=s)
+        reader = s
+        if second:
+            s2.wait_stream(s)
+            reader = s2
+        seqs.copy_pages([cache], moves, stream=reader)
+        del moves
+        junk = [torch.full((n, 2), 1, dtype=torch.int32, device="cuda") for n in (21, 20, 21, 22) for _ in range(8)]
+        with torch.cuda.stream(s):
+            junk += [torch.full((21, 2), 1, dtype=torch.int32, device="cuda") for _ in range(8)] if second else []
+        torch.cuda.synchronize()
+        del junk
+        # pages 5..10 and 11..14 were in use, the last five of them move to 0..4
+        want = torch.arange(40.0)
+        want[:5] = torch.arange(10.0, 15.0)
+        assert torch.equal(cache.kv_pool[:, 0, 0].float().cpu(), want)
+        seqs.trim(dev([0, 0, 0]))
+
+
+def test_grow_on_another_stream_and_its_copies():
+    from mla_latent_kv_mqa_b200 import layer as L, pages as P
+    cache = L.PagedLatentCache(L.dims_for(2, 128, 512, 64), 40)
+    seqs = P.PagedSequences(64, 4, 8, 40)
+    s = torch.cuda.Stream()
+    seqs.grow(dev([100, 0, 0, 0]))
+    seqs.fork(dev([0, 0, 0]), dev([1, 2, 3]))
+    cache.kv_pool.copy_(torch.arange(40, device="cuda")[:, None, None].expand_as(cache.kv_pool).to(cache.kv_pool.dtype))
+    lens = dev([101, 102, 103, 104])
+    torch.cuda.synchronize()
+    _sleep(s)
+    seqs.copy_pages([cache], seqs.grow(lens, stream=s), stream=s)
+    junk = [torch.full((5, 2), 30, dtype=torch.int32, device="cuda") for _ in range(16)]
+    torch.cuda.synchronize()
+    del junk
+    assert sorted(seqs.block_table[:, 1].tolist()) == [1, 2, 3, 4]
+    want = torch.arange(40.0)
+    want[2:5] = 1
+    assert torch.equal(cache.kv_pool[:, 0, 0].float().cpu(), want)
+
+
+@pytest.mark.parametrize("raw", [False, True])
+@pytest.mark.parametrize("flags", [0, 1])
+def test_outputs_and_workspaces_of_another_stream(flags, raw):
+    """Memory that pending work of the current stream still writes is not handed to a call on another stream."""
+    b = Batch([900, 300, 31], [6, 4, 9], heads=32, seed=65, flags=flags)
+    want, want_lse = b.decode()
+    keep, num = dev([[0], [0], [0]]), dev([1, 1, 1])
+    s = torch.cuda.Stream()
+    stream = s.cuda_stream if raw else s
+    b.layer._tree_ws._by_stream.clear()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    mem = [torch.empty_like(want), torch.empty_like(want_lse), torch.empty(1 << 26, dtype=torch.uint8, device="cuda"), torch.empty_like(b.lens)]
+    torch.cuda._sleep(int(30 * 1.9e6))
+    for x in mem:
+        x.fill_(7)
+    del mem, x
+    o, lse = b.layer.decode_tree(b.cache, b.q, b.table, b.lens, b.trees, b.max_len, stream=stream)
+    new = b.trees.keep([b.cache], b.table, b.lens, keep, num, stream=stream)
+    torch.cuda.synchronize()
+    assert torch.equal(o, want) and torch.equal(lse, want_lse)
+    assert new.tolist() == [901, 301, 32]
+    del o, lse, new                                                  # freed with the current stream past them
+    again = b.layer.decode_tree(b.cache, b.q, b.table, b.lens, b.trees, b.max_len, stream=stream)
+    torch.cuda.current_stream().wait_stream(s)
+    assert torch.equal(again[0], want) and torch.equal(again[1], want_lse)
