@@ -13,6 +13,8 @@ A decode step of one layer (itwiki "ë©€í‹° í—¤ë“œ ìž ìž¬ ì–´í…ì…˜", sections ë¶
 """
 from __future__ import annotations
 
+import threading
+
 import torch
 
 from . import native as N
@@ -94,11 +96,19 @@ class PagedLatentCache:
 # microsecond a call.)
 _INT32 = torch.int32
 _on_device = getattr(torch._C, "_cuda_getDevice", None)
+_is_capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", None)
 _MISREAD = ("tensors are contiguous and on the current CUDA device; lengths, tables and indices are int32")
 
 
 def _stream_object(handle: int):
     return torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
+
+
+def _capturing(handle: int, stream) -> bool:
+    if stream is None:
+        return _is_capturing()
+    with torch.cuda.stream(_stream_object(handle)):
+        return _is_capturing()
 
 
 def new_on(stream, make):
@@ -134,11 +144,27 @@ def same_caches(caches, num_blocks) -> N.mla_dims_t:
 
 class Workspace:
     """Device scratch for calls of one kind: a buffer per stream, so that calls on two streams do not meet in one,
-    grown by doubling.  An outgrown buffer is kept, as a captured graph may hold its address."""
+    grown by doubling.  A call that is being captured gets a buffer of its own from the graph's memory
+    (torch.cuda.graph), so that graphs that replay at the same time do not meet either.
+    ``lock``: held from get() until the call's kernels are enqueued, or another thread's would come between them."""
 
     def __init__(self, device):
         self.device = device
-        self._sizes, self._by_stream, self._kept = {}, {}, []
+        self.lock = threading.Lock()
+        self._sizes, self._by_stream = {}, {}
+
+    _shared: dict = {}
+
+    @classmethod
+    def shared(cls, device) -> "Workspace":
+        """The device's one: layers' calls on a stream run one after the other and can share its buffer."""
+        device = torch.device(device)
+        if device.type == "cuda" and device.index is None:
+            device = torch.device("cuda", torch.cuda.current_device())
+        return cls._shared.setdefault(device, cls(device))
+
+    def _new(self, need, stream):
+        return new_on(stream, lambda: (torch.empty(need, dtype=torch.uint8, device=self.device),))[0]
 
     def get(self, key, stream, size):
         """A buffer of at least ``size()`` bytes, which depends on ``key`` alone."""
@@ -148,13 +174,13 @@ class Workspace:
                 self._sizes.clear()
             need = self._sizes[key] = max(256, size())
         handle = N._stream(stream)
+        if _capturing(handle, stream):
+            return self._new(need, stream)
         buf = self._by_stream.get(handle)
         if buf is None or buf.numel() < need:
             if buf is not None:
-                self._kept.append(buf)
                 need = max(need, 2 * buf.numel())
-            buf, = new_on(stream, lambda: (torch.empty(need, dtype=torch.uint8, device=self.device),))
-            self._by_stream[handle] = buf
+            buf = self._by_stream[handle] = self._new(need, stream)
         return buf
 
 
@@ -170,7 +196,7 @@ class MLADecodeLayer:
         self._ws = None
         self._ws_key = None
         self._pf_ws = None
-        self._tree_ws = Workspace(self.device)
+        self._tree_ws, self._tree_key = Workspace.shared(self.device), bytes(dims)
 
     # -- the four calls ----------------------------------------------------------------------
     def append(self, cache: PagedLatentCache, c_kv, k_r, seq_idx, pos, block_table, stream=None):
@@ -281,8 +307,9 @@ class MLADecodeLayer:
     def decode_tree(self, cache: PagedLatentCache, q_abs, block_table, seq_lens, trees, max_seq_len,
                     out_dtype="f32", o_lat=None, lse=None, stream=None, workspace=None):
         """Every drafted node over the committed tokens and the nodes its mask names; returns
-        (o_lat [nodes, n_h, d_c], lse [nodes, n_h]).  Without ``workspace`` (uint8 tensor) the layer's own for the
-        stream is used; captured graphs that may replay at the same time need one each."""
+        (o_lat [nodes, n_h, d_c], lse [nodes, n_h]).  Without ``workspace`` (uint8 tensor) the stream's is used, which
+        the layers of a device share, or one of the graph that is being captured; calls that may run at the same
+        time take no ``workspace`` in common."""
         d = self.dims
         B, max_blocks = block_table.shape
         T = trees.total_nodes
@@ -307,14 +334,16 @@ class MLADecodeLayer:
             lse, = new_on(stream, lambda: (q_abs.new_empty((T, d.n_h), dtype=torch.float32),))
         elif lse.dtype != torch.float32 or lse.shape != (T, d.n_h) or not lse.is_contiguous() or lse.get_device() != here:
             raise ValueError("decode_tree: lse is contiguous [nodes, n_h] fp32, where q_abs is")
-        if workspace is None:
-            workspace = self._tree_ws.get((B, T, max_seq_len), stream,
-                                          lambda: N.mla_decode_tree_workspace_size(d, B, T, max_seq_len))
-        elif workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.get_device() != here:
+        if workspace is not None and (workspace.dtype != torch.uint8 or not workspace.is_contiguous() or
+                                      workspace.get_device() != here):
             raise ValueError("decode_tree: workspace is contiguous uint8, where q_abs is")
-        N.mla_decode_tree(d, B, trees.cu_nodes, T, trees.max_nodes, q_abs, cache.kv_pool, cache.kr_pool,
-                          cache.kv_scale, block_table, max_blocks, cache.num_blocks, seq_lens, max_seq_len,
-                          trees.mask, trees.mask_words, workspace, workspace.numel(), o_lat, dt, lse, stream)
+        with self._tree_ws.lock:
+            if workspace is None:
+                workspace = self._tree_ws.get((self._tree_key, B, T, max_seq_len), stream,
+                                              lambda: N.mla_decode_tree_workspace_size(d, B, T, max_seq_len))
+            N.mla_decode_tree(d, B, trees.cu_nodes, T, trees.max_nodes, q_abs, cache.kv_pool, cache.kr_pool,
+                              cache.kv_scale, block_table, max_blocks, cache.num_blocks, seq_lens, max_seq_len,
+                              trees.mask, trees.mask_words, workspace, workspace.numel(), o_lat, dt, lse, stream)
         return o_lat, lse
 
     def out_proj(self, o_lat, out_dtype="f32", out=None, stream=None):

@@ -94,8 +94,9 @@ class PagedSequences:
             raise ValueError("fork: a parent for every child")
         self._look_over(parent, child)
         n = parent.numel()
-        ws = self._workspace(n, stream)
-        N.mla_pages_fork(self._table, n, parent, child, ws, ws.numel(), stream)
+        with self._ws.lock:
+            ws = self._workspace(n, stream)
+            N.mla_pages_fork(self._table, n, parent, child, ws, ws.numel(), stream)
 
     def grow(self, new_lens, seqs=None, stream=None):
         """Sequences ``seqs`` (default: 0, 1, ...) grow to ``new_lens`` tokens; returns the page copies to
@@ -104,9 +105,10 @@ class PagedSequences:
         if seqs is not None and seqs.numel() != n:
             raise ValueError("grow: a length for every sequence")
         self._look_over(new_lens, seqs)
-        ws = self._workspace(n, stream)
         moves = PageMoves(n, self._block_table.device, stream)
-        N.mla_pages_grow(self._table, n, seqs, new_lens, moves.pairs_ptr, moves.number_ptr, ws, ws.numel(), stream)
+        with self._ws.lock:
+            ws = self._workspace(n, stream)
+            N.mla_pages_grow(self._table, n, seqs, new_lens, moves.pairs_ptr, moves.number_ptr, ws, ws.numel(), stream)
         return moves
 
     def trim(self, new_lens, seqs=None, stream=None):
@@ -114,14 +116,16 @@ class PagedSequences:
         if seqs is not None and seqs.numel() != new_lens.numel():
             raise ValueError("trim: a length for every sequence")
         self._look_over(new_lens, seqs)
-        N.mla_pages_trim(self._table, new_lens.numel(), seqs, new_lens, stream)
+        with self._ws.lock:  # not between the kernels of another call
+            N.mla_pages_trim(self._table, new_lens.numel(), seqs, new_lens, stream)
 
     def compact(self, stream=None):
         """The pages in use take the lowest ids; returns the page copies to make (PageMoves), for copy_pages."""
         self._look_over()
-        ws = self._workspace(0, stream)
         moves = PageMoves(self.num_blocks // 2, self._block_table.device, stream)
-        N.mla_pages_compact(self._table, moves.pairs_ptr, moves.number_ptr, ws, ws.numel(), stream)
+        with self._ws.lock:
+            ws = self._workspace(0, stream)
+            N.mla_pages_compact(self._table, moves.pairs_ptr, moves.number_ptr, ws, ws.numel(), stream)
         return moves
 
     def copy_pages(self, caches, moves, stream=None):

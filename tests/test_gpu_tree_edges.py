@@ -168,3 +168,89 @@ def test_outputs_and_workspaces_of_another_stream(flags, raw):
     again = b.layer.decode_tree(b.cache, b.q, b.table, b.lens, b.trees, b.max_len, stream=stream)
     torch.cuda.current_stream().wait_stream(s)
     assert torch.equal(again[0], want) and torch.equal(again[1], want_lse)
+
+
+# ---- workspaces -----------------------------------------------------------------------------------------
+
+def test_two_graphs_of_a_layer_that_replay_at_the_same_time():
+    """Captured one after the other on the same capture stream, replayed on two streams at once."""
+    a = Batch([3000, 2500], [20, 9], heads=32, seed=71)
+    c = Batch([9000, 700, 41], [6, 4, 30], heads=32, seed=72)
+    c.layer = a.layer
+    want = [tuple(x.clone() for x in y.decode()) for y in (a, c)]
+    graphs, outs = [], []
+    for x in (a, c):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(x.layer.decode_tree(x.cache, x.q, x.table, x.lens, x.trees, x.max_len))
+        graphs.append(g)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for o, lse in outs:
+            o.zero_()
+        torch.cuda.synchronize()
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                for _ in range(5):
+                    g.replay()
+        torch.cuda.synchronize()
+        for got, ref in zip(outs, want):
+            assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
+
+
+def test_a_graph_captured_on_a_stream_that_is_passed():
+    b = Batch([900, 300], [6, 4], heads=32, seed=73)
+    want, want_lse = (x.clone() for x in b.decode())
+    s, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        o, lse = b.layer.decode_tree(b.cache, b.q, b.table, b.lens, b.trees, b.max_len, stream=s.cuda_stream)
+    b.decode()
+    junk = [torch.full((1 << 22,), float("nan"), device="cuda") for _ in range(16)]
+    g.replay()
+    torch.cuda.synchronize()
+    del junk
+    assert torch.equal(o, want) and torch.equal(lse, want_lse)
+
+
+def test_the_layers_of_a_model_share_a_stream_s_workspace():
+    b = Batch([900, 300], [6, 4], heads=32, seed=74)
+    from mla_latent_kv_mqa_b200 import layer as L
+    want, want_lse = b.decode()
+    w = torch.zeros(32 * 128, 512, device="cuda", dtype=torch.bfloat16)
+    layers = [L.MLADecodeLayer(b.dims, w, w) for _ in range(61)]
+    before = torch.cuda.memory_allocated()
+    for lay in layers:
+        o, lse = lay.decode_tree(b.cache, b.q, b.table, b.lens, b.trees, b.max_len)
+        assert torch.equal(o, want) and torch.equal(lse, want_lse)
+    assert torch.cuda.memory_allocated() - before < 8 << 20
+
+
+def test_two_threads_on_one_stream():
+    """Main kernel and join of a call stay together, so do the kernels of the page calls."""
+    import threading
+
+    from mla_latent_kv_mqa_b200 import pages as P
+    a = Batch([3000, 2500], [20, 9], heads=32, seed=75)
+    c = Batch([9000, 700, 41], [6, 4, 30], heads=32, seed=76)
+    want = [tuple(x.clone() for x in y.decode()) for y in (a, c)]
+    seqs = P.PagedSequences(4, 40, 6, 400)
+    seqs.grow(dev(np.full(40, 11)))
+    table, refs = seqs.block_table.clone(), seqs.refs.clone()
+    wrong = []
+
+    def work(k):
+        x = (a, c)[k]
+        own = torch.arange(20 * k, 20 * k + 20, device="cuda", dtype=torch.int32)
+        got = []
+        for _ in range(60):
+            got.append(x.layer.decode_tree(x.cache, x.q, x.table, x.lens, x.trees, x.max_len))
+            seqs.fork(own, own)                                      # each thread's own sequences, onto themselves
+        torch.cuda.synchronize()
+        wrong.append(sum(not (torch.equal(o, want[k][0]) and torch.equal(lse, want[k][1])) for o, lse in got))
+
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(2)]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    assert wrong == [0, 0]
+    assert torch.equal(seqs.block_table, table) and torch.equal(seqs.refs, refs)
