@@ -408,8 +408,11 @@ mla_status_t mla_tree_append(const mla_dims_t *dims, int T, const void *c_kv, co
  *     o_lat = sum_j softmax(s)_j c_j,       lse = ln sum_j exp(s_j).
  * A node that sees no token (no committed one and an empty mask row) gets o_lat = 0, lse = -inf.
  * The mask is taken as it is: any set of drafted tokens, not only ancestors.
- * What a masked token's row holds does not matter, infinities and NaN included: a token of weight 0
- * (masked, or a score of -inf) is no part of the sums.
+ * What a masked token's row holds does not matter, infinities and NaN included.  Nor does what a drafted row holds
+ * reach a node that gives it a score of -inf: a token of weight 0 is no part of the sums.  Committed rows are taken
+ * to be finite.  Where one is not, its scores are what the formula says (so lse is, and
+ * a score of +inf or NaN makes its row NaN); of a token whose score is -inf the tensor-core kernel over a bf16 cache
+ * makes the columns of o NaN in which the row is not finite, the others leave it out.
  *   cu_nodes    [B+1], total_nodes, max_nodes: a host-side upper bound of the n_b
  *   q_abs       [total_nodes, n_h, d_c+d_r] act dtype (from mla_absorb_q)
  *   cache, block_table, seq_lens, max_seq_len: as for mla_decode; seq_lens[b] in [n_b, max_seq_len]

@@ -37,7 +37,9 @@
 // Masks.  Steps before ctx need none.  In the others a row's thread selects by its node's bits.  P is 0
 // where a node does not see a token, and 0 times what such a row holds must be 0: the cleaning warps zero
 // the rows behind the sequence, and the infinities and NaN of drafted rows (whoever sees such a row has
-// them in its scores already).  Committed rows are seen by every row of the tile.
+// them in its scores already, as NaN or as weight 0).  Committed rows are seen by every row of the tile and are
+// taken as they are: over bf16 an infinity among them is NaN in its column of O for a row whose score it makes
+// -inf too (to clean them would take 16 KB of shared memory once more through registers for each V stage).
 //
 // Split along the tokens.  All (tile, step) units of the batch are dealt to the pairs in contiguous
 // equal runs; a tile that lies in several runs leaves partial (O, m, l), at most two a pair, which a

@@ -254,3 +254,52 @@ def test_two_threads_on_one_stream():
     [t.join() for t in threads]
     assert wrong == [0, 0]
     assert torch.equal(seqs.block_table, table) and torch.equal(seqs.refs, refs)
+
+
+# ---- rows that are not finite ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("kv,flags", [("bf16", 0), ("fp8", 0), ("bf16", 1), ("fp8", 1)])
+@pytest.mark.parametrize("ctx", [200, 3000])                         # in one run, and joined from several
+@pytest.mark.parametrize("drafted", [False, True])
+def test_an_infinite_row_and_queries_of_both_signs(kv, flags, ctx, drafted):
+    """Score +inf: NaN.  Score -inf: the token is no part of the sums; a committed one is NaN in the infinite column over
+    a bf16 cache on the tensor cores.  (FP8: an infinite scale makes the row's every column infinite.)"""
+    b = Batch([ctx, 64], [5, 3], kv=kv, flags=flags, seed=81, heads=16)
+    slot, column = (ctx + 1 if drafted else 70), 7
+    b.see[0][:, 1] = True                                            # every node sees the drafted row
+    b.trees.mask.copy_(dev(np.concatenate([R.bits(s, b.trees.mask_words) for s in b.see])))
+    minus = torch.arange(16, device="cuda") % 2 == 1                 # heads whose score is -inf
+    at = b.owned[0][slot // 64], slot % 64
+    if kv == "fp8":
+        b.cache.kv_pool[at] = 0x38                                   # ones: the score's sign is the sum's
+        b.cache.kr_pool[at] = 0
+        b.q[:, :, :512] = b.q[:, :, :512].abs() * torch.where(minus, -1.0, 1.0)[:, None].to(b.q.dtype)
+    else:
+        b.q[:, :, column] = torch.where(minus, -1.0, 1.0).to(b.q.dtype)
+    n0 = 5
+    if kv == "fp8":
+        b.cache.kv_scale[at] = float("inf")
+    else:
+        b.cache.kv_pool[at[0], at[1], column] = float("inf")
+    o, lse = b.decode()
+    assert torch.isnan(o[:n0, ~minus]).all() and not torch.isfinite(lse[:n0, ~minus]).any()
+    rows = R.cache_rows(b.cache.kv_pool, b.cache.kr_pool, b.cache.kv_scale, b.table[0], ctx + 5, 64)
+    sees = np.concatenate([np.ones((5, ctx), dtype=bool), b.see[0]], 1)
+    sees[:, slot] = False
+    sees = torch.from_numpy(sees).cuda()
+    ro, rl, size, reach = R.attend(b.q[:n0], rows, sees, 512, b.scale)
+    bound = R.o_bound(ro, size, reach, b.row, False, b.tensor_core())
+    lb = R.lse_bound(rl, reach, b.row)
+    if kv == "fp8" and b.tensor_core():
+        j = torch.arange(ctx + 5, device="cuda")
+        where = b.owned[0][j // 64], j % 64
+        w = torch.where(torch.isfinite(b.cache.kv_scale[where]), b.cache.kv_scale[where], 0)
+        ds, da = R.fp8_terms(b.q[:n0], b.cache.kv_pool[where], w, sees, 512, b.scale)
+        bound, lb = bound + 2 * size * ds[..., None] + da * float(w.max()), lb + ds
+    right = (o[:n0].double() - ro).abs() <= bound
+    if kv == "bf16" and flags == 0 and not drafted:
+        assert torch.isnan(o[:n0, minus, column]).all()
+        right[:, :, column] = True
+    assert right[:, minus].all()
+    assert ((lse[:n0].double() - rl).abs() <= lb)[:, minus].all()
+    assert torch.isfinite(o[n0:]).all() and torch.isfinite(lse[n0:]).all()
