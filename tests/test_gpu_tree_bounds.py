@@ -1,0 +1,46 @@
+"""The drafted-tree attention against its formula in 64 bits, each kernel held to what it rounds (tests/tree_bounds.py):
+few tokens, where a weight's rounding shows whole, and many."""
+import numpy as np
+import pytest
+import torch
+
+from tests import tree_bounds as T, tree_ref as R
+from tests.test_gpu_tree import TOY, V3, Batch, no_error
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from mla_latent_kv_mqa_b200 import build
+    build.build()
+
+
+def check(b, got, out="f32", sample=9):
+    o, lse = got
+    worst = 0.0
+    for s in range(b.B):
+        nodes = np.unique(np.linspace(0, b.n[s] - 1, min(sample, b.n[s])).astype(int))
+        t, (ro, rl, size, reach) = b.reference(s, nodes)
+        bound = T.o_bound(ro, size, reach, b.row, int(b.ctx[s] + b.n[s]), out == "bf16", T.kind_of(b))
+        lb = R.lse_bound(rl, reach, b.row)
+        if T.kind_of(b) == "fp8":
+            bound = bound + 2 * size * b.extra[0][..., None] + b.extra[1]
+            lb = lb + b.extra[0]
+        worst = max(worst, float(((o[t].double() - ro).abs() / bound).max()))
+        assert ((lse[t].double() - rl).abs() <= lb).all()
+    assert worst <= 1, worst
+    no_error()
+
+
+@pytest.mark.parametrize("kv,act,shape,flags", [("bf16", "bf16", V3, 0), ("fp8", "bf16", V3, 0), ("bf16", "bf16", V3, 1), ("fp8", "bf16", V3, 1),
+                                                ("f32", "f32", TOY, 0)])
+@pytest.mark.parametrize("ctx,n,heads", [([1], [1], 128), ([2, 3, 0], [1, 3, 7], 128), ([5, 9], [2, 30], 20), ([250, 700], [3, 2], 64),
+                                         ([4000], [3], 16), ([9000], [2], 64)])
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("spread", [1.0, 6.0])
+def test_each_kernel_rounds_what_it_says(kv, act, shape, flags, ctx, n, heads, out, spread):
+    b = Batch(ctx, n, heads=heads, kv=kv, act=act, shape=shape, flags=flags, seed=91, spread=spread)
+    check(b, b.decode(out), out)
