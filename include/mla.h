@@ -428,8 +428,8 @@ mla_status_t mla_tree_append(const mla_dims_t *dims, int T, const void *c_kv, co
  * Precision: operands as they are (FP8: the codes exactly, the scales in fp32), fp32 accumulation and
  * softmax.  On the tensor cores P is rounded to bf16 for the value product, as in mla_decode; over an FP8
  * cache P times the token's scale to fp16 instead (11 bits; fewer for a token below 2^-16 of the row's
- * largest, to 2^-27 of it), and a query's content elements below 2^-9 of their row's largest are taken to
- * 2^-17 of it.  A query row with infinities or NaN gets NaN.
+ * largest, or of 2^-80 if that is larger, to 2^-27 of it), and a query's content elements below 2^-9 of their
+ * row's largest, or of 2^-61 if that is larger, are taken to 2^-17 of it.  A query row with infinities or NaN gets NaN.
  * MLA_FLAG_FP8_MMA does not concern this call.  MLA_FLAG_TEST_GIVE_UP does what it does in the tensor-core
  * decode, in every pair of SMs with two or more steps of 256 tokens.
  * Deterministic: the result depends only on the logical cache content. */

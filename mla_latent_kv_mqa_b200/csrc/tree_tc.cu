@@ -29,7 +29,7 @@
 // long context's weights: the cleaning warps turn V's codes into fp16 tiles, exactly, by two instructions for
 // four codes (bf16 takes eight), and P is fp16.  Its 11 bits reach from 2^15 down to 2^-14, so m is chosen to
 // bound P with the tokens' scales in it; what is below 2^-16 of a row's largest weight times scale loses
-// bits, and below 2^-27 is lost.  Content and RoPE scores are apart, since only the first take the token's
+// bits, and below 2^-27 is lost (scales below 2^-80, in a row of none larger, sooner).  Content and RoPE scores are apart, since only the first take the token's
 // scale: one buffer of S, no second.  What is left to the softmax and the conversion sets the pace (tensor
 // pipe 50% busy, clocks not limited): every instruction there shows, so the page's scales come two steps
 // after their page's id, without a wait, and what only a sequence's last pages need is out of the common path.
@@ -381,8 +381,9 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     const __half2 v = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&v);
 }
-// At least log2 of a scale's size, by less than 1 (from -60 on).
-__device__ __forceinline__ int scale_exponent(float s) { return max((int)(__float_as_uint(s) >> 23 & 255u) - 126, -60); }
+// At least log2 of a scale's size, by less than 1; a smaller one counts as 2^-80.  (exp2(score - m) reaches 2^(15 + 80)
+// then, and the sum of 2^31 of them 2^126: it stays in fp32.)
+__device__ __forceinline__ int scale_exponent(float s) { return max((int)(__float_as_uint(s) >> 23 & 255u) - 126, -80); }
 // A pair of bf16 values with 0 for infinities and NaN.
 __device__ __forceinline__ uint32_t finite_pair(uint32_t x) {
     return x & ((x & 0x7f80u) == 0x7f80u ? 0xffff0000u : 0xffffffffu) & ((x & 0x7f800000u) == 0x7f800000u ? 0xffffu : 0xffffffffu);
@@ -447,7 +448,8 @@ __device__ __noinline__ void clean_codes(uint32_t src, int odd, int row0, int dr
 // [128, 256).  A bf16 value has 8 significant bits and a code 4, so both parts together are the value itself,
 // down to 2^-9 of the row's largest; below, they are within 2^-17 of that largest.  Scores come out as
 // multiples of 2^-k, the row's `unit`.  (A content element that is not finite makes every score of its row NaN.)
-// k is 68 at most, so that the RoPE columns stay in range.  Eight lanes a row; a lane holds all its 64 columns before it writes.
+// k is 68 at most, so that the RoPE columns stay in range: 2^-61 counts as the largest of a row with less.  Eight
+// lanes a row; a lane holds all its 64 columns before it writes.
 __device__ __forceinline__ void split_query(uint32_t q, int row, int c, float *unit) {
     const uint32_t at = q + row * 128, key = row & 7, half = c >> 2, ch = 2 * (c & 3);
     uint32_t x[4][8], top = 0;

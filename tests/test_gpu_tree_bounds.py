@@ -44,3 +44,35 @@ def check(b, got, out="f32", sample=9):
 def test_each_kernel_rounds_what_it_says(kv, act, shape, flags, ctx, n, heads, out, spread):
     b = Batch(ctx, n, heads=heads, kv=kv, act=act, shape=shape, flags=flags, seed=91, spread=spread)
     check(b, b.decode(out), out)
+
+
+@pytest.mark.parametrize("ctx", [3, 300, 5000])
+@pytest.mark.parametrize("power", [-70, -90, -100, -140, 50, 100])
+@pytest.mark.parametrize("flags", [0, 1])
+def test_scales_far_from_one(ctx, power, flags):
+    """All scales times a power of two, down to denormals.  fp16 keeps 2^-27 of the row's largest weight times scale,
+    or of 2^-80 where that is larger.  A query's content is taken to 2^-17 of its row's largest, or of 2^-61 where
+    that is larger: the row is multiplied by 2^68 at most, and behind its nearest e4m3 value the rest is off by half of
+    e4m3's smallest step, 2^-10, so an element by 2^-78.  (power 100 passes that by far: weights are any then.)"""
+    b = Batch([ctx], [4], heads=24, kv="fp8", flags=flags, seed=93)
+    b.cache.kv_scale.mul_(2.0 ** power)
+    if power > 0:
+        b.q[:, :, :512] *= 2.0 ** -power
+    o, lse = b.decode()
+    t, (ro, rl, size, reach) = b.reference(0)
+    bound = T.o_bound(ro, size, reach, b.row, ctx + 4, False, T.kind_of(b)) + 2.0 ** -149
+    lb = R.lse_bound(rl, reach, b.row)
+    if T.kind_of(b) == "fp8":
+        ds, da = b.extra
+        ds = ds * (2.0 ** -61 / b.q[t][..., :512].double().abs().amax(-1)).clamp(min=1)
+        largest = float(b.cache.kv_scale[b.owned[0]].nan_to_num(0).max())
+        bound = bound + 2 * size * ds[..., None] + da * max(1.0, 2.0 ** -80 / largest)
+        lb = lb + ds
+        if float(ds.max()) > 0.1:                                    # 2 ds is the first order of exp(2 ds) - 1
+            bound = torch.full_like(bound, 2 * 448 * largest)
+    assert torch.isfinite(o[t]).all()
+    worst = float(((o[t].double() - ro).abs() / bound).max()), float(((lse[t].double() - rl).abs() / lb).max())
+    assert max(worst) <= 1, worst
+    if power > -110:
+        assert (o[t] != 0).any()
+    no_error()
