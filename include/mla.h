@@ -424,7 +424,7 @@ mla_status_t mla_tree_append(const mla_dims_t *dims, int T, const void *c_kv, co
  *   lse         [total_nodes, n_h] fp32, written (may be NULL)
  * The tensor-core kernel runs for d_c = 512, d_r = 64, 64-token pages, bf16 activations, a bf16 or FP8
  * cache, any number of heads and no MLA_FLAG_SIMT_DECODE (q_abs, pools and o_lat 16-byte aligned, or
- * MLA_ERR_INVALID_ARG); other shapes run on the CUDA cores.
+ * MLA_ERR_INVALID_ARG); other shapes with d_c + d_r <= 1452 run on the CUDA cores (MLA_ERR_UNSUPPORTED beyond).
  * Precision: operands as they are (FP8: the codes exactly, the scales in fp32), fp32 accumulation and
  * softmax.  On the tensor cores P is rounded to bf16 for the value product, as in mla_decode; over an FP8
  * cache P times the token's scale to fp16 instead (11 bits; fewer for a token below 2^-16 of the row's

@@ -387,7 +387,7 @@ static bool tree_sizes_ok(const mla_dims_t *dims, int B, int total_nodes, int ma
 }
 
 size_t mla_decode_tree_workspace_size(const mla_dims_t *dims, int B, int total_nodes, int max_seq_len) {
-    if (check_dims(dims) != MLA_OK || !tree_sizes_ok(dims, B, total_nodes, max_seq_len)) return 0;
+    if (check_dims(dims) != MLA_OK || !tree_simt_supported(*dims) || !tree_sizes_ok(dims, B, total_nodes, max_seq_len)) return 0;
     if (tree_tc_supported(*dims)) return tree_tc_workspace_bytes(*dims, B, total_nodes);
     return tree_simt_workspace_bytes(*dims, total_nodes, max_seq_len) + 256;
 }
@@ -401,7 +401,7 @@ mla_status_t mla_decode_tree(const mla_dims_t *dims, int B, const int32_t *cu_no
                              mla_stream_t stream) {
     mla_status_t s = check_dims(dims);
     if (s != MLA_OK) return s;
-    if (!act_ok(out_dtype)) return MLA_ERR_UNSUPPORTED;
+    if (!act_ok(out_dtype) || !tree_simt_supported(*dims)) return MLA_ERR_UNSUPPORTED;
     if (!tree_sizes_ok(dims, B, total_nodes, max_seq_len) || max_blocks_per_seq < 1 || num_blocks < 1 ||
         max_nodes < 1 || max_nodes > kMaxTreeNodes || mask_words < (max_nodes + 31) / 32)
         return MLA_ERR_INVALID_ARG;

@@ -371,6 +371,13 @@ TreeSimtPlan tree_simt_plan(const mla_dims_t &d, int T, int max_seq_len) {
 
 }  // namespace
 
+// Shared memory of a block: its queries and a tile's rows.
+static size_t tree_simt_smem(const mla_dims_t &d) {
+    const size_t row = (size_t)d.d_c + d.d_r;
+    return sizeof(float) * (kHeads * row + kTile * (row + 1));
+}
+bool tree_simt_supported(const mla_dims_t &d) { return tree_simt_smem(d) <= 232448; }
+
 size_t tree_simt_workspace_bytes(const mla_dims_t &d, int T, int max_seq_len) {
     const TreeSimtPlan pl = tree_simt_plan(d, T, max_seq_len);
     if (pl.join) return 0;
@@ -389,8 +396,7 @@ cudaError_t launch_tree_simt(const mla_dims_t &d, const TreeArgs &a, void *ws, c
         part.m = reinterpret_cast<float *>(w);
         part.l = reinterpret_cast<float *>(w + align_up(rows * sizeof(float), 256));
     }
-    const int row = d.d_c + d.d_r;
-    const size_t smem = sizeof(float) * ((size_t)kHeads * row + (size_t)kTile * (row + 1));
+    const size_t smem = tree_simt_smem(d);
     const dim3 grid(a.T, pl.n_split, (d.n_h + kHeads - 1) / kHeads);
     cudaError_t e = cudaSuccess;
     auto run = [&](auto kern) {

@@ -123,6 +123,7 @@ __device__ __forceinline__ void dependent_start() {
 }
 
 // ---- launchers ---------------------------------------------------------------------------------
+bool tree_simt_supported(const mla_dims_t &d);  // d_c + d_r up to 1452: shared memory
 size_t tree_simt_workspace_bytes(const mla_dims_t &d, int T, int max_seq_len);
 cudaError_t launch_tree_simt(const mla_dims_t &d, const TreeArgs &a, void *ws, cudaStream_t st);
 // Tensor cores: d_c = 512, d_r = 64, 64-token pages, bf16 activations.

@@ -170,6 +170,14 @@ def test_outputs_and_workspaces_of_another_stream(flags, raw):
     assert torch.equal(again[0], want) and torch.equal(again[1], want_lse)
 
 
+# ---- the widest rows --------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("kv,act,shape", [("f32", "f32", (16, 1024, 428)), ("fp8", "bf16", (8, 16, 1436))])
+def test_the_widest_rows(kv, act, shape):
+    b = Batch([129, 33], [5, 3], kv=kv, act=act, shape=shape, page=16, heads=3, seed=7)
+    b.check(b.decode())
+
+
 # ---- workspaces -----------------------------------------------------------------------------------------
 
 def test_two_graphs_of_a_layer_that_replay_at_the_same_time():

@@ -15,6 +15,21 @@ def M():
     return SimpleNamespace(L=layer, P=pages, T=tree)
 
 
+def test_rows_wider_than_a_block_s_memory_are_unsupported(M):
+    """1452 columns are the most that eight queries and 32 rows fit the shared memory with."""
+    import ctypes
+
+    from mla_latent_kv_mqa_b200 import native as N
+    for d_c, d_r, holds in ((1024, 428, True), (1024, 430, False), (1024, 1024, False), (600, 900, False), (16, 1436, True)):
+        assert (4 * (8 * (d_c + d_r) + 32 * (d_c + d_r + 1)) <= 227 * 1024) == holds
+        dims = N.make_dims(4, 8, d_c, d_r, 64)
+        assert (N.mla_decode_tree_workspace_size(dims, 1, 4, 100) > 0) == holds
+        if not holds:
+            rc = N.library().mla_decode_tree(ctypes.byref(dims), 1, 16, 4, 4, 16, 16, None, None, 16, 4, 8, 16, 100, 16, 1, 256, 1 << 40,
+                                             16, 0, None, None)
+            assert rc == N.MLA_ERR_UNSUPPORTED
+
+
 def i32(*x, device="cpu"):
     return torch.tensor(x, dtype=torch.int32, device=device)
 
