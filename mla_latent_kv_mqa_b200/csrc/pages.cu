@@ -300,10 +300,9 @@ grow_kernel(const __grid_constant__ PageTable p, int n, const int32_t *seqs,
 
 // ---- mla_pages_compact -----------------------------------------------------------------------
 // One block decides: with `used` pages in use, the k-th page in use behind the first `used` ids moves to
-// the k-th free id among them.  A second kernel follows the moved ids through the block table.
+// the k-th free id among them.  A second kernel follows the ids through the block table.
 __global__ void __launch_bounds__(kPlanThreads)
-compact_plan_kernel(const __grid_constant__ PageTable p, int32_t *moves, int32_t *num_moves, int32_t *used_out,
-                    int32_t *to) {
+compact_plan_kernel(const __grid_constant__ PageTable p, int32_t *moves, int32_t *num_moves, int32_t *to) {
     dependent_start();
     __shared__ ScanScratch scan;
     const int tid = threadIdx.x;
@@ -327,7 +326,9 @@ compact_plan_kernel(const __grid_constant__ PageTable p, int32_t *moves, int32_t
         holes += sum;
         int m = movers + block_exclusive(__popc(mover), &scan, &sum);
         movers += sum;
-        for (unsigned dead = ~live & there & ~front; dead; dead &= dead - 1) to[v1 + __ffs(dead) - 1] = -1;
+#pragma unroll
+        for (int k = 0; k < kSearch; ++k)  // where a page is afterwards, -1: nobody holds it (a mover's place follows)
+            if (there >> k & 1) to[v1 + k] = live >> k & 1 ? v1 + k : -1;
         for (; hole; hole &= hole - 1) moves[2 * h++ + 1] = v1 + __ffs(hole) - 1;
         for (; mover; mover &= mover - 1) moves[2 * m++] = v1 + __ffs(mover) - 1;
     }
@@ -338,25 +339,20 @@ compact_plan_kernel(const __grid_constant__ PageTable p, int32_t *moves, int32_t
         p.refs[s] = 0;
         to[s] = d;
     }
-    if (tid == 0) {
-        *num_moves = movers;
-        *used_out = used;
-    }
+    if (tid == 0) *num_moves = movers;
 }
 
 constexpr int kFollowThreads = 256;
 __global__ void __launch_bounds__(kFollowThreads)
-compact_follow_kernel(const __grid_constant__ PageTable p, const int32_t *used_in,
-                      const int32_t *to) {
+compact_follow_kernel(const __grid_constant__ PageTable p, const int32_t *to) {
     dependent_start();
-    const int used = *used_in;
     const size_t n = (size_t)p.num_seqs * p.max_blocks;
     for (size_t i = (size_t)blockIdx.x * kFollowThreads + threadIdx.x; i < n; i += (size_t)gridDim.x * kFollowThreads) {
         const int v = p.bt[i];
-        if (v < used) continue;
+        if (v < 0) continue;
         const int d = v < p.num_blocks ? to[v] : -1;
         if (d < 0) record_error(p.err, kErrBadBlock);  // a page that nobody holds: the entry stays
-        else p.bt[i] = d;
+        else if (d != v) p.bt[i] = d;
     }
 }
 
@@ -424,7 +420,7 @@ struct PagesWs {
     int32_t *a, *b, *c, *d, *e;
     size_t bytes;
 };
-// fork: lens [n], rows [n][max_blocks].  grow: owner, count, last, want, free.  compact: used, to.
+// fork: lens [n], rows [n][max_blocks].  grow: owner, count, last, want, free.  compact: to (in b).
 PagesWs pages_ws(const PageTable &p, int n, void *base) {
     char *w = reinterpret_cast<char *>(base);
     size_t at = 0;
@@ -469,12 +465,12 @@ cudaError_t launch_pages_trim(const PageTable &p, int n, const int32_t *seqs, co
 
 cudaError_t launch_pages_compact(const PageTable &p, int32_t *moves, int32_t *num_moves, void *ws, cudaStream_t st) {
     const PagesWs s = pages_ws(p, 0, ws);
-    const cudaError_t e = launch_dependent(compact_plan_kernel, dim3(1), kPlanThreads, 0, st, p, moves, num_moves, s.a, s.b);
+    const cudaError_t e = launch_dependent(compact_plan_kernel, dim3(1), kPlanThreads, 0, st, p, moves, num_moves, s.b);
     if (e != cudaSuccess) return e;
     const size_t n = (size_t)p.num_seqs * p.max_blocks, blocks = (n + kFollowThreads - 1) / kFollowThreads;
     const int most = 4 * sm_count();
     return launch_dependent(compact_follow_kernel, dim3(blocks < (size_t)most ? (int)blocks : most), kFollowThreads, 0, st,
-                            p, s.a, s.b);
+                            p, s.b);
 }
 
 cudaError_t launch_copy_pages(const mla_dims_t &d, int num_pools, const mla_pool_t *pools, int num_blocks,

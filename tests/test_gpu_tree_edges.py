@@ -311,3 +311,22 @@ def test_an_infinite_row_and_queries_of_both_signs(kv, flags, ctx, drafted):
     assert right[:, minus].all()
     assert ((lse[:n0].double() - rl).abs() <= lb)[:, minus].all()
     assert torch.isfinite(o[n0:]).all() and torch.isfinite(lse[n0:]).all()
+
+
+# ---- pages ----------------------------------------------------------------------------------------------
+
+def test_compact_reports_an_entry_of_a_page_that_nobody_holds_wherever_it_lies():
+    """Also among the lowest ids, where a page in use moves to it; entries of pages in use follow."""
+    from mla_latent_kv_mqa_b200 import native as N, pages as P
+    seqs = P.PagedSequences(4, 4, 3, 12)
+    seqs.grow(dev([8, 8, 8, 0]))                                     # pages 0,1 / 2,3 / 4,5
+    seqs.trim(dev([0]), dev([0]))
+    seqs.block_table[3, 1] = 1
+    moves, number = seqs.compact()
+    assert N.mla_get_last_device_error() == N.MLA_ERR_BAD_BLOCK_TABLE
+    assert moves[:int(number)].tolist() == [[4, 0], [5, 1]]
+    assert seqs.block_table.tolist() == [[-1] * 3, [2, 3, -1], [0, 1, -1], [-1, 1, -1]]
+    assert seqs.refs.tolist() == [1] * 4 + [0] * 8
+    seqs.block_table[3, 1] = -1
+    moves, number = seqs.compact()
+    assert int(number) == 0 and N.mla_get_last_device_error() == N.MLA_OK
