@@ -510,7 +510,10 @@ mla_status_t mla_pages_fork(const mla_page_table_t *table, int n, const int32_t 
  * taken, and its last page, where that is part-filled and held by others too, is replaced by a page of
  * its own, whose content moves[k] = (from, to) asks mla_cache_copy_pages for.  Of the sequences of one
  * call that share such a page the last keeps it if nobody else holds it.  An entry with new_lens[i] <=
- * its length is left as it is.  Entries beyond the length that already hold a page keep it.
+ * its length is left as it is.  Entries beyond the length that already hold a page keep it if the page is the
+ * sequence's alone (where a length was lowered with pages left behind it and another sequence holds one of those too,
+ * mla_pages_trim comes first); otherwise the entry is bad (MLA_ERR_BAD_BLOCK_TABLE), as is one whose part-filled page
+ * nobody holds.
  *   moves      [n, 2] int32, num_moves [1] int32 on the device, written
  * All or nothing: a bad entry, or too few free pages (MLA_ERR_OUT_OF_PAGES), leaves the table as it
  * was, with num_moves 0. */

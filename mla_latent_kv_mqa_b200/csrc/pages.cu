@@ -160,7 +160,7 @@ grow_kernel(const __grid_constant__ PageTable p, int n, const int32_t *seqs,
         if (cur < 0 || len < 0 || pages_of(len, p.page) > p.max_blocks) err_code = kErrBadSeqLen;
         else if (len > cur && cur % p.page) {
             const int v = *entry(s, cur / p.page);
-            if (v < 0 || v >= p.num_blocks) err_code = kErrBadBlock;
+            if (v < 0 || v >= p.num_blocks || p.refs[v] < 1) err_code = kErrBadBlock;
             else {
                 ws.count[v] = 0;
                 ws.last[v] = -1;
@@ -195,13 +195,18 @@ grow_kernel(const __grid_constant__ PageTable p, int n, const int32_t *seqs,
         }
         const int lo = pages_of(cur, p.page), hi = len > cur ? pages_of(len, p.page) : lo;
         const bool few = hi - lo <= kFewPages;
+        auto wants = [&](int at, int k) {  // a page; one that is there has to be the sequence's alone, its rows are written next
+            const int v = *entry(at, k);
+            if (v >= 0 && (v >= p.num_blocks || p.refs[v] != 1)) err_code = kErrBadBlock;
+            return (int)(v < 0);
+        };
         if (few)
-            for (int k = lo; k < hi; ++k) want += *entry(s, k) < 0;
+            for (int k = lo; k < hi; ++k) want += wants(s, k);
         for (unsigned many = __ballot_sync(0xffffffffu, !few); many; many &= many - 1) {
             const int who = __ffs(many) - 1;
             const int ws_ = __shfl_sync(0xffffffffu, s, who), wlo = __shfl_sync(0xffffffffu, lo, who), whi = __shfl_sync(0xffffffffu, hi, who);
             int w = 0;
-            for (int k = wlo + lane; k < whi; k += 32) w += *entry(ws_, k) < 0;
+            for (int k = wlo + lane; k < whi; k += 32) w += wants(ws_, k);
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
             if (lane == who) want = w;
@@ -215,6 +220,13 @@ grow_kernel(const __grid_constant__ PageTable p, int n, const int32_t *seqs,
         }
     }
     __syncthreads();
+    if (err_code) {
+        if (tid == 0) {
+            record_error(p.err, (unsigned)err_code);
+            *num_moves = 0;
+        }
+        return;
+    }
     int total = 0, copies = 0;
     for (int i0 = 0; i0 < n; i0 += kPlanThreads) {  // the entries' first pages and first copies
         const int i = i0 + tid, w = i < n ? ws.want[i] : 0;

@@ -330,3 +330,36 @@ def test_compact_reports_an_entry_of_a_page_that_nobody_holds_wherever_it_lies()
     seqs.block_table[3, 1] = -1
     moves, number = seqs.compact()
     assert int(number) == 0 and N.mla_get_last_device_error() == N.MLA_OK
+
+
+@pytest.mark.parametrize("width", [4, 60])                           # few pages, and many a sequence
+def test_grow_refuses_to_write_a_reserved_page_that_another_sequence_holds(width):
+    from mla_latent_kv_mqa_b200 import native as N, pages as P
+    seqs = P.PagedSequences(4, 3, width, 200)
+    seqs.grow(dev([4 * width, 3, 0]))
+    seqs.fork(dev([0]), dev([2]))
+    seqs.seq_lens[2] = 6                                             # cut without a trim: its pages behind are shared
+    before = [x.clone() for x in (seqs.block_table, seqs.refs, seqs.seq_lens)]
+    for new in (4 * width, 9):
+        _, number = seqs.grow(dev([new, 5]), dev([2, 1]))
+        assert int(number) == 0 and N.mla_get_last_device_error() == N.MLA_ERR_BAD_BLOCK_TABLE
+        assert all(torch.equal(x, y) for x, y in zip(before, (seqs.block_table, seqs.refs, seqs.seq_lens)))
+    seqs.trim(seqs.seq_lens.clone())
+    moves, number = seqs.grow(dev([4 * width, 5]), dev([2, 1]))
+    assert N.mla_get_last_device_error() == N.MLA_OK and int(number) == 1
+    assert (seqs.refs[seqs.block_table[seqs.block_table >= 0].long()] >= 1).all()
+    held = torch.bincount(seqs.block_table[seqs.block_table >= 0].long(), minlength=200)
+    assert torch.equal(held.int(), seqs.refs)
+    shared = set(seqs.block_table[0].tolist()) & set(seqs.block_table[2].tolist())
+    assert shared - {-1} == {int(before[0][0, 0])}                   # the full page alone
+    # its own pages behind a lowered length stay
+    seqs.seq_lens[0] = 5
+    seqs.trim(dev([0]), dev([2]))
+    row = seqs.block_table[0].clone()
+    seqs.grow(dev([4 * width]))
+    assert torch.equal(seqs.block_table[0], row) and N.mla_get_last_device_error() == N.MLA_OK
+    # an entry that names a page nobody holds
+    seqs.seq_lens[1] = 6
+    seqs.refs[seqs.block_table[1, 1].long()] = 0
+    seqs.grow(dev([7]), dev([1]))
+    assert N.mla_get_last_device_error() == N.MLA_ERR_BAD_BLOCK_TABLE
