@@ -76,11 +76,7 @@ class PagedLatentCache:
 
     def pool(self) -> N.mla_pool_t:
         """The buffers as mla_cache_keep and mla_cache_copy_pages take them."""
-        known = self.__dict__.get("_pool")
-        if known is None or known[0] is not self.kv_pool or known[1] is not self.kr_pool or known[2] is not self.kv_scale:
-            known = self._pool = (self.kv_pool, self.kr_pool, self.kv_scale,
-                                  N.make_pool(self.kv_pool, self.kr_pool, self.kv_scale))
-        return known[3]
+        return N.make_pool(self.kv_pool, self.kr_pool, self.kv_scale)
 
     @property
     def nbytes(self) -> int:

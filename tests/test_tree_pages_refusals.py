@@ -95,6 +95,18 @@ def test_keep_lists_and_caches(M):
         trees.keep([], table, lens, torch.zeros(1, 1, dtype=torch.int32), i32(1))
 
 
+def test_a_pool_is_where_its_tensors_are_now(M):
+    """A buffer whose storage is swapped in place is taken at its new address by every call."""
+    dims = M.L.dims_for(2, 8, 16, 4, kv="fp8", page=4)
+    cache = M.L.PagedLatentCache(dims, 3, device="cpu")
+    assert (cache.pool().kv_pool, cache.pool().kv_scale) == (cache.kv_pool.data_ptr(), cache.kv_scale.data_ptr())
+    other = [torch.empty_like(x) for x in (cache.kv_pool, cache.kr_pool, cache.kv_scale)]
+    for x, y in zip((cache.kv_pool, cache.kr_pool, cache.kv_scale), other):
+        x.set_(y)
+    p = cache.pool()
+    assert (p.kv_pool, p.kr_pool, p.kv_scale) == tuple(x.data_ptr() for x in other)
+
+
 def test_cache_buffers_are_on_one_device(M):
     dims = M.L.dims_for(2, 8, 16, 4, kv="fp8", page=4)
     kv, kr, s = torch.zeros(3, 4, 16, dtype=torch.uint8), torch.zeros(3, 4, 4, dtype=torch.bfloat16), torch.zeros(3, 4)
