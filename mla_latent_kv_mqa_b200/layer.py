@@ -93,6 +93,7 @@ class PagedLatentCache:
 _INT32 = torch.int32
 _on_device = getattr(torch._C, "_cuda_getDevice", None)
 _is_capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", None)
+_current_handle = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _MISREAD = ("tensors are contiguous and on the current CUDA device; lengths, tables and indices are int32")
 
 
@@ -100,18 +101,9 @@ def _stream_object(handle: int):
     return torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
 
 
-def _capturing(handle: int, stream) -> bool:
-    if stream is None:
-        return _is_capturing()
-    with torch.cuda.stream(_stream_object(handle)):
-        return _is_capturing()
-
-
 def new_on(stream, make):
-    """make()'s tensors, for a call on ``stream``.  On another stream than the current one they are taken from that
+    """make()'s tensors, for a call that names its ``stream``.  On another one than the current they are taken from that
     stream's memory (what held it before has run there) and given back once both streams are past them."""
-    if stream is None:
-        return make()
     here, handle = N._stream(None), N._stream(stream)
     if here == handle:
         return make()
@@ -147,7 +139,7 @@ class Workspace:
     def __init__(self, device):
         self.device = device
         self.lock = threading.Lock()
-        self._sizes, self._by_stream = {}, {}
+        self._by_stream, self._known = {}, {}
 
     _shared: dict = {}
 
@@ -160,23 +152,31 @@ class Workspace:
         return cls._shared.setdefault(device, cls(device))
 
     def _new(self, need, stream):
-        return new_on(stream, lambda: (torch.empty(need, dtype=torch.uint8, device=self.device),))[0]
+        make = lambda: (torch.empty(need, dtype=torch.uint8, device=self.device),)
+        return (make() if stream is None else new_on(stream, make))[0]
 
-    def get(self, key, stream, size):
-        """A buffer of at least ``size()`` bytes, which depends on ``key`` alone."""
-        need = self._sizes.get(key)
-        if need is None:
-            if len(self._sizes) > 1024:  # lengths that change every step
-                self._sizes.clear()
-            need = self._sizes[key] = max(256, size())
-        handle = N._stream(stream)
-        if _capturing(handle, stream):
+    def get(self, key, handle, stream, size, *args):
+        """A buffer of at least ``size(*args)`` bytes, which depend on ``key`` alone, for a call on ``stream`` (its handle)."""
+        if stream is None:
+            capturing = _is_capturing()
+        else:
+            with torch.cuda.stream(_stream_object(handle)):
+                capturing = _is_capturing()
+        known = None if capturing else self._known.get((key, handle))
+        if known is not None:
+            return known
+        need = max(256, size(*args))
+        if capturing:
             return self._new(need, stream)
         buf = self._by_stream.get(handle)
         if buf is None or buf.numel() < need:
             if buf is not None:
                 need = max(need, 2 * buf.numel())
+                self._known.clear()
             buf = self._by_stream[handle] = self._new(need, stream)
+        if len(self._known) > 1024:  # lengths that change every step
+            self._known.clear()
+        self._known[key, handle] = buf
         return buf
 
 
@@ -294,11 +294,12 @@ class MLADecodeLayer:
         if not fits(d, cache.dims):
             raise ValueError("tree_append: the cache's rows are not the layer's")
         if (here < 0 or here != _on_device() or k_r.get_device() != here or block_table.get_device() != here or
-                trees.slot.get_device() != here or cache.kv_pool.get_device() != here or block_table.dtype is not _INT32 or
+                trees._slot.get_device() != here or cache.kv_pool.get_device() != here or block_table.dtype is not _INT32 or
                 not (c_kv.is_contiguous() and k_r.is_contiguous() and block_table.is_contiguous())):
             raise ValueError(_MISREAD)
-        N.mla_tree_append(d, T, c_kv, k_r, trees.seq_idx, trees.slot, trees.pos, block_table, B,
-                          max_blocks, cache.num_blocks, cache.kv_pool, cache.kr_pool, cache.kv_scale, stream)
+        N.mla_tree_append(d, T, c_kv, k_r, trees._seq_idx, trees._slot, trees._pos, block_table, B, max_blocks,
+                          cache.num_blocks, cache.kv_pool, cache.kr_pool, cache.kv_scale,
+                          _current_handle(here) if stream is None else stream)
 
     def decode_tree(self, cache: PagedLatentCache, q_abs, block_table, seq_lens, trees, max_seq_len,
                     out_dtype="f32", o_lat=None, lse=None, stream=None, workspace=None):
@@ -317,29 +318,37 @@ class MLADecodeLayer:
             raise ValueError("decode_tree: the cache's rows are not the layer's")
         here = q_abs.get_device()
         if (here < 0 or here != _on_device() or block_table.get_device() != here or seq_lens.get_device() != here or
-                trees.cu_nodes.get_device() != here or cache.kv_pool.get_device() != here or
+                trees._cu_nodes.get_device() != here or cache.kv_pool.get_device() != here or
                 block_table.dtype is not _INT32 or seq_lens.dtype is not _INT32 or
                 not (q_abs.is_contiguous() and block_table.is_contiguous() and seq_lens.is_contiguous())):
             raise ValueError(_MISREAD)
         if o_lat is None:
-            o_lat, = new_on(stream, lambda: (q_abs.new_empty((T, d.n_h, d.d_c), dtype=TORCH_ACT[dt]),))
+            shape = (T, d.n_h, d.d_c)
+            if stream is None:
+                o_lat = q_abs.new_empty(shape, dtype=TORCH_ACT[dt])
+            else:
+                o_lat, = new_on(stream, lambda: (q_abs.new_empty(shape, dtype=TORCH_ACT[dt]),))
         elif (o_lat.dtype != TORCH_ACT[dt] or o_lat.shape != (T, d.n_h, d.d_c) or not o_lat.is_contiguous() or
               o_lat.get_device() != here):
             raise ValueError("decode_tree: o_lat is contiguous [nodes, n_h, d_c] of out_dtype, where q_abs is")
         if lse is None:
-            lse, = new_on(stream, lambda: (q_abs.new_empty((T, d.n_h), dtype=torch.float32),))
+            if stream is None:
+                lse = q_abs.new_empty((T, d.n_h), dtype=torch.float32)
+            else:
+                lse, = new_on(stream, lambda: (q_abs.new_empty((T, d.n_h), dtype=torch.float32),))
         elif lse.dtype != torch.float32 or lse.shape != (T, d.n_h) or not lse.is_contiguous() or lse.get_device() != here:
             raise ValueError("decode_tree: lse is contiguous [nodes, n_h] fp32, where q_abs is")
         if workspace is not None and (workspace.dtype != torch.uint8 or not workspace.is_contiguous() or
                                       workspace.get_device() != here):
             raise ValueError("decode_tree: workspace is contiguous uint8, where q_abs is")
-        with self._tree_ws.lock:
+        handle, shared = _current_handle(here) if stream is None else N._stream(stream), self._tree_ws
+        with shared.lock:
             if workspace is None:
-                workspace = self._tree_ws.get((self._tree_key, B, T, max_seq_len), stream,
-                                              lambda: N.mla_decode_tree_workspace_size(d, B, T, max_seq_len))
-            N.mla_decode_tree(d, B, trees.cu_nodes, T, trees.max_nodes, q_abs, cache.kv_pool, cache.kr_pool,
+                workspace = shared.get((self._tree_key, B, T, max_seq_len), handle, stream,
+                                       N.mla_decode_tree_workspace_size, d, B, T, max_seq_len)
+            N.mla_decode_tree(d, B, trees._cu_nodes, T, trees.max_nodes, q_abs, cache.kv_pool, cache.kr_pool,
                               cache.kv_scale, block_table, max_blocks, cache.num_blocks, seq_lens, max_seq_len,
-                              trees.mask, trees.mask_words, workspace, workspace.numel(), o_lat, dt, lse, stream)
+                              trees._mask, trees.mask_words, workspace, workspace.numel(), o_lat, dt, lse, handle)
         return o_lat, lse
 
     def out_proj(self, o_lat, out_dtype="f32", out=None, stream=None):

@@ -17,17 +17,20 @@ from __future__ import annotations
 import torch
 
 from . import native as N
-from .layer import _INT32, _MISREAD, Workspace, _on_device, _stream_object, new_on, same_caches
+from .layer import _INT32, _MISREAD, Workspace, _current_handle, _on_device, _stream_object, new_on, same_caches
 
 
 class PageMoves:
     """Page copies to make, on the device: ``pairs`` [most, 2] of (from, to) and their ``number`` [1].  One buffer
     holds both, of the stream that writes them; unpacks as (pairs, number)."""
 
-    def __init__(self, most: int, device, stream=None):
+    def __init__(self, most: int, device, stream=None, handle=None):
         self.most = most
-        self._buf, = new_on(stream, lambda: (torch.empty((most + 1, 2), dtype=torch.int32, device=device),))
-        self._stream = N._stream(stream) if self._buf.is_cuda else None
+        if stream is None:
+            self._buf = torch.empty((most + 1, 2), dtype=torch.int32, device=device)
+        else:
+            self._buf, = new_on(stream, lambda: (torch.empty((most + 1, 2), dtype=torch.int32, device=device),))
+        self._handle = handle  # of the stream that writes them
         self.pairs_ptr = self._buf.data_ptr()
         self.number_ptr = self.pairs_ptr + 8 * most
 
@@ -38,12 +41,6 @@ class PageMoves:
     @property
     def number(self) -> torch.Tensor:
         return self._buf[self.most, :1]
-
-    def used_on(self, stream):
-        """A call on ``stream`` reads the moves: their memory is not given back before it has."""
-        handle = N._stream(stream)
-        if handle != self._stream:
-            self._buf.record_stream(_stream_object(handle))
 
     def __iter__(self):
         return iter((self.pairs, self.number))
@@ -77,26 +74,28 @@ class PagedSequences:
     def seq_lens(self) -> torch.Tensor:
         return self._seq_lens
 
-    def _look_over(self, *indices):
+    def _look_over(self, stream, *indices):
+        """The handle of the call's stream, once its tensors are what the kernels read."""
         here = self._device
         if here < 0 or here != _on_device():
             raise ValueError(_MISREAD)
         for x in indices:
             if x is not None and (x.dtype is not _INT32 or x.get_device() != here or not x.is_contiguous()):
                 raise ValueError(_MISREAD)
+        return _current_handle(here) if stream is None else N._stream(stream)
 
-    def _workspace(self, n: int, stream):
-        return self._ws.get(n, stream, lambda: N.mla_pages_workspace_size(self._table, n))
+    def _workspace(self, n: int, handle, stream):
+        return self._ws.get(n, handle, stream, N.mla_pages_workspace_size, self._table, n)
 
     def fork(self, parent, child, stream=None):
         """Sequence child[i] becomes a copy of parent[i]; all parents are read before any child changes."""
         if parent.numel() != child.numel():
             raise ValueError("fork: a parent for every child")
-        self._look_over(parent, child)
+        handle = self._look_over(stream, parent, child)
         n = parent.numel()
         with self._ws.lock:
-            ws = self._workspace(n, stream)
-            N.mla_pages_fork(self._table, n, parent, child, ws, ws.numel(), stream)
+            ws = self._workspace(n, handle, stream)
+            N.mla_pages_fork(self._table, n, parent, child, ws, ws.numel(), handle)
 
     def grow(self, new_lens, seqs=None, stream=None):
         """Sequences ``seqs`` (default: 0, 1, ...) grow to ``new_lens`` tokens; returns the page copies to
@@ -104,28 +103,28 @@ class PagedSequences:
         n = new_lens.numel()
         if seqs is not None and seqs.numel() != n:
             raise ValueError("grow: a length for every sequence")
-        self._look_over(new_lens, seqs)
-        moves = PageMoves(n, self._block_table.device, stream)
+        handle = self._look_over(stream, new_lens, seqs)
+        moves = PageMoves(n, self._block_table.device, stream, handle)
         with self._ws.lock:
-            ws = self._workspace(n, stream)
-            N.mla_pages_grow(self._table, n, seqs, new_lens, moves.pairs_ptr, moves.number_ptr, ws, ws.numel(), stream)
+            ws = self._workspace(n, handle, stream)
+            N.mla_pages_grow(self._table, n, seqs, new_lens, moves.pairs_ptr, moves.number_ptr, ws, ws.numel(), handle)
         return moves
 
     def trim(self, new_lens, seqs=None, stream=None):
         """Sequences are cut to ``new_lens`` tokens (0: the sequence ends); their pages lose a holder."""
         if seqs is not None and seqs.numel() != new_lens.numel():
             raise ValueError("trim: a length for every sequence")
-        self._look_over(new_lens, seqs)
+        handle = self._look_over(stream, new_lens, seqs)
         with self._ws.lock:  # not between the kernels of another call
-            N.mla_pages_trim(self._table, new_lens.numel(), seqs, new_lens, stream)
+            N.mla_pages_trim(self._table, new_lens.numel(), seqs, new_lens, handle)
 
     def compact(self, stream=None):
         """The pages in use take the lowest ids; returns the page copies to make (PageMoves), for copy_pages."""
-        self._look_over()
-        moves = PageMoves(self.num_blocks // 2, self._block_table.device, stream)
+        handle = self._look_over(stream)
+        moves = PageMoves(self.num_blocks // 2, self._block_table.device, stream, handle)
         with self._ws.lock:
-            ws = self._workspace(0, stream)
-            N.mla_pages_compact(self._table, moves.pairs_ptr, moves.number_ptr, ws, ws.numel(), stream)
+            ws = self._workspace(0, handle, stream)
+            N.mla_pages_compact(self._table, moves.pairs_ptr, moves.number_ptr, ws, ws.numel(), handle)
         return moves
 
     def copy_pages(self, caches, moves, stream=None):
@@ -135,17 +134,19 @@ class PagedSequences:
         dims = same_caches(caches, self.num_blocks)
         if dims.page_size != self._table.page_size:
             raise ValueError("copy_pages: the caches' pages are not the table's")
-        self._look_over()
-        if any(c.kv_pool.get_device() != self._device for c in caches):
-            raise ValueError(_MISREAD)
+        handle = self._look_over(stream)
+        for c in caches:
+            if c.kv_pool.get_device() != self._device:
+                raise ValueError(_MISREAD)
         pools = N.make_pools([c.pool() for c in caches])
         if isinstance(moves, PageMoves):
             pairs, number, most = moves.pairs_ptr, moves.number_ptr, moves.most
-            moves.used_on(stream)
+            if handle != moves._handle:  # their memory is not given back before this stream has read them
+                moves._buf.record_stream(_stream_object(handle))
         else:
             pairs, number = moves
-            self._look_over(pairs, number)
+            self._look_over(stream, pairs, number)
             if pairs.dim() != 2 or pairs.shape[1] != 2 or (number is not None and number.numel() < 1):
                 raise ValueError("copy_pages: moves are pairs [n, 2] and their number [1], or None for all")
             most = pairs.shape[0]
-        N.mla_cache_copy_pages(dims, pools, self.num_blocks, pairs, number, most, stream)
+        N.mla_cache_copy_pages(dims, pools, self.num_blocks, pairs, number, most, handle)

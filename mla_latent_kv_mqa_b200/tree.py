@@ -18,7 +18,7 @@ from __future__ import annotations
 import torch
 
 from . import native as N
-from .layer import _INT32, _MISREAD, _on_device, new_on, same_caches
+from .layer import _INT32, _MISREAD, _current_handle, _on_device, new_on, same_caches
 
 
 class DraftTrees:
@@ -79,11 +79,11 @@ class DraftTrees:
         if seq_lens.numel() != self.B:
             raise ValueError("prepare: seq_lens has an entry per tree")
         here = seq_lens.get_device()
-        if (here < 0 or here != _on_device() or self.cu_nodes.get_device() != here or seq_lens.dtype is not _INT32 or
+        if (here < 0 or here != _on_device() or self._cu_nodes.get_device() != here or seq_lens.dtype is not _INT32 or
                 not seq_lens.is_contiguous()):
             raise ValueError(_MISREAD)
-        N.mla_tree_prepare(self.B, self.cu_nodes, self.total_nodes, self.parent, seq_lens, self.mask_words, self.mask,
-                           self.pos, self.slot, self.seq_idx, stream)
+        N.mla_tree_prepare(self.B, self._cu_nodes, self.total_nodes, self._parent, seq_lens, self.mask_words, self._mask,
+                           self._pos, self._slot, self._seq_idx, _current_handle(here) if stream is None else stream)
 
     def keep(self, caches, block_table, seq_lens, keep, num_keep, new_lens=None, stream=None):
         """The rows of the accepted nodes ``keep`` [B, max_keep] (each row's first num_keep[b],
@@ -94,17 +94,21 @@ class DraftTrees:
         if not caches:
             raise ValueError("keep: no caches")
         here = seq_lens.get_device()
-        if (here < 0 or here != _on_device() or self.cu_nodes.get_device() != here or block_table.get_device() != here or
+        if (here < 0 or here != _on_device() or self._cu_nodes.get_device() != here or block_table.get_device() != here or
                 keep.get_device() != here or num_keep.get_device() != here or any(c.kv_pool.get_device() != here for c in caches) or
                 block_table.dtype is not _INT32 or seq_lens.dtype is not _INT32 or keep.dtype is not _INT32 or
                 num_keep.dtype is not _INT32 or
                 not (block_table.is_contiguous() and seq_lens.is_contiguous() and keep.is_contiguous() and num_keep.is_contiguous())):
             raise ValueError(_MISREAD)
         if new_lens is None:
-            new_lens, = new_on(stream, lambda: (torch.empty_like(seq_lens),))
+            if stream is None:
+                new_lens = torch.empty_like(seq_lens)
+            else:
+                new_lens, = new_on(stream, lambda: (torch.empty_like(seq_lens),))
         elif new_lens.dtype is not _INT32 or new_lens.numel() != B or new_lens.get_device() != here or not new_lens.is_contiguous():
             raise ValueError(_MISREAD)
         dims, pools = same_caches(caches, caches[0].num_blocks), N.make_pools([c.pool() for c in caches])
-        N.mla_cache_keep(dims, pools, B, self.cu_nodes, self.total_nodes, block_table, max_blocks,
-                         caches[0].num_blocks, seq_lens, keep, num_keep, keep.shape[1], new_lens, stream)
+        N.mla_cache_keep(dims, pools, B, self._cu_nodes, self.total_nodes, block_table, max_blocks,
+                         caches[0].num_blocks, seq_lens, keep, num_keep, keep.shape[1], new_lens,
+                         _current_handle(here) if stream is None else stream)
         return new_lens

@@ -146,12 +146,13 @@ def test_grow_on_another_stream_and_its_copies():
 @pytest.mark.parametrize("flags", [0, 1])
 def test_outputs_and_workspaces_of_another_stream(flags, raw):
     """Memory that pending work of the current stream still writes is not handed to a call on another stream."""
+    from mla_latent_kv_mqa_b200 import layer as L
     b = Batch([900, 300, 31], [6, 4, 9], heads=32, seed=65, flags=flags)
     want, want_lse = b.decode()
     keep, num = dev([[0], [0], [0]]), dev([1, 1, 1])
     s = torch.cuda.Stream()
     stream = s.cuda_stream if raw else s
-    b.layer._tree_ws._by_stream.clear()
+    b.layer._tree_ws = L.Workspace(b.layer.device)
     torch.cuda.synchronize()
     torch.cuda.empty_cache()
     mem = [torch.empty_like(want), torch.empty_like(want_lse), torch.empty(1 << 26, dtype=torch.uint8, device="cuda"), torch.empty_like(b.lens)]
