@@ -95,7 +95,6 @@ constexpr int LOAD_K_WARP = 0, LOAD_V_WARP = 1, QK_WARP = 2, PV_WARP = 3, SM_WAR
 constexpr int SM_WARPS = 8, SM_THREADS = 32 * SM_WARPS, CLEAN_THREADS = 128;
 constexpr uint32_t S_COL = 0, O_COL = 256, TMEM_COLS = 512;
 constexpr float RESCALE_LOG2 = 8.0f;
-constexpr int TURN_STEPS = 64;                    // steps of the sequences whose tiles may be turned (launch_tree_tc)
 constexpr int BAR_MAX = 1, BAR_CLEAN = 2;
 
 struct __align__(16) Ctrl {
@@ -1301,9 +1300,16 @@ cudaError_t launch_tree_tc(const mla_dims_t &d, const TreeArgs &a, void *ws, cud
     cfg.stream = st;
     cfg.attrs = &pdl;
     cfg.numAttrs = 1;
-    // Few tiles of long sequences, each over several pairs (4 x 131072 tokens, four tiles each): turned 481 us, as they
-    // come 540.  Many tiles have nothing to share, and the turns' instructions cost them 3% (24 ragged sequences 440 -> 455 us).
-    const bool turn = 2 * tree_tiles(a.B, (int64_t)q_rows) <= pairs && a.max_seq_len >= TURN_STEPS * STEP;
+    // Turned where few tiles are each spread over several pairs, a sequence has two tiles or more to share what L2 holds
+    // (their mean: the host knows no more), and it may be long.  Measured, turned against as they come (us, 74 pairs):
+    //   bf16, 128 heads   8 x 32768, 2 tiles 156-180 / 176-189   4 x 65536, 4 tiles 270-282 / 318-330   4 x 131072 556 / 650
+    //                     4 x 16384, 4 tiles 119-137 / 116-126   8 x 32768, 1 tile   98 / 92
+    //   FP8               4 x 65536, 4 tiles 303-311 / 316-319   4 x 131072 602-608 / 641-648
+    //                     4 x 32768, 4 tiles 169 / 165-167       8 x 32768, 2 tiles 171 / 169-171       8 x 32768, 1 tile 103 / 100
+    // Many tiles have nothing to share, and the turns' instructions cost them 3% (24 ragged sequences).  max_seq_len is the
+    // caller's bound: short sequences under a long one are turned for nothing (4 x 2000 under 131072: bf16 46 / 49, FP8 45 / 44).
+    const bool turn = 2 * tree_tiles(a.B, (int64_t)q_rows) <= pairs && q_rows >= (uint64_t)a.B * 2 * TILE &&
+                      a.max_seq_len >= (f8 ? 65536 : 32768);
     auto kern = f8 ? turn ? tree_tc_kernel<true, true> : tree_tc_kernel<true, false>
                    : turn ? tree_tc_kernel<false, true> : tree_tc_kernel<false, false>;
     cudaError_t e = cudaLaunchKernelEx(&cfg, kern, tm_q, tm_k, tm_v, tm_c, a, pl);

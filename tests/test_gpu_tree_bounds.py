@@ -46,6 +46,16 @@ def test_each_kernel_rounds_what_it_says(kv, act, shape, flags, ctx, n, heads, o
     check(b, b.decode(out), out)
 
 
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+@pytest.mark.parametrize("ctx,n,heads", [([70000, 66001], [4, 3], 128), ([70000, 300, 33000], [4, 1, 9], 64), ([40000] * 3, [1, 1, 1], 128),
+                                         ([66000, 5], [40, 2], 16)])
+def test_long_sequences_with_tiles_that_share_them_and_without(kv, ctx, n, heads):
+    b = Batch(ctx, n, heads=heads, kv=kv, seed=95)
+    first = b.decode()
+    check(b, first, sample=2)
+    assert all(torch.equal(x, y) for x, y in zip(first, b.decode()))
+
+
 @pytest.mark.parametrize("ctx", [3, 300, 5000])
 @pytest.mark.parametrize("power", [-70, -90, -100, -140, 50, 100])
 @pytest.mark.parametrize("flags", [0, 1])
