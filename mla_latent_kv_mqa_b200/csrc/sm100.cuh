@@ -293,15 +293,7 @@ __device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols
 // D (+)= A * B^T over both CTAs' shared memory at the same offsets: M = 128 as 64 rows of A from each
 // CTA, N as one half of B's rows from each.  A CTA's D: its 64 rows in lanes 0-63 (columns 0 .. N/2 - 1
 // of D) and again in lanes 64-127 (columns N/2 .. N - 1).
-__device__ __forceinline__ void mma_ss_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                            uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-// With the descriptors' words apart; `hi` is both descriptors' high word.
+// The descriptors' words come apart; `hi` is both descriptors' high word.
 __device__ __forceinline__ void mma_ss_pair(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t idesc,
                                             bool accumulate) {
     asm volatile(
@@ -383,13 +375,6 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32
         "%30, %31, %32};" ::"r"(taddr),
         MLA_W8(0), MLA_W8(8), MLA_W8(16), MLA_W8(24)
         : "memory");
-}
-// 8 consecutive 32-bit TMEM columns of this thread's lane.
-__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&v)[8]) {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                 : MLA_R8(0)
-                 : "r"(taddr)
-                 : "memory");
 }
 // 16 consecutive 32-bit TMEM columns of this thread's lane.
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
