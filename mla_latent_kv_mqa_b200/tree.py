@@ -26,7 +26,8 @@ class DraftTrees:
     int32 on the device, and ``max_nodes``, a host-side bound of a sequence's nodes.
 
     ``mask`` [total_nodes, mask_words], ``pos``, ``slot`` and ``seq_idx`` [total_nodes] are written by
-    prepare(); a caller with masks of its own hands ``mask`` over instead (int32 words)."""
+    prepare(); a caller with masks of its own hands ``mask`` over (int32 words) and writes it after prepare(), which
+    fills it with the ancestors."""
 
     def __init__(self, cu_nodes: torch.Tensor, parent: torch.Tensor, max_nodes: int, mask: torch.Tensor | None = None):
         if not 1 <= max_nodes <= N.MLA_MAX_TREE_NODES:
@@ -48,7 +49,8 @@ class DraftTrees:
             raise ValueError("mask must be contiguous int32 [total_nodes, >= ceil(max_nodes / 32)]")
         dev = cu_nodes.device
         self._mask = torch.empty((self.total_nodes, self.mask_words), dtype=torch.int32, device=dev) if mask is None else mask
-        self._pos, self._slot, self._seq_idx = (torch.empty(self.total_nodes, dtype=torch.int32, device=dev) for _ in range(3))
+        self._pos, self._slot = (torch.empty(self.total_nodes, dtype=torch.int32, device=dev) for _ in range(2))
+        self._seq_idx = torch.full((self.total_nodes,), -1, dtype=torch.int32, device=dev)  # an append before prepare() goes nowhere
 
     # Looked over once, above: written in place (copy_), not replaced.
     @property

@@ -177,6 +177,23 @@ def test_outputs_and_workspaces_of_another_stream(flags, raw):
 def test_the_widest_rows(kv, act, shape):
     b = Batch([129, 33], [5, 3], kv=kv, act=act, shape=shape, page=16, heads=3, seed=7)
     b.check(b.decode())
+    b = Batch([3000, 700], [5, 3], kv=kv, act=act, shape=shape, page=16, heads=3, seed=8)   # a cluster of them joins
+    b.check(b.decode())
+
+
+# ---- rows before they have places ---------------------------------------------------------------------------
+
+def test_an_append_before_prepare_goes_nowhere():
+    from mla_latent_kv_mqa_b200 import native as N, tree as T
+    b = Batch([100, 30], [6, 4], heads=2)
+    junk = [torch.full((10,), 1, dtype=torch.int32, device="cuda") for _ in range(32)]
+    del junk                                                         # memory that new tensors find
+    trees = T.DraftTrees(b.trees.cu_nodes, b.trees.parent, 6)
+    before = b.cache.kv_pool.clone()
+    b.layer.tree_append(b.cache, torch.ones(10, 512, device="cuda").bfloat16(), torch.ones(10, 64, device="cuda").bfloat16(), trees, b.table)
+    torch.cuda.synchronize()
+    assert torch.equal(before.view(torch.int16), b.cache.kv_pool.view(torch.int16))
+    assert N.mla_get_last_device_error() == N.MLA_OK
 
 
 # ---- workspaces -----------------------------------------------------------------------------------------
