@@ -457,6 +457,7 @@ typedef struct {
  *   num_keep    [B] int32, in [0, min(max_keep, n_b)]
  *   new_lens    [B] int32, written: ctx_b + num_keep[b] (may be NULL; not seq_lens itself, which the
  *               layers' blocks read while it is written)
+ * B = 0 or num_pools = 0 is a no-op: nothing is written, new_lens neither.
  * A sequence whose kept nodes are not as stated (MLA_ERR_BAD_TREE), or whose length or pages are bad,
  * is left as it is, its new length seq_lens[b].  Pages of the drafted rows are the sequence's own
  * (mla_pages_grow sees to that): a page that two sequences of the call share is not written in order. */
@@ -501,7 +502,8 @@ size_t mla_pages_workspace_size(const mla_page_table_t *table, int n);
 /* mla_pages_fork -- sequence child[i] becomes a copy of parent[i] as it was before the call: its table
  * row, whose pages gain a holder, and its length.  What child[i] held before is given back.  A sequence
  * may be parent of many and child of one, of itself too (a beam search's reordering).  A bad entry is
- * skipped; where one child is named twice, both entries are. */
+ * skipped; where one child is named twice, both entries are.  A page of the parent's that is none of the pool's
+ * sets MLA_ERR_BAD_BLOCK_TABLE, and the child's entry is -1. */
 mla_status_t mla_pages_fork(const mla_page_table_t *table, int n, const int32_t *parent,
                             const int32_t *child, void *workspace, size_t workspace_bytes,
                             mla_stream_t stream);

@@ -7,8 +7,9 @@
 // atomics, whose order does not show, and pages are taken in the order of their ids.
 //
 // Measured (one B200, warm, whole calls): forking and growing beams with 447 MB of copies 82 us, compacting
-// with 1.08 GB moved 195 us: 5.4 TB/s, 0.83 of a plain copy's rate, with ~10 us of deciding ahead of the
-// copies; with little to copy the host's calls take most of the time (38 us for fork, grow, copies and trim).
+// with 1.08 GB moved 197 us: 5.4 TB/s, 0.83 of a plain copy's rate, with ~10 us of deciding ahead of the
+// copies; with little to copy the host's calls take most of the time (39-43 us for fork, grow and copies, or trim,
+// compact and copies, with the three copies that fill the tables before them).
 #include "mla_internal.cuh"
 #include "tree.cuh"
 

@@ -24,7 +24,7 @@
 //
 // FP8.  K's codes are operands as they are, at twice the rate, against two e4m3 parts of each query, which
 // together are the bf16 query (split_query): no K passes through registers, and S takes as long as in bf16.
-// (K's codes converted to bf16 tiles by four more warps took 593 us where this takes 420, with 96 registers a
+// (K's codes converted to bf16 tiles by four more warps took 593 us where this took 420, with 96 registers a
 // thread for the softmax, which spilled.)  V would need P in parts too, and a part's range is too small for a
 // long context's weights: the cleaning warps turn V's codes into fp16 tiles, exactly, by two instructions for
 // four codes (bf16 takes eight), and P is fp16.  Its 11 bits reach from 2^15 down to 2^-14, so m is chosen to
@@ -45,11 +45,12 @@
 // equal runs; a tile that lies in several runs leaves partial (O, m, l), at most two a pair, which a
 // second kernel joins.  Where few tiles are spread over many pairs, a tile's steps are turned (tile_turn).
 //
-// Measured (one B200, warm): 24 sequences of 1024-8190 tokens, 3-24 nodes, 128 heads 431 us = 1080 TFLOP/s;
-// 16 of 6000-8192, 64 nodes 1.8 ms = 1130; 4 of 131072, 4 nodes 481 us = 1210; FP8, 32 of 4097-8192, 2-12 nodes
-// 420 us = 950.  (GPUs that power holds lower: 13% more.)  A step takes ~6600 clocks over bf16, of which the
-// MMAs run 4352.  L2 hands the SMs 5.1 GB a call, 11.5 TB/s where loads alone reach 12.4 (557 KB a step and pair:
-// 128 rows a pair use a byte, and O leaves no tensor memory for more rows), and shared memory is busy ~5500 clocks.
+// Measured (B200, warm; ten calls after a pause, and in a loop of seconds, which power slows): 24 sequences of
+// 1024-8190 tokens, 3-24 nodes, 128 heads 449 us = 1040 TFLOP/s, 505-535 in the loop; 16 of 6000-8192, 64 nodes
+// 1.83 ms = 1110, 1.99-2.15; 4 of 131072, 4 nodes 490 us = 1190, 555-577; FP8, 32 of 4097-8192, 2-12 nodes 436 us = 920,
+// 471-492.  A step takes ~6800 clocks over bf16, of which the MMAs run 4352.  L2 hands the SMs 5.1 GB a call of the
+// first, 11.5 TB/s where loads alone reach 12.5 (557 KB a step and pair: 128 rows a pair use a byte, and O leaves no
+// tensor memory for more rows).
 //
 // Every wait is bounded (2 s).  On give-up both CTAs' abort flags are set, MLA_ERR_DEVICE_TIMEOUT is
 // recorded, and both CTAs stay until copies and MMAs in flight have had time to land.  What the join acts on
