@@ -14,6 +14,7 @@ A decode step of one layer (itwiki "ë©€í‹° í—¤ë“œ ìž ìž¬ ì–´í…ì…˜", sections ë¶
 from __future__ import annotations
 
 import threading
+import weakref
 
 import torch
 
@@ -33,6 +34,8 @@ class PagedLatentCache:
     bf16 / f32: ``kv_pool`` [num_blocks, page, d_c + d_r] rows [c_kv ; RoPE(k_r)].
     fp8: ``kv_pool`` [num_blocks, page, d_c] e4m3 codes, ``kr_pool`` [num_blocks, page, d_r]
     bf16, ``kv_scale`` [num_blocks, page] fp32.  ``poison`` fills every slot with NaN first."""
+
+    _pool = None  # pool()'s last answer, with the addresses it is for
 
     def __init__(self, dims: N.mla_dims_t, num_blocks: int, device="cuda", poison: bool = False):
         self.dims = dims
@@ -76,7 +79,12 @@ class PagedLatentCache:
 
     def pool(self) -> N.mla_pool_t:
         """The buffers as mla_cache_keep and mla_cache_copy_pages take them."""
-        return N.make_pool(self.kv_pool, self.kr_pool, self.kv_scale)
+        kr, scale = self.kr_pool, self.kv_scale
+        at = self.kv_pool.data_ptr(), None if kr is None else kr.data_ptr(), None if scale is None else scale.data_ptr()
+        known = self._pool
+        if known is None or known[0] != at:
+            known = self._pool = at, N.mla_pool_t(*at)
+        return known[1]
 
     @property
     def nbytes(self) -> int:
@@ -98,7 +106,7 @@ _MISREAD = ("tensors are contiguous and on the current CUDA device; lengths, tab
 
 
 def _stream_object(handle: int):
-    return torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
+    return torch.cuda.ExternalStream(handle) if handle > 1 else torch.cuda.default_stream()  # 0, 1: the legacy stream
 
 
 def new_on(stream, make):
@@ -141,11 +149,12 @@ class Workspace:
         self.lock = threading.Lock()
         self._by_stream, self._known = {}, {}
 
-    _shared: dict = {}
+    _shared = weakref.WeakValueDictionary()
 
     @classmethod
     def shared(cls, device) -> "Workspace":
-        """The device's one: layers' calls on a stream run one after the other and can share its buffer."""
+        """The device's one, while a layer is there: layers' calls on a stream run one after the other and can share its
+        buffer."""
         device = torch.device(device)
         if device.type == "cuda" and device.index is None:
             device = torch.device("cuda", torch.cuda.current_device())
@@ -289,7 +298,8 @@ class MLADecodeLayer:
         T, here = trees.total_nodes, c_kv.get_device()
         d = self.dims
         act = TORCH_ACT[d.act_dtype]
-        if c_kv.shape != (T, d.d_c) or k_r.shape != (T, d.d_r) or c_kv.dtype is not act or k_r.dtype is not act or B != trees.B:
+        if (c_kv.size(0) != T or k_r.size(0) != T or c_kv.numel() != T * d.d_c or k_r.numel() != T * d.d_r or
+                c_kv.dtype is not act or k_r.dtype is not act or B != trees.B):
             raise ValueError("tree_append: c_kv [nodes, d_c] and k_r [nodes, d_r] of the layer's type, block_table a row per tree")
         if not fits(d, cache.dims):
             raise ValueError("tree_append: the cache's rows are not the layer's")
@@ -304,15 +314,15 @@ class MLADecodeLayer:
     def decode_tree(self, cache: PagedLatentCache, q_abs, block_table, seq_lens, trees, max_seq_len,
                     out_dtype="f32", o_lat=None, lse=None, stream=None, workspace=None):
         """Every drafted node over the committed tokens and the nodes its mask names; returns
-        (o_lat [nodes, n_h, d_c], lse [nodes, n_h]).  Without ``workspace`` (uint8 tensor) the stream's is used, which
+        (o_lat [nodes, n_h, d_c], lse [nodes, n_h]).  Without ``workspace`` (a tensor's bytes) the stream's is used, which
         the layers of a device share, or one of the graph that is being captured; calls that may run at the same
         time take no ``workspace`` in common."""
         d = self.dims
         B, max_blocks = block_table.shape
         T = trees.total_nodes
         dt = DTYPE[out_dtype]
-        if (q_abs.shape != (T, d.n_h, d.d_c + d.d_r) or q_abs.dtype is not TORCH_ACT[d.act_dtype] or B != trees.B or
-                seq_lens.numel() != B):
+        if (q_abs.size(0) != T or q_abs.numel() != T * d.n_h * (d.d_c + d.d_r) or q_abs.dtype is not TORCH_ACT[d.act_dtype] or
+                B != trees.B or seq_lens.numel() != B):
             raise ValueError("decode_tree: q_abs is [nodes, n_h, d_c + d_r] of the layer's type, block_table and seq_lens have a row per tree")
         if not fits(d, cache.dims):
             raise ValueError("decode_tree: the cache's rows are not the layer's")
@@ -338,9 +348,8 @@ class MLADecodeLayer:
                 lse, = new_on(stream, lambda: (q_abs.new_empty((T, d.n_h), dtype=torch.float32),))
         elif lse.dtype != torch.float32 or lse.shape != (T, d.n_h) or not lse.is_contiguous() or lse.get_device() != here:
             raise ValueError("decode_tree: lse is contiguous [nodes, n_h] fp32, where q_abs is")
-        if workspace is not None and (workspace.dtype != torch.uint8 or not workspace.is_contiguous() or
-                                      workspace.get_device() != here):
-            raise ValueError("decode_tree: workspace is contiguous uint8, where q_abs is")
+        if workspace is not None and (not workspace.is_contiguous() or workspace.get_device() != here):
+            raise ValueError("decode_tree: workspace is contiguous, where q_abs is")
         handle, shared = _current_handle(here) if stream is None else N._stream(stream), self._tree_ws
         with shared.lock:
             if workspace is None:
@@ -348,7 +357,7 @@ class MLADecodeLayer:
                                        N.mla_decode_tree_workspace_size, d, B, T, max_seq_len)
             N.mla_decode_tree(d, B, trees._cu_nodes, T, trees.max_nodes, q_abs, cache.kv_pool, cache.kr_pool,
                               cache.kv_scale, block_table, max_blocks, cache.num_blocks, seq_lens, max_seq_len,
-                              trees._mask, trees.mask_words, workspace, workspace.numel(), o_lat, dt, lse, handle)
+                              trees._mask, trees.mask_words, workspace, workspace.nbytes, o_lat, dt, lse, handle)
         return o_lat, lse
 
     def out_proj(self, o_lat, out_dtype="f32", out=None, stream=None):

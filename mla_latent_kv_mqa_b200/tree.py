@@ -21,6 +21,16 @@ from . import native as N
 from .layer import _INT32, _MISREAD, _current_handle, _on_device, new_on, same_caches
 
 
+def _checked(name: str) -> property:
+    """A tensor that is replaced only by one of its shape, type and device (or written in place)."""
+    def put(self, x):
+        old = getattr(self, name)
+        if x.shape != old.shape or x.dtype != old.dtype or x.device != old.device or not x.is_contiguous():
+            raise ValueError(f"{name[1:]} must be contiguous {old.dtype} {tuple(old.shape)} on {old.device}")
+        setattr(self, name, x)
+    return property(lambda self: getattr(self, name), put)
+
+
 class DraftTrees:
     """The drafted nodes of B sequences, packed: ``cu_nodes`` [B + 1] and ``parent`` [total_nodes],
     int32 on the device, and ``max_nodes``, a host-side bound of a sequence's nodes.
@@ -52,30 +62,9 @@ class DraftTrees:
         self._pos, self._slot = (torch.empty(self.total_nodes, dtype=torch.int32, device=dev) for _ in range(2))
         self._seq_idx = torch.full((self.total_nodes,), -1, dtype=torch.int32, device=dev)  # an append before prepare() goes nowhere
 
-    # Looked over once, above: written in place (copy_), not replaced.
-    @property
-    def cu_nodes(self) -> torch.Tensor:
-        return self._cu_nodes
-
-    @property
-    def parent(self) -> torch.Tensor:
-        return self._parent
-
-    @property
-    def mask(self) -> torch.Tensor:
-        return self._mask
-
-    @property
-    def pos(self) -> torch.Tensor:
-        return self._pos
-
-    @property
-    def slot(self) -> torch.Tensor:
-        return self._slot
-
-    @property
-    def seq_idx(self) -> torch.Tensor:
-        return self._seq_idx
+    # Looked over once, when they come, not in every call.
+    cu_nodes, parent, mask = _checked("_cu_nodes"), _checked("_parent"), _checked("_mask")
+    pos, slot, seq_idx = _checked("_pos"), _checked("_slot"), _checked("_seq_idx")
 
     def prepare(self, seq_lens, stream=None):
         if seq_lens.numel() != self.B:
@@ -97,11 +86,14 @@ class DraftTrees:
             raise ValueError("keep: no caches")
         here = seq_lens.get_device()
         if (here < 0 or here != _on_device() or self._cu_nodes.get_device() != here or block_table.get_device() != here or
-                keep.get_device() != here or num_keep.get_device() != here or any(c.kv_pool.get_device() != here for c in caches) or
+                keep.get_device() != here or num_keep.get_device() != here or
                 block_table.dtype is not _INT32 or seq_lens.dtype is not _INT32 or keep.dtype is not _INT32 or
                 num_keep.dtype is not _INT32 or
                 not (block_table.is_contiguous() and seq_lens.is_contiguous() and keep.is_contiguous() and num_keep.is_contiguous())):
             raise ValueError(_MISREAD)
+        for c in caches:
+            if c.kv_pool.get_device() != here:
+                raise ValueError(_MISREAD)
         if new_lens is None:
             if stream is None:
                 new_lens = torch.empty_like(seq_lens)

@@ -62,9 +62,14 @@ def test_host_tensors_among_device_ones_are_refused():
         b.decode(o_lat=torch.zeros(10, 4, 512))
     with pytest.raises(ValueError):
         b.decode(lse=torch.zeros(10, 4))
-    for ws in (torch.zeros(1 << 26, dtype=torch.uint8), torch.zeros(1 << 24, device="cuda")):
+    for ws in (torch.zeros(1 << 26, dtype=torch.uint8), torch.zeros(1 << 27, dtype=torch.uint8, device="cuda")[::2]):
         with pytest.raises(ValueError):
             b.decode(workspace=ws)
+    want = b.decode()
+    got = b.decode(workspace=torch.empty(1 << 24, device="cuda"))
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    got = b.layer.decode_tree(b.cache, b.q.view(10, -1), b.table, b.lens, b.trees, b.max_len)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     keep, num = dev([[0], [0]]), dev([1, 1])
     other = L.PagedLatentCache(b.dims, b.cache.num_blocks, device="cpu")
     with pytest.raises(ValueError):

@@ -51,12 +51,13 @@ def test_decode_tree_queries_and_caches(M):
         with pytest.raises(ValueError, match=match):
             lay.decode_tree(**{**dict(cache=cache, q_abs=torch.zeros(2, 2, 20), block_table=table, seq_lens=lens, trees=trees,
                                       max_seq_len=8), **kw})
-    for q in (torch.zeros(2, 1, 20), torch.zeros(2, 2, 16), torch.zeros(2, 40), torch.zeros(2, 2, 20, dtype=torch.bfloat16),
+    for q in (torch.zeros(2, 1, 20), torch.zeros(2, 2, 16), torch.zeros(4, 20), torch.zeros(2, 2, 20, dtype=torch.bfloat16),
               torch.zeros(2, 2, 20, dtype=torch.float64)):
         call("q_abs is", q_abs=q)
     for c in other.values():
         call("cache's rows", cache=c)
-    call("contiguous and on the current", )                              # host tensors
+    call("contiguous and on the current")                                # host tensors
+    call("contiguous and on the current", q_abs=torch.zeros(2, 40))
 
 
 def test_tree_append_rows(M):
@@ -69,6 +70,8 @@ def test_tree_append_rows(M):
     wrong = M.L.PagedLatentCache(M.L.dims_for(2, 8, 16, 4, act="f32", kv="bf16", page=4), 3, device="cpu")
     with pytest.raises(ValueError, match="cache's rows"):
         lay.tree_append(wrong, torch.zeros(2, 16), torch.zeros(2, 4), trees, table)
+    with pytest.raises(ValueError, match="contiguous and on"):             # a head axis of one is a row all the same
+        lay.tree_append(cache, torch.zeros(2, 16), torch.zeros(2, 1, 4), trees, table)
 
 
 def test_trees_are_on_one_device_and_stay_as_looked_over(M):
@@ -81,8 +84,13 @@ def test_trees_are_on_one_device_and_stay_as_looked_over(M):
     trees = M.T.DraftTrees(cu, parent, 2, mask)
     assert trees.mask is mask
     for name in ("cu_nodes", "parent", "mask", "pos", "slot", "seq_idx"):
-        with pytest.raises(AttributeError):
-            setattr(trees, name, torch.zeros(1))
+        old = getattr(trees, name)
+        for bad in (torch.zeros(1, dtype=torch.int32), old.long(), old.to("meta"), old.repeat_interleave(2, 0)[::2]):
+            with pytest.raises(ValueError, match=name):
+                setattr(trees, name, bad)
+        new = old.clone()
+        setattr(trees, name, new)
+        assert getattr(trees, name) is new
 
 
 def test_keep_lists_and_caches(M):
