@@ -109,6 +109,16 @@ def _stream_object(handle: int):
     return torch.cuda.ExternalStream(handle) if handle > 1 else torch.cuda.default_stream()  # 0, 1: the legacy stream
 
 
+def used_on(stream, *tensors):
+    """A call on ``stream``, named by its caller, uses the tensors: their memory is not given back before it has."""
+    handle = N._stream(stream)
+    if handle != N._stream(None):
+        stream = _stream_object(handle)
+        for x in tensors:
+            if x is not None:
+                x.record_stream(stream)
+
+
 def new_on(stream, make):
     """make()'s tensors, for a call that names its ``stream``.  On another one than the current they are taken from that
     stream's memory (what held it before has run there) and given back once both streams are past them."""
@@ -307,6 +317,9 @@ class MLADecodeLayer:
                 trees._slot.get_device() != here or cache.kv_pool.get_device() != here or block_table.dtype is not _INT32 or
                 not (c_kv.is_contiguous() and k_r.is_contiguous() and block_table.is_contiguous())):
             raise ValueError(_MISREAD)
+        if stream is not None:
+            used_on(stream, c_kv, k_r, block_table, trees._seq_idx, trees._slot, trees._pos, cache.kv_pool, cache.kr_pool,
+                    cache.kv_scale)
         N.mla_tree_append(d, T, c_kv, k_r, trees._seq_idx, trees._slot, trees._pos, block_table, B, max_blocks,
                           cache.num_blocks, cache.kv_pool, cache.kr_pool, cache.kv_scale,
                           _current_handle(here) if stream is None else stream)
@@ -350,7 +363,13 @@ class MLADecodeLayer:
             raise ValueError("decode_tree: lse is contiguous [nodes, n_h] fp32, where q_abs is")
         if workspace is not None and (not workspace.is_contiguous() or workspace.get_device() != here):
             raise ValueError("decode_tree: workspace is contiguous, where q_abs is")
-        handle, shared = _current_handle(here) if stream is None else N._stream(stream), self._tree_ws
+        if stream is None:
+            handle = _current_handle(here)
+        else:
+            handle = N._stream(stream)
+            used_on(stream, q_abs, block_table, seq_lens, trees._cu_nodes, trees._mask, cache.kv_pool, cache.kr_pool, cache.kv_scale,
+                    o_lat, lse, workspace)
+        shared = self._tree_ws
         with shared.lock:
             if workspace is None:
                 workspace = shared.get((self._tree_key, B, T, max_seq_len), handle, stream,

@@ -9,15 +9,14 @@ hold each (include/mla.h, "Pages of the cache").
     seqs.copy_pages(caches, seqs.compact())      # pages in use to the front of the pool
 
 ``block_table``, ``refs`` and ``seq_lens`` are the tensors the other calls take.  One table serves the
-caches of all layers.  Calls take the current stream, or ``stream``: what a caller hands to a call on another
-stream than the current one, it keeps until that stream is past it.
+caches of all layers.  Calls take the current stream, or ``stream``.
 """
 from __future__ import annotations
 
 import torch
 
 from . import native as N
-from .layer import _INT32, _MISREAD, Workspace, _current_handle, _on_device, _stream_object, new_on, same_caches
+from .layer import _INT32, _MISREAD, Workspace, _current_handle, _on_device, _stream_object, new_on, same_caches, used_on
 
 
 class PageMoves:
@@ -82,7 +81,10 @@ class PagedSequences:
         for x in indices:
             if x is not None and (x.dtype is not _INT32 or x.get_device() != here or not x.is_contiguous()):
                 raise ValueError(_MISREAD)
-        return _current_handle(here) if stream is None else N._stream(stream)
+        if stream is None:
+            return _current_handle(here)
+        used_on(stream, self._block_table, self._refs, self._seq_lens, *indices)
+        return N._stream(stream)
 
     def _workspace(self, n: int, handle, stream):
         return self._ws.get(n, handle, stream, N.mla_pages_workspace_size, self._table, n)
@@ -149,4 +151,6 @@ class PagedSequences:
             if pairs.dim() != 2 or pairs.shape[1] != 2 or (number is not None and number.numel() < 1):
                 raise ValueError("copy_pages: moves are pairs [n, 2] and their number [1], or None for all")
             most = pairs.shape[0]
+        if stream is not None:
+            used_on(stream, *(x for c in caches for x in (c.kv_pool, c.kr_pool, c.kv_scale)))
         N.mla_cache_copy_pages(dims, pools, self.num_blocks, pairs, number, most, handle)

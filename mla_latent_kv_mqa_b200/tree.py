@@ -18,7 +18,7 @@ from __future__ import annotations
 import torch
 
 from . import native as N
-from .layer import _INT32, _MISREAD, _current_handle, _on_device, new_on, same_caches
+from .layer import _INT32, _MISREAD, _current_handle, _on_device, new_on, same_caches, used_on
 
 
 def _checked(name: str) -> property:
@@ -73,6 +73,8 @@ class DraftTrees:
         if (here < 0 or here != _on_device() or self._cu_nodes.get_device() != here or seq_lens.dtype is not _INT32 or
                 not seq_lens.is_contiguous()):
             raise ValueError(_MISREAD)
+        if stream is not None:
+            used_on(stream, seq_lens, self._cu_nodes, self._parent, self._mask, self._pos, self._slot, self._seq_idx)
         N.mla_tree_prepare(self.B, self._cu_nodes, self.total_nodes, self._parent, seq_lens, self.mask_words, self._mask,
                            self._pos, self._slot, self._seq_idx, _current_handle(here) if stream is None else stream)
 
@@ -102,6 +104,9 @@ class DraftTrees:
         elif new_lens.dtype is not _INT32 or new_lens.numel() != B or new_lens.get_device() != here or not new_lens.is_contiguous():
             raise ValueError(_MISREAD)
         dims, pools = same_caches(caches, caches[0].num_blocks), N.make_pools([c.pool() for c in caches])
+        if stream is not None:
+            used_on(stream, block_table, seq_lens, keep, num_keep, new_lens, self._cu_nodes,
+                    *(x for c in caches for x in (c.kv_pool, c.kr_pool, c.kv_scale)))
         N.mla_cache_keep(dims, pools, B, self._cu_nodes, self.total_nodes, block_table, max_blocks,
                          caches[0].num_blocks, seq_lens, keep, num_keep, keep.shape[1], new_lens,
                          _current_handle(here) if stream is None else stream)

@@ -386,3 +386,38 @@ def test_grow_refuses_to_write_a_reserved_page_that_another_sequence_holds(width
     seqs.refs[seqs.block_table[1, 1].long()] = 0
     seqs.grow(dev([7]), dev([1]))
     assert N.mla_get_last_device_error() == N.MLA_ERR_BAD_BLOCK_TABLE
+
+
+def test_what_a_call_on_another_stream_uses_may_be_dropped():
+    """Lists, trees, queries and tables that nobody holds any more when the stream comes to them."""
+    from mla_latent_kv_mqa_b200 import layer as L, pages as P, tree as T
+    b = Batch([900, 300, 31], [6, 4, 9], heads=32, seed=67)
+    want, want_lse = (x.clone() for x in b.decode())
+    s = torch.cuda.Stream()
+    ones = lambda n: torch.full((n,), 1, dtype=torch.int32, device="cuda")
+    cu, parent, lens = b.trees.cu_nodes.clone(), b.trees.parent.clone(), b.lens.clone()
+    trees = T.DraftTrees(cu, parent, b.most)
+    q, table = b.q.clone(), b.table.clone()
+    seqs = P.PagedSequences(64, 3, 8, 40)
+    rows = torch.randn(19, 512, device="cuda").bfloat16(), torch.randn(19, 64, device="cuda").bfloat16()
+    other = L.PagedLatentCache(b.dims, b.cache.num_blocks)
+    held = L.PagedLatentCache(b.dims, b.cache.num_blocks)
+    for c in (other, held):
+        c.kv_pool.zero_()
+    b.trees.prepare(lens)
+    b.layer.tree_append(held, *rows, b.trees, table)
+    new_lens, seq = dev([100, 30, 200]), dev([0, 1, 2])
+    torch.cuda.synchronize()
+    _sleep(s)
+    trees.prepare(lens, stream=s)
+    o, lse = b.layer.decode_tree(b.cache, q, table, lens, trees, b.max_len, stream=s)
+    b.layer.tree_append(other, *rows, trees, table, stream=s)
+    seqs.grow(new_lens, seq, stream=s)
+    del cu, parent, lens, trees, q, table, rows, new_lens, seq
+    junk = [ones(n) for n in (3, 4, 19, 20, 2, 38) for _ in range(8)] + [torch.full_like(b.q, 9.0) for _ in range(2)]
+    junk += [torch.full_like(b.table, 0) for _ in range(4)] + [torch.full((19, k), 5.0, device="cuda").bfloat16() for k in (512, 64) for _ in range(2)]
+    torch.cuda.synchronize()
+    del junk
+    assert torch.equal(o, want) and torch.equal(lse, want_lse)
+    assert torch.equal(other.kv_pool, held.kv_pool)
+    assert seqs.seq_lens.tolist() == [100, 30, 200]
